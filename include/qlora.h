@@ -407,6 +407,170 @@ qlora_status qlora_loftq_init(const float *W0, const qlora_nf4 *wq, const float 
  * arguments. */
 size_t qlora_loftq_workspace_bytes(int64_t in, int64_t out, int32_t k);
 
+/*
+ * The two ends of an adapter's training step: the objectives that start its
+ * backward pass, and dropout whose mask is never stored.
+ *
+ * Notation: x one row of logits, y its label, s the inverse temperature,
+ *   m = max_v x_v,  z = log sum_v exp(s (x_v - m)),
+ *   log p_v = s (x_v - m) - z,  H = -sum_v p_v log p_v (0 log 0 = 0).
+ *
+ * In this section, other than above:
+ *   - Logits are [T, V] in rows of `ld` elements (V <= ld <= 2^32; the
+ *     gradient has its own ldd), 1 <= V <= 2^24, T <= 2^24.  Vectors over
+ *     tokens are dense fp32, of at most 2^30 tokens.
+ *   - Pointers need their element's alignment only (rows of an odd V start
+ *     anywhere; a packed batch can be entered at any token).
+ *   - A token whose label lies outside [0, V) (-100, say) is not scored: its
+ *     logits are not read, its logp, stats and entropy are 0 and its
+ *     gradient row is 0.
+ *   - A logit of -inf is a word that cannot occur (p = 0, gradient 0); a
+ *     row of nothing else has logp = -inf, H = 0 and a zero gradient row.  A
+ *     NaN or +inf makes its own row's results NaN.
+ *   - Arithmetic is fp32, the sums that give a loss fp64 across workgroups;
+ *     results are rounded to the output's type once.
+ */
+
+/*
+ * qlora_token_logp_fwd: logp[t] = log p_y of each row.
+ *   stats [T, 2]  fp32 (output): m and z, which the backward reads.
+ *   entropy [T]   fp32 (output) H, or NULL.
+ * scale > 0 is s.  ws: qlora_token_logp_workspace_bytes(T, V, dt) bytes (may
+ * be 0, ws then NULL).  T = 0 is a no-op.
+ */
+qlora_status qlora_token_logp_fwd(const void *logits, int64_t ld, int64_t T, int64_t V,
+                                  qlora_dtype dt, const int64_t *labels, float scale,
+                                  float *logp, float *stats, float *entropy, void *ws,
+                                  size_t ws_bytes, hipStream_t stream);
+size_t qlora_token_logp_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt);
+
+/*
+ * qlora_token_logp_bwd: the logits' gradient from that of logp and of H,
+ *   dx_v = s (g (1[v = y] - p_v) - gH p_v (log p_v + H)).
+ *   g [T]; entropy and g_entropy [T] both, or both NULL (no entropy term).
+ *   dlogits [T, V] dt, rows of ldd elements; may be `logits` itself with
+ *   ldd = ld (the gradient then replaces the logits).
+ */
+qlora_status qlora_token_logp_bwd(const void *logits, int64_t ld, int64_t T, int64_t V,
+                                  qlora_dtype dt, const int64_t *labels, float scale,
+                                  const float *stats, const float *entropy, const float *g,
+                                  const float *g_entropy, void *dlogits, int64_t ldd,
+                                  hipStream_t stream);
+
+/*
+ * qlora_pref_loss: loss of P pairs of answers (chosen, rejected) and its
+ * gradient, from the log-probabilities of their tokens.
+ *   logp, ref [T]: under the model and the frozen reference (NULL: none).
+ *   mask [T] uint8: a token counts where it is not 0 (prompt and padding are
+ *     0, whatever their logp holds); NULL: every token counts.
+ *   cu [2P + 1] int64: answer i is tokens cu[i] .. cu[i + 1] - 1 (not
+ *     decreasing; values outside [0, T] are taken as the nearer end); pair k
+ *     is answers k (chosen) and P + k (rejected).
+ * With S_i = sum (logp - ref) over the answer's counted tokens (divided by
+ * their number if `average`; 0 for an answer without any), h = S_k - S_(P+k):
+ *   SIGMOID  u = beta h - margin,
+ *            l = -(1 - smoothing) log sigma(u) - smoothing log sigma(-u)
+ *   SQUARED  l = (h - 1 / (2 beta))^2
+ *   HINGE    l = max(0, 1 - (beta h - margin))
+ *   loss [1] = mean l;  rewards [2P] = beta S_i;
+ *   dlogp [T] = dloss / dlogp (0 for tokens that do not count).
+ * 1 <= P <= 2^20; beta > 0, finite margin, 0 <= smoothing <= 0.5 (QLORA_ERR_VALUE).
+ */
+typedef enum {
+  QLORA_PREF_SIGMOID = 0,
+  QLORA_PREF_SQUARED = 1,
+  QLORA_PREF_HINGE = 2
+} qlora_pref_kind;
+
+typedef struct {
+  int32_t kind; /* qlora_pref_kind */
+  float beta;
+  float margin;
+  float smoothing;
+  int32_t average;
+} qlora_pref;
+
+qlora_status qlora_pref_loss(const float *logp, const float *ref, const uint8_t *mask,
+                             const int64_t *cu, int64_t P, int64_t T, const qlora_pref *pref,
+                             float *loss, float *rewards, float *dlogp, void *ws,
+                             size_t ws_bytes, hipStream_t stream);
+size_t qlora_pref_workspace_bytes(int64_t P, int64_t T);
+
+/*
+ * qlora_policy_loss: a policy objective over tokens and its gradient.
+ *   weight [T]: a token's share of the loss (for a mean over N live tokens,
+ *     1 / N; for a mean over answers of their means, 1 / (answers * length)).
+ *     0: the token is skipped, whatever its other inputs hold.  NULL: all 1.
+ *   adv [T] (NULL: all 1), old [T] logp when the answer was drawn (NULL: the
+ *     model's own, ratio 1), ref [T] the frozen reference's (NULL: no KL
+ *     term), entropy [T] (NULL: 0).
+ * With d = logp - old, r = exp(d), q = ref - logp, per token
+ *   NLL   f = adv logp, f' = adv (adv = NULL: cross-entropy)
+ *   CLIP  f = min(r adv, clamp(r, 1 - clip_lo, 1 + clip_hi) adv), for
+ *         adv < 0 and clip_dual > 0 at least clip_dual adv; f' = r adv, or 0
+ *         where a bound holds: adv > 0 and d > log(1 + clip_hi), adv < 0 and
+ *         d < log(1 - clip_lo) or d > log(clip_dual) (logs rounded to fp32)
+ *   k = exp(q) - q - 1 (non-negative, its mean under the policy is the KL),
+ *   loss  = sum weight (-f + kl_coef k - ent_coef entropy)
+ *   dlogp = weight (-f' + kl_coef (1 - exp(q))),
+ *   dentropy = -weight ent_coef (NULL: not wanted).
+ *   out [4]: loss, sum weight k, sum weight [a bound holds], sum weight
+ *   entropy.
+ * 0 <= clip_lo <= 1, clip_hi >= 0 (may be infinite), clip_dual = 0 or > 1,
+ * finite coefficients (QLORA_ERR_VALUE).  T = 0 gives out = 0.
+ */
+typedef enum { QLORA_OBJ_NLL = 0, QLORA_OBJ_CLIP = 1 } qlora_objective;
+
+typedef struct {
+  int32_t kind; /* qlora_objective */
+  float clip_lo;
+  float clip_hi;
+  float clip_dual;
+  float kl_coef;
+  float ent_coef;
+} qlora_policy;
+
+qlora_status qlora_policy_loss(const float *logp, const float *entropy, int64_t T,
+                               const float *weight, const float *adv, const float *old,
+                               const float *ref, const qlora_policy *policy, float *out,
+                               float *dlogp, float *dentropy, void *ws, size_t ws_bytes,
+                               hipStream_t stream);
+size_t qlora_policy_workspace_bytes(int64_t T);
+
+/*
+ * qlora_policy_logits: the same objective from the logits to the logits'
+ * gradient in one pass over the rows (logp and H from them as in
+ * qlora_token_logp_fwd, the gradient as in qlora_token_logp_bwd).  With NLL,
+ * adv = NULL and weight = 1 / N it is the cross-entropy of N tokens.
+ *   logp [T] (output, or NULL; 0 where a token is not scored or its weight is
+ *   0); dlogits as in qlora_token_logp_bwd, also in place.
+ */
+qlora_status qlora_policy_logits(const void *logits, int64_t ld, int64_t T, int64_t V,
+                                 qlora_dtype dt, const int64_t *labels, float scale,
+                                 const float *weight, const float *adv, const float *old,
+                                 const float *ref, const qlora_policy *policy, float *out,
+                                 float *logp, void *dlogits, int64_t ldd, void *ws,
+                                 size_t ws_bytes, hipStream_t stream);
+size_t qlora_policy_logits_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt);
+
+/*
+ * qlora_dropout: y = residual + keep * x / (1 - p) (residual NULL: none),
+ * [rows, cols] in dt, rows of ldx, ldr, ldy elements.  The mask is a function
+ * of (seed, counter, cols, row, column) alone, so the same call on the
+ * incoming gradient, without residual, is the backward pass, and nothing is
+ * stored: element (i, j) takes the 16-bit half j % 2 (low first) of word
+ * (j % 8) / 2 of the Philox4x32-10 block (Salmon et al., "Parallel random
+ * numbers: as easy as 1, 2, 3") whose key is `seed` and whose counter is
+ * (n, counter), n = i ceil(cols / 8) + j / 8, each 64 bits low word first.
+ * It is kept where that value is at least p16 = floor(65536 p + 0.5), capped
+ * at 65535; 1 - p stands for 1 - p16 / 65536, so the mean is kept exactly.
+ * A dropped x may hold anything.  y may be x or residual (same ld).
+ * 0 <= p < 1 (QLORA_ERR_VALUE); rows, cols <= 2^31 - 8, ld <= 2^32.
+ */
+qlora_status qlora_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                           int64_t rows, int64_t cols, qlora_dtype dt, float p, uint64_t seed,
+                           uint64_t counter, void *y, int64_t ldy, hipStream_t stream);
+
 /* Human-readable name of a status code (host-only, static string). */
 const char *qlora_status_string(qlora_status s);
 
@@ -442,7 +606,11 @@ typedef enum {
   QLORA_KERNEL_DA_PASS = 5,     /* dA = X^T.G (partials, or whole with dB) */
   QLORA_KERNEL_REDUCE = 6,      /* deterministic reduction of partials    */
   QLORA_KERNEL_FWD_SMALLM = 7,  /* small-M forward                        */
-  QLORA_KERNEL_COUNT = 8
+  QLORA_KERNEL_LOGP = 8,        /* token log-probabilities, both passes   */
+  QLORA_KERNEL_PREF = 9,        /* preference loss                        */
+  QLORA_KERNEL_POLICY = 10,     /* policy loss (tokens, logits)           */
+  QLORA_KERNEL_DROPOUT = 11,    /* dropout from the counter               */
+  QLORA_KERNEL_COUNT = 12
 } qlora_kernel_kind;
 
 int qlora_timing_enable(int kind_mask);

@@ -26,6 +26,10 @@ What it computes (plain, slow, obviously correct):
   the merged dense weight deq(Wq) + A.B; adapters initialised from the
   best rank-r approximation of the quantization residual W0 - deq(Q(W0)).
 * ``optim``   -- one Adam (AdamW) step of an adapter matrix, in float64.
+* ``objective`` -- token log-probabilities and entropy of logits with their
+  gradient, the preference losses, the clipped policy objective, and the
+  Philox4x32-10 mask of the dropout, from their published formulas (pinned by
+  ``tests/test_objective_oracle.py``).
 
 Parity status: every function here is pinned by ``tests/test_oracle_pins.py``
 against values the pages print or against closed forms; no function is

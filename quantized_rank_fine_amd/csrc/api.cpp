@@ -342,6 +342,41 @@ qlora_status linear_bwd(const qlora_nf4 *wq, const void *X, const void *dY, int6
 #undef QLORA_RUN
 }
 
+// The objectives and dropout (token vectors, strided rows, element alignment).
+constexpr int64_t kMaxVocab = int64_t(1) << 24;
+constexpr int64_t kMaxLd = int64_t(1) << 32;
+constexpr int64_t kMaxVec = int64_t(1) << 30;
+constexpr int64_t kMaxPairs = int64_t(1) << 20;
+
+bool aligned_to(const void *p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool aligned_el(const void *p, qlora_dtype dt) { return aligned_to(p, dt == QLORA_BF16 ? 2 : 4); }
+
+qlora_status check_logits(int64_t ld, int64_t T, int64_t V, qlora_dtype dt, float scale) {
+  if (!tokens_ok(T) || V < 1 || V > kMaxVocab || ld < V || ld > kMaxLd) return QLORA_ERR_SHAPE;
+  if (!dtype_ok(dt)) return QLORA_ERR_DTYPE;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return QLORA_ERR_VALUE;
+  return QLORA_OK;
+}
+
+qlora_status policy_params(const qlora_policy *q, PolicyParams &p) {
+  if (!q) return QLORA_ERR_NULL;
+  const bool ok = (q->kind == QLORA_OBJ_NLL || q->kind == QLORA_OBJ_CLIP) &&
+                  q->clip_lo >= 0.0f && q->clip_lo <= 1.0f && q->clip_hi >= 0.0f &&
+                  (q->clip_dual == 0.0f || (q->clip_dual > 1.0f && std::isfinite(q->clip_dual))) &&
+                  std::isfinite(q->kl_coef) && std::isfinite(q->ent_coef);
+  if (!ok) return QLORA_ERR_VALUE;
+  p.clip = q->kind == QLORA_OBJ_CLIP;
+  p.lo = float(1.0 - double(q->clip_lo));
+  p.hi = float(1.0 + double(q->clip_hi));
+  p.dual = q->clip_dual;
+  p.log_lo = float(std::log1p(-double(q->clip_lo)));
+  p.log_hi = float(std::log1p(double(q->clip_hi)));
+  p.log_dual = q->clip_dual > 0.0f ? float(std::log(double(q->clip_dual))) : INFINITY;
+  p.kl = q->kl_coef;
+  p.ent = q->ent_coef;
+  return QLORA_OK;
+}
+
 bool adam_hparams_ok(const qlora_adam_hparams *h) {
   return h && h->step >= 1 && std::isfinite(h->lr) && std::isfinite(h->eps) &&
          std::isfinite(h->weight_decay) && h->beta1 >= 0.0f && h->beta1 < 1.0f &&
@@ -626,6 +661,166 @@ qlora_status qlora_adam_step(float *theta, const float *grad, float *m, float *v
                          theta_bf16, stream));
 }
 
+size_t qlora_token_logp_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt) {
+  (void)T; (void)V; (void)dt;
+  return 0;
+}
+
+qlora_status qlora_token_logp_fwd(const void *logits, int64_t ld, int64_t T, int64_t V,
+                                  qlora_dtype dt, const int64_t *labels, float scale,
+                                  float *logp, float *stats, float *entropy, void *ws,
+                                  size_t ws_bytes, hipStream_t stream) {
+  (void)ws; (void)ws_bytes;
+  qlora_status st = check_logits(ld, T, V, dt, scale);
+  if (st != QLORA_OK || T == 0) return st;
+  if (!logits || !labels || !logp || !stats) return QLORA_ERR_NULL;
+  if (!aligned_el(logits, dt) || !aligned_to(labels, 8) || !aligned_to(logp, 4) ||
+      !aligned_to(stats, 4) || !aligned_to(entropy, 4))
+    return QLORA_ERR_ALIGN;
+  const LogitRows a{logits, ld, T, V, dt == QLORA_BF16, labels, scale};
+  return dev(timed(QLORA_KERNEL_LOGP, stream,
+                   [&] { return launch_logp_fwd(a, logp, stats, entropy, stream); }));
+}
+
+qlora_status qlora_token_logp_bwd(const void *logits, int64_t ld, int64_t T, int64_t V,
+                                  qlora_dtype dt, const int64_t *labels, float scale,
+                                  const float *stats, const float *entropy, const float *g,
+                                  const float *g_entropy, void *dlogits, int64_t ldd,
+                                  hipStream_t stream) {
+  qlora_status st = check_logits(ld, T, V, dt, scale);
+  if (st != QLORA_OK) return st;
+  if (ldd < V || ldd > kMaxLd) return QLORA_ERR_SHAPE;
+  if (T == 0) return QLORA_OK;
+  if (!logits || !labels || !stats || !g || !dlogits || !entropy != !g_entropy)
+    return QLORA_ERR_NULL;
+  if (!aligned_el(logits, dt) || !aligned_el(dlogits, dt) || !aligned_to(labels, 8) ||
+      !aligned_to(stats, 4) || !aligned_to(entropy, 4) || !aligned_to(g, 4) ||
+      !aligned_to(g_entropy, 4))
+    return QLORA_ERR_ALIGN;
+  const LogitRows a{logits, ld, T, V, dt == QLORA_BF16, labels, scale};
+  return dev(timed(QLORA_KERNEL_LOGP, stream, [&] {
+    return launch_logp_bwd(a, stats, entropy, g, g_entropy, dlogits, ldd, stream);
+  }));
+}
+
+size_t qlora_pref_workspace_bytes(int64_t P, int64_t T) {
+  if (P < 1 || P > kMaxPairs || T < 0 || T > kMaxVec) return 0;
+  return size_t(2 * P) * size_t(pref_splits(P, T)) * 2 * sizeof(double);
+}
+
+qlora_status qlora_pref_loss(const float *logp, const float *ref, const uint8_t *mask,
+                             const int64_t *cu, int64_t P, int64_t T, const qlora_pref *pref,
+                             float *loss, float *rewards, float *dlogp, void *ws,
+                             size_t ws_bytes, hipStream_t stream) {
+  if (P < 1 || P > kMaxPairs || T < 0 || T > kMaxVec) return QLORA_ERR_SHAPE;
+  if (!pref) return QLORA_ERR_NULL;
+  if (pref->kind < QLORA_PREF_SIGMOID || pref->kind > QLORA_PREF_HINGE) return QLORA_ERR_VALUE;
+  if (!(pref->beta > 0.0f) || !std::isfinite(pref->beta) || !std::isfinite(pref->margin) ||
+      !(pref->smoothing >= 0.0f && pref->smoothing <= 0.5f))
+    return QLORA_ERR_VALUE;
+  if (!cu || !loss || !rewards || (T > 0 && (!logp || !dlogp))) return QLORA_ERR_NULL;
+  if (!aligned_to(logp, 4) || !aligned_to(ref, 4) || !aligned_to(cu, 8) ||
+      !aligned_to(loss, 4) || !aligned_to(rewards, 4) || !aligned_to(dlogp, 4))
+    return QLORA_ERR_ALIGN;
+  const size_t need = qlora_pref_workspace_bytes(P, T);
+  if (need && !ws) return QLORA_ERR_NULL;
+  if (!aligned_to(ws, 8)) return QLORA_ERR_ALIGN;
+  if (ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  const PrefParams p{pref->kind, pref->beta, pref->margin, pref->smoothing, pref->average};
+  return dev(timed(QLORA_KERNEL_PREF, stream, [&] {
+    return launch_pref(logp, ref, mask, cu, P, T, p, loss, rewards, dlogp,
+                       static_cast<double *>(ws), stream);
+  }));
+}
+
+size_t qlora_policy_workspace_bytes(int64_t T) {
+  if (T < 0 || T > kMaxVec) return 0;
+  const int64_t n = policy_blocks(T);
+  return n > 1 ? size_t(n) * 4 * sizeof(double) : 0;
+}
+
+qlora_status qlora_policy_loss(const float *logp, const float *entropy, int64_t T,
+                               const float *weight, const float *adv, const float *old,
+                               const float *ref, const qlora_policy *policy, float *out,
+                               float *dlogp, float *dentropy, void *ws, size_t ws_bytes,
+                               hipStream_t stream) {
+  if (T < 0 || T > kMaxVec) return QLORA_ERR_SHAPE;
+  PolicyParams p;
+  qlora_status st = policy_params(policy, p);
+  if (st != QLORA_OK) return st;
+  if (!out || (T > 0 && (!logp || !dlogp))) return QLORA_ERR_NULL;
+  for (const float *v : {logp, entropy, weight, adv, old, ref, static_cast<const float *>(out),
+                         static_cast<const float *>(dlogp), static_cast<const float *>(dentropy)})
+    if (!aligned_to(v, 4)) return QLORA_ERR_ALIGN;
+  const size_t need = qlora_policy_workspace_bytes(T);
+  if (need && !ws) return QLORA_ERR_NULL;
+  if (!aligned_to(ws, 8)) return QLORA_ERR_ALIGN;
+  if (ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  return dev(timed(QLORA_KERNEL_POLICY, stream, [&] {
+    return launch_policy(logp, entropy, T, PolicyTokens{weight, adv, old, ref}, p, out, dlogp,
+                         dentropy, static_cast<double *>(ws), stream);
+  }));
+}
+
+size_t qlora_policy_logits_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt) {
+  if (check_logits(V, T, V, dt, 1.0f) != QLORA_OK) return 0;
+  return size_t(T) * 4 * sizeof(float);
+}
+
+qlora_status qlora_policy_logits(const void *logits, int64_t ld, int64_t T, int64_t V,
+                                 qlora_dtype dt, const int64_t *labels, float scale,
+                                 const float *weight, const float *adv, const float *old,
+                                 const float *ref, const qlora_policy *policy, float *out,
+                                 float *logp, void *dlogits, int64_t ldd, void *ws,
+                                 size_t ws_bytes, hipStream_t stream) {
+  qlora_status st = check_logits(ld, T, V, dt, scale);
+  if (st != QLORA_OK) return st;
+  if (ldd < V || ldd > kMaxLd) return QLORA_ERR_SHAPE;
+  PolicyParams p;
+  st = policy_params(policy, p);
+  if (st != QLORA_OK) return st;
+  if (!out || (T > 0 && (!logits || !labels || !dlogits || !ws))) return QLORA_ERR_NULL;
+  if (!aligned_el(logits, dt) || !aligned_el(dlogits, dt) || !aligned_to(labels, 8) ||
+      !aligned_to(ws, 16))
+    return QLORA_ERR_ALIGN;
+  for (const float *v : {weight, adv, old, ref, static_cast<const float *>(out),
+                         static_cast<const float *>(logp)})
+    if (!aligned_to(v, 4)) return QLORA_ERR_ALIGN;
+  if (ws_bytes < qlora_policy_logits_workspace_bytes(T, V, dt)) return QLORA_ERR_WORKSPACE;
+  float *terms = static_cast<float *>(ws);
+  if (T > 0) {
+    const LogitRows a{logits, ld, T, V, dt == QLORA_BF16, labels, scale};
+    const hipError_t e = timed(QLORA_KERNEL_POLICY, stream, [&] {
+      return launch_policy_logits(a, PolicyTokens{weight, adv, old, ref}, p, terms, logp,
+                                  dlogits, ldd, stream);
+    });
+    if (e != hipSuccess) return QLORA_ERR_DEVICE;
+  }
+  return dev(timed(QLORA_KERNEL_POLICY, stream,
+                   [&] { return launch_sum4(terms, T, out, stream); }));
+}
+
+qlora_status qlora_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                           int64_t rows, int64_t cols, qlora_dtype dt, float p, uint64_t seed,
+                           uint64_t counter, void *y, int64_t ldy, hipStream_t stream) {
+  constexpr int64_t most = (int64_t(1) << 31) - 8;
+  if (rows < 0 || cols < 0 || rows > most || cols > most) return QLORA_ERR_SHAPE;
+  if (ldx < cols || ldy < cols || (residual && ldr < cols) || ldx > kMaxLd || ldy > kMaxLd ||
+      (residual && ldr > kMaxLd))
+    return QLORA_ERR_SHAPE;
+  if (!dtype_ok(dt)) return QLORA_ERR_DTYPE;
+  if (!(p >= 0.0f && p < 1.0f)) return QLORA_ERR_VALUE;
+  if (rows == 0 || cols == 0) return QLORA_OK;
+  if (!x || !y) return QLORA_ERR_NULL;
+  if (!aligned_el(x, dt) || !aligned_el(y, dt) || !aligned_el(residual, dt))
+    return QLORA_ERR_ALIGN;
+  DropoutArgs a{x, residual, y, ldx, residual ? ldr : 0, ldy, rows, cols, 0, 1.0f, seed, counter};
+  a.p16 = std::min(uint32_t(65536.0 * double(p) + 0.5), 65535u);
+  a.c = float(65536.0 / (65536.0 - a.p16));
+  return dev(timed(QLORA_KERNEL_DROPOUT, stream,
+                   [&] { return launch_dropout(a, dt == QLORA_BF16, stream); }));
+}
+
 int qlora_timing_enable(int kind_mask) {
   g_timing.mask.store(kind_mask & ((1 << QLORA_KERNEL_COUNT) - 1), std::memory_order_relaxed);
   return 0;
@@ -665,7 +860,8 @@ void qlora_timing_reset(void) {
 
 const char *qlora_kernel_name(int kind) {
   static const char *names[QLORA_KERNEL_COUNT] = {
-      "quantize", "xa_rowdot", "fwd_gemm", "dy_pass", "dx_gemm", "da_pass", "reduce", "fwd_smallm"};
+      "quantize", "xa_rowdot", "fwd_gemm", "dy_pass", "dx_gemm", "da_pass", "reduce", "fwd_smallm",
+      "token_logp", "pref_loss", "policy_loss", "dropout"};
   if (kind < 0 || kind >= QLORA_KERNEL_COUNT) return "unknown";
   return names[kind];
 }

@@ -278,6 +278,73 @@ inline int64_t pad8(int64_t m) { return (m + 7) / 8 * 8; }
 
 hipError_t launch_fill_zero(float *p, int64_t n, hipStream_t s);
 
+// Rows of logits [T x V] (row stride ld elements), their labels and inverse
+// temperature.
+struct LogitRows {
+  const void *x;
+  int64_t ld, T, V;
+  bool bf16;
+  const int64_t *labels;
+  float scale;
+};
+
+// The token objective of qlora_policy_loss: the branch bounds on d = logp -
+// old are log(1 - clip_lo), log(1 + clip_hi) and log(clip_dual) (infinite when
+// there is no such bound), formed in double and rounded to fp32 once.
+struct PolicyParams {
+  int clip;                    // 0: NLL
+  float lo, hi, dual;          // 1 - clip_lo, 1 + clip_hi, clip_dual
+  float log_lo, log_hi, log_dual;
+  float kl, ent;
+};
+struct PolicyTokens {
+  const float *weight, *adv, *old, *ref;   // each may be null
+};
+
+// log p of the labels: logp, stats [T x 2] = (m, z), entropy (may be null).
+hipError_t launch_logp_fwd(const LogitRows &a, float *logp, float *stats, float *entropy,
+                           hipStream_t s);
+hipError_t launch_logp_bwd(const LogitRows &a, const float *stats, const float *entropy,
+                           const float *g, const float *g_entropy, void *dx, int64_t ldd,
+                           hipStream_t s);
+// The objective from the logits to their gradient; terms [T x 4] fp32 receives
+// each token's weighted (loss, k, bound, entropy) for launch_sum4.
+hipError_t launch_policy_logits(const LogitRows &a, const PolicyTokens &t,
+                                const PolicyParams &p, float *terms, float *logp, void *dx,
+                                int64_t ldd, hipStream_t s);
+// out[4] = the columns' sums of terms [n x 4], fp64, in a fixed order.
+hipError_t launch_sum4(const float *terms, int64_t n, float *out, hipStream_t s);
+
+// The objective over token arrays.  partial: policy_blocks(T) * 4 doubles,
+// unused (may be null) when that is 1.
+int64_t policy_blocks(int64_t T);
+hipError_t launch_policy(const float *logp, const float *entropy, int64_t T,
+                         const PolicyTokens &t, const PolicyParams &p, float *out, float *dlogp,
+                         float *dentropy, double *partial, hipStream_t s);
+
+// Preference loss.  partial: 2 P pref_splits(P, T) (sum, count) pairs of
+// doubles, unused (may be null) when pref_splits is 0 (one workgroup).
+struct PrefParams {
+  int kind;
+  float beta, margin, smoothing;
+  int average;
+};
+int64_t pref_splits(int64_t P, int64_t T);
+hipError_t launch_pref(const float *logp, const float *ref, const uint8_t *mask,
+                       const int64_t *cu, int64_t P, int64_t T, const PrefParams &p, float *loss,
+                       float *rewards, float *dlogp, double *partial, hipStream_t s);
+
+// y = residual + keep x c, kept where a 16-bit draw is at least p16.
+struct DropoutArgs {
+  const void *x, *res;         // res may be null
+  void *y;
+  int64_t ldx, ldr, ldy, rows, cols;
+  uint32_t p16;
+  float c;
+  uint64_t seed, counter;
+};
+hipError_t launch_dropout(const DropoutArgs &a, bool bf16, hipStream_t s);
+
 // Size of the device-resident scratch array of the forward that allocates
 // nothing, and the device address of the current device's copy (looked up
 // once per device).

@@ -23,7 +23,9 @@ STATUS = {0: "ok", 1: "null pointer", 2: "invalid shape", 3: "pointer not 16-byt
           4: "invalid dtype", 5: "workspace too small", 6: "HIP runtime error",
           7: "invalid value"}
 KERNELS = ("quantize", "xa_rowdot", "fwd_gemm", "dy_pass", "dx_gemm", "da_pass", "reduce",
-           "fwd_smallm")
+           "fwd_smallm", "token_logp", "pref_loss", "policy_loss", "dropout")
+PREF_SIGMOID, PREF_SQUARED, PREF_HINGE = 0, 1, 2                     # qlora_pref_kind
+OBJ_NLL, OBJ_CLIP = 0, 1                                             # qlora_objective
 
 
 class QloraError(RuntimeError):
@@ -53,6 +55,17 @@ class qlora_adam_hparams(ctypes.Structure):
     _fields_ = [("step", ctypes.c_int64), ("lr", ctypes.c_float), ("beta1", ctypes.c_float),
                 ("beta2", ctypes.c_float), ("eps", ctypes.c_float),
                 ("weight_decay", ctypes.c_float)]
+
+
+class qlora_pref(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("beta", ctypes.c_float), ("margin", ctypes.c_float),
+                ("smoothing", ctypes.c_float), ("average", ctypes.c_int32)]
+
+
+class qlora_policy(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("clip_lo", ctypes.c_float),
+                ("clip_hi", ctypes.c_float), ("clip_dual", ctypes.c_float),
+                ("kl_coef", ctypes.c_float), ("ent_coef", ctypes.c_float)]
 
 
 _lib = None
@@ -100,6 +113,27 @@ def lib():
     L.qlora_loftq_init.argtypes = [vp, pnf4, vp, i32, i32, i32, vp, vp, ctypes.c_int, vp, sz, vp]
     L.qlora_loftq_workspace_bytes.argtypes = [i64, i64, i32]
     L.qlora_loftq_workspace_bytes.restype = sz
+    ci, u64 = ctypes.c_int, ctypes.c_uint64
+    L.qlora_token_logp_fwd.argtypes = [vp, i64, i64, i64, ci, vp, f32, vp, vp, vp, vp, sz, vp]
+    L.qlora_token_logp_bwd.argtypes = [vp, i64, i64, i64, ci, vp, f32, vp, vp, vp, vp, vp, i64,
+                                       vp]
+    L.qlora_pref_loss.argtypes = [vp, vp, vp, vp, i64, i64, ctypes.POINTER(qlora_pref), vp, vp,
+                                  vp, vp, sz, vp]
+    ppol = ctypes.POINTER(qlora_policy)
+    L.qlora_policy_loss.argtypes = [vp, vp, i64, vp, vp, vp, vp, ppol, vp, vp, vp, vp, sz, vp]
+    L.qlora_policy_logits.argtypes = [vp, i64, i64, i64, ci, vp, f32, vp, vp, vp, vp, ppol, vp,
+                                      vp, vp, i64, vp, sz, vp]
+    L.qlora_dropout.argtypes = [vp, i64, vp, i64, i64, i64, ci, f32, u64, u64, vp, i64, vp]
+    for f in (L.qlora_token_logp_fwd, L.qlora_token_logp_bwd, L.qlora_pref_loss,
+              L.qlora_policy_loss, L.qlora_policy_logits, L.qlora_dropout):
+        f.restype = ctypes.c_int
+    L.qlora_token_logp_workspace_bytes.argtypes = [i64, i64, ci]
+    L.qlora_policy_logits_workspace_bytes.argtypes = [i64, i64, ci]
+    L.qlora_pref_workspace_bytes.argtypes = [i64, i64]
+    L.qlora_policy_workspace_bytes.argtypes = [i64]
+    for f in (L.qlora_token_logp_workspace_bytes, L.qlora_policy_logits_workspace_bytes,
+              L.qlora_pref_workspace_bytes, L.qlora_policy_workspace_bytes):
+        f.restype = sz
     for f in (L.qlora_quantize, L.qlora_linear_fwd, L.qlora_linear_bwd, L.qlora_merge,
               L.qlora_adam_step, L.qlora_loftq_init, L.qlora_linear_fwd_lora,
               L.qlora_linear_bwd_lora, L.qlora_linear_bwd_adam):
@@ -326,6 +360,91 @@ def qlora_linear_fwd_group(wqs, Xs, M, act, As, Bs, r, adt, Ys, XAs, ws, ws_byte
                                         int(r), int(adt), arr(Ys), arr(XAs), _ptr(ws),
                                         int(ws_bytes), _stream(stream)),
            "qlora_linear_fwd_group")
+
+
+def pref_struct(kind, beta, margin=0.0, smoothing=0.0, average=False):
+    """qlora_pref: the objective of qlora_pref_loss."""
+    return qlora_pref(int(kind), float(beta), float(margin), float(smoothing), int(average))
+
+
+def policy_struct(kind, clip_lo=0.2, clip_hi=0.2, clip_dual=0.0, kl_coef=0.0, ent_coef=0.0):
+    """qlora_policy: the objective of qlora_policy_loss and qlora_policy_logits."""
+    return qlora_policy(int(kind), float(clip_lo), float(clip_hi), float(clip_dual),
+                        float(kl_coef), float(ent_coef))
+
+
+def qlora_token_logp_workspace_bytes(T, V, dt):
+    return int(lib().qlora_token_logp_workspace_bytes(int(T), int(V), int(dt)))
+
+
+def qlora_token_logp_fwd(logits, ld, T, V, dt, labels, scale, logp, stats, entropy, ws, ws_bytes,
+                         stream=None):
+    """Log-probability of each row's label (int64), the row's (m, z) and, if
+    `entropy` is not None, its entropy."""
+    _check(lib().qlora_token_logp_fwd(_ptr(logits), int(ld), int(T), int(V), int(dt),
+                                      _ptr(labels), float(scale), _ptr(logp), _ptr(stats),
+                                      _ptr(entropy), _ptr(ws), int(ws_bytes), _stream(stream)),
+           "qlora_token_logp_fwd")
+
+
+def qlora_token_logp_bwd(logits, ld, T, V, dt, labels, scale, stats, entropy, g, g_entropy,
+                         dlogits, ldd, stream=None):
+    """The logits' gradient (dlogits may be logits) from that of the
+    log-probabilities and, unless both are None, of the entropies."""
+    _check(lib().qlora_token_logp_bwd(_ptr(logits), int(ld), int(T), int(V), int(dt),
+                                      _ptr(labels), float(scale), _ptr(stats), _ptr(entropy),
+                                      _ptr(g), _ptr(g_entropy), _ptr(dlogits), int(ldd),
+                                      _stream(stream)), "qlora_token_logp_bwd")
+
+
+def qlora_pref_workspace_bytes(P, T):
+    return int(lib().qlora_pref_workspace_bytes(int(P), int(T)))
+
+
+def qlora_pref_loss(logp, ref, mask, cu, P, T, pref, loss, rewards, dlogp, ws, ws_bytes,
+                    stream=None):
+    """Loss of P pairs of answers and its gradient by token; `pref` from
+    pref_struct; ref and mask may be None."""
+    _check(lib().qlora_pref_loss(_ptr(logp), _ptr(ref), _ptr(mask), _ptr(cu), int(P), int(T),
+                                 ctypes.byref(pref), _ptr(loss), _ptr(rewards), _ptr(dlogp),
+                                 _ptr(ws), int(ws_bytes), _stream(stream)), "qlora_pref_loss")
+
+
+def qlora_policy_workspace_bytes(T):
+    return int(lib().qlora_policy_workspace_bytes(int(T)))
+
+
+def qlora_policy_loss(logp, entropy, T, weight, adv, old, ref, policy, out, dlogp, dentropy, ws,
+                      ws_bytes, stream=None):
+    """Policy objective over tokens: out[4], dlogp and, if wanted, dentropy;
+    `policy` from policy_struct; entropy, weight, adv, old, ref may be None."""
+    _check(lib().qlora_policy_loss(_ptr(logp), _ptr(entropy), int(T), _ptr(weight), _ptr(adv),
+                                   _ptr(old), _ptr(ref), ctypes.byref(policy), _ptr(out),
+                                   _ptr(dlogp), _ptr(dentropy), _ptr(ws), int(ws_bytes),
+                                   _stream(stream)), "qlora_policy_loss")
+
+
+def qlora_policy_logits_workspace_bytes(T, V, dt):
+    return int(lib().qlora_policy_logits_workspace_bytes(int(T), int(V), int(dt)))
+
+
+def qlora_policy_logits(logits, ld, T, V, dt, labels, scale, weight, adv, old, ref, policy, out,
+                        logp, dlogits, ldd, ws, ws_bytes, stream=None):
+    """The same objective from the logits to their gradient (dlogits may be
+    logits); logp may be None."""
+    _check(lib().qlora_policy_logits(_ptr(logits), int(ld), int(T), int(V), int(dt),
+                                     _ptr(labels), float(scale), _ptr(weight), _ptr(adv),
+                                     _ptr(old), _ptr(ref), ctypes.byref(policy), _ptr(out),
+                                     _ptr(logp), _ptr(dlogits), int(ldd), _ptr(ws),
+                                     int(ws_bytes), _stream(stream)), "qlora_policy_logits")
+
+
+def qlora_dropout(x, ldx, residual, ldr, rows, cols, dt, p, seed, counter, y, ldy, stream=None):
+    """y = residual + keep * x / (1 - p) with the mask of (seed, counter);
+    residual may be None.  The backward is the same call on the gradient."""
+    _check(lib().qlora_dropout(_ptr(x), int(ldx), _ptr(residual), int(ldr), int(rows), int(cols),
+                               int(dt), float(p), int(seed), int(counter), _ptr(y), int(ldy),
+                               _stream(stream)), "qlora_dropout")
 
 
 def qlora_levels():
