@@ -450,6 +450,7 @@ size_t qlora_token_logp_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt);
  *   g [T]; entropy and g_entropy [T] both, or both NULL (no entropy term).
  *   dlogits [T, V] dt, rows of ldd elements; may be `logits` itself with
  *   ldd = ld (the gradient then replaces the logits).
+ * Where g (and gH) is 0 the row is 0 and its logits are not read.
  */
 qlora_status qlora_token_logp_bwd(const void *logits, int64_t ld, int64_t T, int64_t V,
                                   qlora_dtype dt, const int64_t *labels, float scale,

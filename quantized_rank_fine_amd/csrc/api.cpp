@@ -358,6 +358,21 @@ qlora_status check_logits(int64_t ld, int64_t T, int64_t V, qlora_dtype dt, floa
   return QLORA_OK;
 }
 
+// Workspace of the objective from the logits: every token's terms, and the
+// partial sums of many.
+struct TermsPlan {
+  size_t off_partial = 0, total = 0;
+};
+
+TermsPlan plan_terms(int64_t T) {
+  TermsPlan p;
+  Layout L;
+  L.take(size_t(T) * 4 * sizeof(float));
+  if (terms_blocks(T) > 1) p.off_partial = L.take(size_t(terms_blocks(T)) * 4 * sizeof(double));
+  p.total = L.o;
+  return p;
+}
+
 qlora_status policy_params(const qlora_policy *q, PolicyParams &p) {
   if (!q) return QLORA_ERR_NULL;
   const bool ok = (q->kind == QLORA_OBJ_NLL || q->kind == QLORA_OBJ_CLIP) &&
@@ -764,7 +779,7 @@ qlora_status qlora_policy_loss(const float *logp, const float *entropy, int64_t 
 
 size_t qlora_policy_logits_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt) {
   if (check_logits(V, T, V, dt, 1.0f) != QLORA_OK) return 0;
-  return size_t(T) * 4 * sizeof(float);
+  return plan_terms(T).total;
 }
 
 qlora_status qlora_policy_logits(const void *logits, int64_t ld, int64_t T, int64_t V,
@@ -786,8 +801,10 @@ qlora_status qlora_policy_logits(const void *logits, int64_t ld, int64_t T, int6
   for (const float *v : {weight, adv, old, ref, static_cast<const float *>(out),
                          static_cast<const float *>(logp)})
     if (!aligned_to(v, 4)) return QLORA_ERR_ALIGN;
-  if (ws_bytes < qlora_policy_logits_workspace_bytes(T, V, dt)) return QLORA_ERR_WORKSPACE;
+  const TermsPlan plan = plan_terms(T);
+  if (ws_bytes < plan.total) return QLORA_ERR_WORKSPACE;
   float *terms = static_cast<float *>(ws);
+  double *partial = plan.off_partial ? at<double>(ws, plan.off_partial) : nullptr;
   if (T > 0) {
     const LogitRows a{logits, ld, T, V, dt == QLORA_BF16, labels, scale};
     const hipError_t e = timed(QLORA_KERNEL_POLICY, stream, [&] {
@@ -797,7 +814,7 @@ qlora_status qlora_policy_logits(const void *logits, int64_t ld, int64_t T, int6
     if (e != hipSuccess) return QLORA_ERR_DEVICE;
   }
   return dev(timed(QLORA_KERNEL_POLICY, stream,
-                   [&] { return launch_sum4(terms, T, out, stream); }));
+                   [&] { return launch_sum_terms(terms, T, out, partial, stream); }));
 }
 
 qlora_status qlora_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr,

@@ -308,12 +308,15 @@ hipError_t launch_logp_bwd(const LogitRows &a, const float *stats, const float *
                            const float *g, const float *g_entropy, void *dx, int64_t ldd,
                            hipStream_t s);
 // The objective from the logits to their gradient; terms [T x 4] fp32 receives
-// each token's weighted (loss, k, bound, entropy) for launch_sum4.
+// each token's weighted (loss, k, bound, entropy) for launch_sum_terms.
 hipError_t launch_policy_logits(const LogitRows &a, const PolicyTokens &t,
                                 const PolicyParams &p, float *terms, float *logp, void *dx,
                                 int64_t ldd, hipStream_t s);
-// out[4] = the columns' sums of terms [n x 4], fp64, in a fixed order.
-hipError_t launch_sum4(const float *terms, int64_t n, float *out, hipStream_t s);
+// out[4] = the columns' sums of terms [n x 4], fp64, in an order that n fixes.
+// partial: terms_blocks(n) * 4 doubles, unused (may be null) when that is 1.
+int64_t terms_blocks(int64_t n);
+hipError_t launch_sum_terms(const float *terms, int64_t n, float *out, double *partial,
+                            hipStream_t s);
 
 // The objective over token arrays.  partial: policy_blocks(T) * 4 doubles,
 // unused (may be null) when that is 1.

@@ -1,161 +1,252 @@
 // Row kernels over logits: the label's log-probability and the entropy, the
 // logits' gradient, and the policy objective that does both at once.
 //
-// For one row x with label y and inverse temperature s:
-//   m = max x,  z = log sum exp(s (x - m)),  log p_v = s (x_v - m) - z,
-//   H = z - sum e_v s (x_v - m) / sum e_v,   e_v = exp(s (x_v - m)),
+// For one row x with label y and inverse temperature s, c = s log2 e:
+//   m = max x,  L_v = c (x_v - m),  e_v = exp2(L_v),
+//   t = sum e,  w = sum e L,
+//   z = ln t,  log p_v = s (x_v - m) - z,  H = z - ln 2 w / t,
 //   dx_v = s (g (1[v = y] - p_v) - gH p_v (log p_v + H)).
 // m is the maximum of the raw logits and z is kept beside it: their
 // difference from a logit is exact enough for any size of logit, where
-// s x - (s m + z) would lose the digits that s m holds.  exp is taken as
-// exp2(c (x - m)), c = s log2 e, on the hardware's exp2.
+// s x - (s m + z) would lose the digits that s m holds.
 //
-// One pass with the running maximum m, t = sum e and w = sum e (x - m): when
-// the maximum rises by d, e shrinks by f = exp2(-c d), so
-//   w <- f (w - d t),  t <- f t.
+// Sums taken against one maximum are brought to a higher one: with L' = L + d
+// and f = exp2(d), t' = f t and w' = f (w + d t).
 //
-// HBM-bound: the forward reads each scored row once; the gradient also writes
-// each row once.  Rows of an odd V start at any element, so a group of 8
-// logits is loaded at its element's alignment.
+// HBM-bound: the forward reads each scored row once, the gradient also writes
+// each row once.  Rows of an odd V start at any element: a row is cut into up
+// to 7 words before its first 16-byte boundary, groups of 8, and up to 7 after
+// the last whole group.
 #include "objective.h"
 
 namespace qlora {
 namespace {
 
-// A launch holds less than 2^32 threads: workgroups go round the rows.
-constexpr int64_t kMaxBlocks = int64_t(1) << 21;
+// Rows in the y and z of a launch, a row's segments in x: neighbouring
+// workgroups run through a row, and no dimension reaches its limit.
+constexpr int64_t kRowsY = int64_t(1) << 15;
 constexpr float kLog2e = 1.44269504088896340736f;
-
-// 8 consecutive elements at element alignment.
-template <bool BF16>
-struct Row {
-  const char *p;
-  __device__ __forceinline__ Row(const void *x, int64_t at)
-      : p(static_cast<const char *>(x) + at * (BF16 ? 2 : 4)) {}
-  __device__ __forceinline__ void load8(int64_t v, float (&e)[8]) const {
-    if (BF16) {
-      u32x4_t u;
-      __builtin_memcpy(&u, p + v * 2, 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[2 * i] = bf16_lo_to_f32(u[i]);
-        e[2 * i + 1] = bf16_hi_to_f32(u[i]);
-      }
-    } else {
-      __builtin_memcpy(e, p + v * 4, 32);
-    }
-  }
-  __device__ __forceinline__ float load1(int64_t v) const {
-    if (BF16) {
-      uint16_t h;
-      __builtin_memcpy(&h, p + v * 2, 2);
-      return __uint_as_float(uint32_t(h) << 16);
-    }
-    float f;
-    __builtin_memcpy(&f, p + v * 4, 4);
-    return f;
-  }
-  // the group's elements, -inf past the row's end
-  __device__ __forceinline__ void load(int64_t v, int64_t V, float (&e)[8]) const {
-    if (v + 8 <= V) {
-      load8(v, e);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = v + i < V ? load1(v + i) : -INFINITY;
-    }
-  }
-};
+constexpr float kLn2 = 0.69314718055994530942f;
+// exp2 is 0 from here down: an exponent of -inf, which would turn 0 L into
+// NaN, is taken as this.
+constexpr float kLeast = -200.0f;
 
 template <bool BF16>
-__device__ __forceinline__ void store(void *x, int64_t at, int64_t left, const float (&e)[8]) {
+__device__ __forceinline__ const char *row_at(const void *x, int64_t at) {
+  return static_cast<const char *>(x) + at * (BF16 ? 2 : 4);
+}
+template <bool BF16>
+__device__ __forceinline__ char *row_at(void *x, int64_t at) {
+  return static_cast<char *>(x) + at * (BF16 ? 2 : 4);
+}
+
+__device__ __forceinline__ int64_t row_index() {
+  return int64_t(blockIdx.z) * kRowsY + blockIdx.y;
+}
+
+// Word v of a row, and words v .. v + 7 at their element's alignment (V is at
+// most 2^24, so a row's offsets fit 32 bits).
+template <bool BF16>
+__device__ __forceinline__ float load1(const char *row, uint32_t v) {
   if (BF16) {
-    char *p = static_cast<char *>(x) + at * 2;
-    const u32x4_t u = {pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
-                       pack_bf16x2(e[6], e[7])};
-    if (left >= 8) {
-      __builtin_memcpy(p, &u, 16);
-    } else {
+    uint16_t h;
+    __builtin_memcpy(&h, row + v * 2u, 2);
+    return __uint_as_float(uint32_t(h) << 16);
+  }
+  float f;
+  __builtin_memcpy(&f, row + v * 4u, 4);
+  return f;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const char *row, uint32_t v, float (&e)[8]) {
+  if (BF16) {
+    u32x4_t u;
+    __builtin_memcpy(&u, row + v * 2u, 16);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) {
-          const uint16_t h = uint16_t(u[i / 2] >> (16 * (i % 2)));
-          __builtin_memcpy(p + 2 * i, &h, 2);
-        }
+    for (int i = 0; i < 4; ++i) {
+      e[2 * i] = bf16_lo_to_f32(u[i]);
+      e[2 * i + 1] = bf16_hi_to_f32(u[i]);
     }
   } else {
-    char *p = static_cast<char *>(x) + at * 4;
-    if (left >= 8) {
-      __builtin_memcpy(p, e, 32);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) __builtin_memcpy(p + 4 * i, &e[i], 4);
-    }
+    __builtin_memcpy(e, row + v * 4u, 32);
   }
 }
 
-struct Stat {
-  float m, t, w;   // maximum, sum e, sum e (x - m)
+template <bool BF16>
+__device__ __forceinline__ void store1(char *row, uint32_t v, float e) {
+  if (BF16) {
+    const uint16_t h = __builtin_bit_cast(uint16_t, (__bf16)e);
+    __builtin_memcpy(row + v * 2u, &h, 2);
+  } else {
+    __builtin_memcpy(row + v * 4u, &e, 4);
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(char *row, uint32_t v, const float (&e)[8]) {
+  if (BF16) {
+    const u32x4_t u = {pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                       pack_bf16x2(e[6], e[7])};
+    __builtin_memcpy(row + v * 2u, &u, 16);
+  } else {
+    __builtin_memcpy(row + v * 4u, e, 32);
+  }
+}
+
+// The cut of a row of V words at address `row`: `head` words, groups of 8 words
+// from there on, `whole` words in all, and the rest.  Head and rest ("ones")
+// are one word to a lane, the rest in lanes 0 .. 7, the head in 8 .. 15.
+template <bool BF16>
+struct Cut {
+  int32_t head, whole, V;
+  __device__ __forceinline__ Cut(const char *row, int32_t words) : V(words) {
+    const int32_t off = int32_t(-reinterpret_cast<uintptr_t>(row) & 15u) / (BF16 ? 2 : 4);
+    head = off < V ? off : V;
+    whole = (V - head) / 8 * 8;
+  }
+  // the word of lane `at` among the ones, or V
+  __device__ __forceinline__ int32_t one(int32_t at) const {
+    if (at < 8) return head + whole + at < V ? head + whole + at : V;
+    return at - 8 < head ? at - 8 : V;
+  }
 };
 
-// a's sums brought to the maximum `top` (>= a.m); nothing seen yet is
-// m = -inf, t = w = 0 and stays so.
+// Words of a row in registers: group g of a lane is the 8 words from
+// head + from + 8 (g threads + lane) on, as they lie in memory.  Groups past
+// the last whole one load that one again and are masked to -inf, so every load
+// is whole and none leaves the row.  The ones come with the row's first chunk.
+template <bool BF16, int threads, int NG>
+struct Held {
+  static constexpr int32_t words = threads * 8 * NG;
+  u32x4_t q[BF16 ? NG : 2 * NG];
+  float one;
+
+  __device__ __forceinline__ static int32_t first(int g) {
+    return (g * threads + int(threadIdx.x)) * 8;
+  }
+  // the groups [from, from + words) of a row, from < whole or 0
+  __device__ __forceinline__ void load(const char *row, const Cut<BF16> &k, int32_t from) {
+    const int32_t last = k.whole - 8;
+    if (last >= 0) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int32_t v = from + first(g);
+        const uint32_t at = uint32_t(k.head + (v <= last ? v : last));
+        if (BF16) {
+          __builtin_memcpy(&q[g], row + at * 2u, 16);
+        } else {
+          __builtin_memcpy(&q[2 * g], row + at * 4u, 16);
+          __builtin_memcpy(&q[2 * g + 1], row + at * 4u + 16u, 16);
+        }
+      }
+    }
+    one = -INFINITY;
+    if (from == 0) {
+      const int32_t v = k.one(int32_t(threadIdx.x));
+      if (v < k.V) one = load1<BF16>(row, v);
+    }
+    if (from + words > last) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        if (from + first(g) > last) {
+          const uint32_t w = BF16 ? 0xff80ff80u : 0xff800000u;
+          q[BF16 ? g : 2 * g] = u32x4_t{w, w, w, w};
+          if (!BF16) q[2 * g + 1] = u32x4_t{w, w, w, w};
+        }
+    }
+  }
+  // Between two passes over the registers: without it the compiler keeps the
+  // unpacked words of one pass for the next, twice the registers and more.
+  __device__ __forceinline__ void keep() {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? NG : 2 * NG); ++i) asm volatile("" : "+v"(q[i]));
+  }
+  __device__ __forceinline__ void get(int g, float (&e)[8]) const {
+    if (BF16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        e[2 * i] = bf16_lo_to_f32(q[g][i]);
+        e[2 * i + 1] = bf16_hi_to_f32(q[g][i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = __uint_as_float(q[2 * g + i / 4][i % 4]);
+    }
+  }
+};
+
+struct Stat {
+  float m, t, w;   // maximum, sum e, sum e L with L = c x - reference(m)
+};
+
+// L is taken as c x - M with M = c m rounded once, in one fused operation:
+// whatever M is, it cancels from log p.  M is 0 where there is no word yet and
+// where c m is too large for it; t then comes out 0 or infinite with m finite
+// and the row is summed again by careful_row.
+__device__ __forceinline__ float reference(float m, float c) {
+  const float M = c * m;
+  return fabsf(M) < 1e30f ? M : 0.0f;
+}
+
+template <bool ENT>
+__device__ __forceinline__ void add(Stat &a, float x, float c, float M) {
+  const float L = __builtin_fmaf(c, x, -M);
+  const float p = __builtin_amdgcn_exp2f(L);   // a NaN logit leaves its mark in t
+  a.t += p;
+  if (ENT) a.w = __builtin_fmaf(p, fmaxf(L, kLeast), a.w);
+}
+
+// a's sums brought from their own reference to that of `top` >= a.m.
 __device__ __forceinline__ Stat raised(const Stat &a, float top, float c) {
-  const float d = a.m - top;                      // <= 0, or NaN from -inf - -inf
-  if (!(a.m > -INFINITY)) return {top, a.t, a.w};
-  const float f = __builtin_amdgcn_exp2f(c * d);
-  // a maximum that rose by an infinite step leaves nothing (0 * inf)
-  return {top, f * a.t, f > 0.0f ? f * (a.w + d * a.t) : 0.0f};
+  const float d = reference(a.m, c) - reference(top, c);
+  // nothing summed yet: t and w are 0, or NaN from NaN logits alone
+  const float f = a.m > -INFINITY ? __builtin_amdgcn_exp2f(d) : 0.0f;
+  return {top, f * a.t, f * __builtin_fmaf(d, a.t, a.w)};
 }
 
-__device__ __forceinline__ Stat joined(const Stat &a, const Stat &b, float c) {
-  const float top = fmaxf(a.m, b.m);
-  const Stat x = raised(a, top, c), y = raised(b, top, c);
-  return {top, x.t + y.t, x.w + y.w};
-}
-
-__device__ __forceinline__ void add8(Stat &a, const float (&e)[8], float c) {
-  float top = a.m;
+// A lane's share of a chunk into its running sums.
+template <bool ENT, bool BF16, int threads, int NG>
+__device__ __forceinline__ void add_chunk(Stat &a, Held<BF16, threads, NG> &h, float c) {
+  float top = fmaxf(a.m, h.one);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, e[i]);
-  a = raised(a, top, c);
-  // a group of nothing but -inf: differences from 0, every e is 0
-  const float base = top > -INFINITY ? top : 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = e[i] - base;
-    const float q = __builtin_amdgcn_exp2f(c * d);
-    a.t += q;
-    a.w += q > 0.0f ? q * d : 0.0f;
-  }
-}
-
-// A NaN logit is skipped by the maximum but not by the sum: t becomes NaN.
-template <int threads>
-__device__ __forceinline__ Stat block_stat(Stat a, float c, Stat *red) {
-  __syncthreads();   // the previous row's results have been read
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const Stat b = {__shfl_xor(a.m, o), __shfl_xor(a.t, o), __shfl_xor(a.w, o)};
-    a = joined(a, b, c);
-  }
-  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = a;
-  __syncthreads();
-  a = red[0];
-#pragma unroll
-  for (int w = 1; w < threads / 64; ++w) a = joined(a, red[w], c);
-  return a;
-}
-
-template <bool BF16, int threads>
-__device__ __forceinline__ Stat row_stat(const Row<BF16> &row, int64_t V, float c, Stat *red) {
-  Stat s = {-INFINITY, 0.0f, 0.0f};
-  for (int64_t v = int64_t(threadIdx.x) * 8; v < V; v += threads * 8) {
+  for (int g = 0; g < NG; ++g) {
     float e[8];
-    row.load(v, V, e);
-    add8(s, e, c);
+    h.get(g, e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, e[i]);
   }
-  return block_stat<threads>(s, c, red);
+  a = raised(a, top, c);
+  h.keep();
+  const float M = reference(top, c);
+  add<ENT>(a, h.one, c, M);
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    float e[8];
+    h.get(g, e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) add<ENT>(a, e[i], c, M);
+  }
+}
+
+// The sums of 64 lanes as one, in every lane.
+__device__ __forceinline__ Stat joined(const Stat &a, float c) {
+  const float top = wave_max(a.m);
+  const Stat b = raised(a, top, c);
+  return {top, wave_sum(b.t), wave_sum(b.w)};
+}
+
+// The sums of a workgroup as one, in every lane, in an order that `threads`
+// alone fixes.
+template <int threads>
+__device__ __forceinline__ Stat joined_block(Stat a, float c, Stat *red) {
+  a = joined(a, c);
+  if (threads == 64) return a;
+  const int lane = threadIdx.x % 64;
+  if (lane == 0) red[threadIdx.x / 64] = a;
+  __syncthreads();
+  a = lane < threads / 64 ? red[lane] : Stat{-INFINITY, 0.0f, 0.0f};
+  return joined(a, c);
 }
 
 struct RowResult {
@@ -163,169 +254,329 @@ struct RowResult {
 };
 
 // Results of a row from its sums and its label's logit.
-__device__ __forceinline__ RowResult row_result(const Stat &a, float xy, float scale) {
-  if (a.t != a.t) return {a.t, a.t, a.t, a.t};
+// `off`: c m - M, by which z takes the rounding of M back.
+__device__ __forceinline__ RowResult row_result(const Stat &a, float off, float xy, float scale) {
+  if (!(a.t < INFINITY)) {
+    const float nan = a.t - a.t;
+    return {nan, nan, nan, nan};
+  }
   if (!(a.m > -INFINITY)) return {-INFINITY, 0.0f, -INFINITY, 0.0f};
-  const float z = logf(a.t);
-  return {a.m, z, scale * (xy - a.m) - z, z - scale * (a.w / a.t)};
+  const float l = logf(a.t), z = l - kLn2 * off;
+  return {a.m, z, scale * (xy - a.m) - z, l - kLn2 * (a.w / a.t)};
 }
 
+// The sums of a row whose c m is out of reach: L = c (x - m) in two steps, the
+// row read again.  Such rows are all but -inf; speed does not matter here.
 template <bool BF16, int threads>
-__global__ __launch_bounds__(threads) void logp_fwd_kernel(LogitRows a, float *logp, float *stats,
-                                                           float *entropy) {
-  __shared__ Stat red[threads / 64];
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const int64_t y = a.labels[t];
-    RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (y >= 0 && y < a.V) {
-      const Row<BF16> row(a.x, t * a.ld);
-      const Stat s = row_stat<BF16, threads>(row, a.V, a.scale * kLog2e, red);
-      if (threadIdx.x == 0) r = row_result(s, row.load1(y), a.scale);
-    }
-    if (threadIdx.x == 0) {
-      logp[t] = r.logp;
-      stats[2 * t] = r.m;
-      stats[2 * t + 1] = r.z;
-      if (entropy) entropy[t] = r.ent;
-    }
+__device__ __forceinline__ Stat careful_row(const char *row, int32_t V, float m, float c,
+                                         Stat *red) {
+  Stat a = {0.0f, 0.0f, 0.0f};
+  for (int32_t v = int32_t(threadIdx.x); v < V; v += threads) {
+    const float L = c * (load1<BF16>(row, v) - m);
+    const float p = __builtin_amdgcn_exp2f(L);
+    a.t += p;
+    a.w = __builtin_fmaf(p, fmaxf(L, kLeast), a.w);
   }
+  __syncthreads();
+  return joined_block<threads>(a, c, red);
 }
 
-// The gradient of 8 logits: d = s (g (1[v = y] - p) - gh p (log p + H)).
-__device__ __forceinline__ void grad8(float (&e)[8], int64_t v, int64_t y, float scale, float m,
-                                      float z, float g, float gh, float ent) {
+// A row's results: its chunks summed one after the other.  h holds the last
+// chunk afterwards (the whole row where it is the only one).
+template <bool ENT, bool ONE, bool BF16, int threads, int NG>
+__device__ __forceinline__ RowResult row_stat(Held<BF16, threads, NG> &h, const char *row,
+                                              int32_t V, int32_t y, float scale, Stat *red) {
+  const float c = scale * kLog2e;
+  Stat a = {-INFINITY, 0.0f, 0.0f};
+  const Cut<BF16> k(row, V);
+  h.load(row, k, 0);
+  const float xy = load1<BF16>(row, uint32_t(y));
+  add_chunk<ENT>(a, h, c);
+  for (int32_t from = h.words; !ONE && from < k.whole; from += h.words) {
+    h.load(row, k, from);
+    add_chunk<ENT>(a, h, c);
+  }
+  a = joined_block<threads>(a, c, red);
+  float off = __builtin_fmaf(c, a.m, -reference(a.m, c));
+  if (!(a.t > 0.0f && a.t < INFINITY) && fabsf(a.m) < INFINITY) {
+    const float m = a.m;
+    a = careful_row<BF16, threads>(row, V, m, c, red);
+    a.m = m;
+    off = 0.0f;
+  }
+  return row_result(a, off, xy, scale);
+}
+
+// Coefficients of a row's gradient: with L = log2 p,
+//   dx = s (g 1[v = y] - g p - gH p (ln 2 L + H)) = hot 1[v = y] + p (k0 + k1 L).
+struct GradCoef {
+  float hot, k0, k1, z2;
+};
+
+__device__ __forceinline__ GradCoef grad_coef(float scale, float g, float gh, float ent, float z) {
+  // a row of NaN stays one, also where the clamp of L makes p 0
+  const float nan = z != z ? z : 0.0f;
+  return {scale * g, -scale * (g + gh * ent) + nan, -scale * gh * kLn2, z * kLog2e};
+}
+
+template <bool ENT, int N>
+__device__ __forceinline__ void grad(float (&e)[N], int32_t label, float m, float c,
+                                     const GradCoef &k) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float lp = scale * (e[i] - m) - z;
-    const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
-    float d = (v + i == y ? g : 0.0f) - g * p;
-    if (gh != 0.0f) d -= p > 0.0f ? gh * (p * (lp + ent)) : gh * p;
-    e[i] = scale * d;
+  for (int i = 0; i < N; ++i) {
+    float L = __builtin_fmaf(c, e[i] - m, -k.z2);
+    if (ENT) L = fmaxf(L, kLeast);
+    const float p = __builtin_amdgcn_exp2f(L);
+    e[i] = p * (ENT ? __builtin_fmaf(k.k1, L, k.k0) : k.k0);
+  }
+  if (uint32_t(label) < uint32_t(N)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] += i == label ? k.hot : 0.0f;
   }
 }
 
+// Zeros, a row's gradient where there is none.
 template <bool BF16, int threads>
-__device__ __forceinline__ void grad_row(const Row<BF16> &row, void *dx, int64_t at, int64_t V,
-                                         int64_t y, float scale, float m, float z, float g,
-                                         float gh, float ent, bool live) {
-  for (int64_t v = int64_t(threadIdx.x) * 8; v < V; v += threads * 8) {
-    float e[8] = {};
-    if (live) {
-      row.load(v, V, e);
-      grad8(e, v, y, scale, m, z, g, gh, ent);
-    }
-    store<BF16>(dx, at + v, V - v, e);
+__device__ __forceinline__ void zero_row(char *out, int32_t V) {
+  const float e[8] = {};
+  const Cut<BF16> k(out, V);
+  for (int32_t v = int32_t(threadIdx.x) * 8; v < k.whole; v += threads * 8)
+    store8<BF16>(out, k.head + v, e);
+  const int32_t one = k.one(int32_t(threadIdx.x));
+  if (one < V) store1<BF16>(out, one, 0.0f);
+}
+
+template <bool BF16, bool ENT, int threads, int NG>
+__global__ __launch_bounds__(threads) void logp_fwd_kernel(LogitRows a, float *logp,
+                                                                  float *stats, float *entropy) {
+  __shared__ Stat red[threads / 64];
+  const int64_t t = row_index();
+  if (t >= a.T) return;
+  const int64_t y = a.labels[t];
+  RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (y >= 0 && y < a.V) {
+    Held<BF16, threads, NG> h;
+    r = row_stat<ENT, false>(h, row_at<BF16>(a.x, t * a.ld), int32_t(a.V), int32_t(y), a.scale,
+                      red);
+  }
+  if (threadIdx.x == 0) {
+    logp[t] = r.logp;
+    stats[2 * t] = r.m;
+    stats[2 * t + 1] = r.z;
+    if (ENT) entropy[t] = r.ent;
   }
 }
 
-template <bool BF16, int threads>
+// One segment of threads * 8 * NG words of a row's gradient to a workgroup.
+template <bool BF16, bool ENT, int threads, int NG>
 __global__ __launch_bounds__(threads) void logp_bwd_kernel(LogitRows a, const float *stats,
                                                            const float *entropy, const float *g,
                                                            const float *g_entropy, void *dx,
                                                            int64_t ldd) {
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const int64_t y = a.labels[t];
-    const float m = stats[2 * t], z = stats[2 * t + 1];
-    const bool live = y >= 0 && y < a.V && m != -INFINITY;
-    const Row<BF16> row(a.x, t * a.ld);
-    grad_row<BF16, threads>(row, dx, t * ldd, a.V, y, a.scale, m, z, g[t],
-                            g_entropy ? g_entropy[t] : 0.0f, entropy ? entropy[t] : 0.0f, live);
+  const int64_t t = row_index();
+  if (t >= a.T) return;
+  const int32_t V = int32_t(a.V);
+  const float c = a.scale * kLog2e;
+  const char *row = row_at<BF16>(a.x, t * a.ld);
+  char *out = row_at<BF16>(dx, t * ldd);
+  const Cut<BF16> q(row, V);
+  const int32_t from = (int32_t(blockIdx.x) * threads * NG + int32_t(threadIdx.x)) * 8;
+  const int32_t one = blockIdx.x == 0 ? q.one(int32_t(threadIdx.x)) : V;
+  const int64_t y = a.labels[t];
+  const float m = stats[2 * t], z = stats[2 * t + 1];
+  const float gt = g[t], gh = ENT ? g_entropy[t] : 0.0f;
+  if (y >= 0 && y < V && m != -INFINITY && (gt != 0.0f || gh != 0.0f)) {
+    float e[NG][8];
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      if (from + i * threads * 8 < q.whole)
+        load8<BF16>(row, q.head + from + i * threads * 8, e[i]);
+    const GradCoef k = grad_coef(a.scale, gt, gh, ENT ? entropy[t] : 0.0f, z);
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const int32_t v = q.head + from + i * threads * 8;
+      if (from + i * threads * 8 < q.whole) {
+        grad<ENT>(e[i], int32_t(y) - v, m, c, k);
+        store8<BF16>(out, v, e[i]);
+      }
+    }
+    if (one < V) {
+      float d[1] = {load1<BF16>(row, one)};
+      grad<ENT>(d, int32_t(y) - one, m, c, k);
+      store1<BF16>(out, one, d[0]);
+    }
+  } else {
+    const float e[8] = {};
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      if (from + i * threads * 8 < q.whole) store8<BF16>(out, q.head + from + i * threads * 8, e);
+    if (one < V) store1<BF16>(out, one, 0.0f);
+  }
+}
+
+// The gradient of a row whose words h holds, or, where the row is longer than
+// that, of the row read again (each word by the lane that then overwrites it).
+template <bool ENT, bool ONE, bool BF16, int threads, int NG>
+__device__ __forceinline__ void row_grad(Held<BF16, threads, NG> &h, const char *row, char *out,
+                                         int32_t V, int32_t y, float m, float c,
+                                         const GradCoef &k) {
+  const Cut<BF16> q(row, V);
+  if (ONE) {
+    h.keep();
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const int32_t v = h.first(i);
+      if (v < q.whole) {
+        float e[8];
+        h.get(i, e);
+        grad<ENT>(e, y - q.head - v, m, c, k);
+        store8<BF16>(out, q.head + v, e);
+      }
+      // one group's words unpacked at a time
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+    for (int32_t v = int32_t(threadIdx.x) * 8; v < q.whole; v += threads * 8) {
+      float e[8];
+      load8<BF16>(row, q.head + v, e);
+      grad<ENT>(e, y - q.head - v, m, c, k);
+      store8<BF16>(out, q.head + v, e);
+    }
+  }
+  const int32_t one = q.one(int32_t(threadIdx.x));
+  if (one < V) {
+    float d[1] = {ONE ? h.one : load1<BF16>(row, one)};
+    grad<ENT>(d, y - one, m, c, k);
+    store1<BF16>(out, one, d[0]);
   }
 }
 
 // The policy objective from a row's logits to their gradient: the row's
-// coefficient depends on the row alone, so the gradient follows in the same
-// workgroup.
-template <bool BF16, int threads>
-__global__ __launch_bounds__(threads) void policy_logits_kernel(LogitRows a, PolicyTokens k,
-                                                                PolicyParams p, float *terms,
-                                                                float *logp, void *dx,
-                                                                int64_t ldd) {
+// coefficient depends on the row alone, so the gradient follows from the
+// registers that gave the sums.  Every logit has been read before the barrier
+// of the sums, so dx may be the logits.
+template <bool BF16, bool ENT, bool ONE, int threads, int NG>
+__global__ __launch_bounds__(threads) void policy_logits_kernel(
+    LogitRows a, PolicyTokens k, PolicyParams p, float *terms, float *logp, void *dx,
+    int64_t ldd) {
   __shared__ Stat red[threads / 64];
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const int64_t y = a.labels[t];
-    const float w = k.weight ? k.weight[t] : 1.0f;
-    const Row<BF16> row(a.x, t * a.ld);
-    bool live = y >= 0 && y < a.V && w != 0.0f;
-    float g = 0.0f;
-    RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
-    f32x4_t term = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (live) {
-      // read before the workgroup's barriers, so before dx may overwrite it
-      const float xy = row.load1(y);
-      const Stat s = row_stat<BF16, threads>(row, a.V, a.scale * kLog2e, red);
-      r = row_result(s, xy, a.scale);
-      const PolicyToken q = policy_token(p, k, t, r.logp, r.ent);
-      term = f32x4_t{w * q.loss, w * q.k, w * q.bound, w * r.ent};
-      g = w * q.dlogp;
-      live = r.m != -INFINITY;
+  const int32_t V = int32_t(a.V);
+  const int64_t t = row_index();
+  if (t >= a.T) return;
+  const int64_t y = a.labels[t];
+  const float w = k.weight ? k.weight[t] : 1.0f;
+  const char *row = row_at<BF16>(a.x, t * a.ld);
+  char *out = row_at<BF16>(dx, t * ldd);
+  RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4_t term = {0.0f, 0.0f, 0.0f, 0.0f};
+  bool some = false;
+  if (y >= 0 && y < V && w != 0.0f) {
+    Held<BF16, threads, NG> h;
+    r = row_stat<true, ONE>(h, row, V, int32_t(y), a.scale, red);
+    const PolicyToken q = policy_token(p, r.logp, r.ent, k.adv ? k.adv[t] : 1.0f,
+                                       k.old ? r.logp - k.old[t] : 0.0f, k.ref,
+                                       k.ref ? k.ref[t] : 0.0f);
+    term = f32x4_t{w * q.loss, w * q.k, w * q.bound, w * r.ent};
+    const float g = w * q.dlogp, gh = -p.ent * w;
+    some = r.m != -INFINITY && (g != 0.0f || gh != 0.0f);
+    if (some) {
+      const GradCoef kc = grad_coef(a.scale, g, gh, r.ent, r.z);
+      row_grad<ENT, ONE>(h, row, out, V, int32_t(y), r.m, a.scale * kLog2e, kc);
     }
-    grad_row<BF16, threads>(row, dx, t * ldd, a.V, y, a.scale, r.m, r.z, g, -p.ent * w, r.ent,
-                            live);
-    if (threadIdx.x == 0) {
-      reinterpret_cast<f32x4_t *>(terms)[t] = term;
-      if (logp) logp[t] = r.logp;
-    }
+  }
+  if (!some) zero_row<BF16, threads>(out, V);
+  if (threadIdx.x == 0) {
+    reinterpret_cast<f32x4_t *>(terms)[t] = term;
+    if (logp) logp[t] = r.logp;
   }
 }
 
-__global__ __launch_bounds__(1024) void sum4_kernel(const float *terms, int64_t n, float *out) {
-  __shared__ double red[16];
-  double s[4] = {};
-  for (int64_t i = threadIdx.x; i < n; i += 1024) {
-    const f32x4_t v = reinterpret_cast<const f32x4_t *>(terms)[i];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] += v[j];
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const double v = block_sum<1024>(s[j], red);
-    if (threadIdx.x == 0) out[j] = float(v);
-  }
+dim3 row_grid(int64_t T, int64_t segments = 1) {
+  return dim3(unsigned(segments), unsigned(min64(T, kRowsY)),
+              unsigned((T + kRowsY - 1) / kRowsY));
+}
+
+// Lanes and groups to a row.  A lane wants 4 to 8 groups of 8 words in flight,
+// and every wavefront of a row repeats the row's last reductions, so a row
+// takes the fewest wavefronts that hold it so.  Measured, us (V, T; bf16):
+//   V = 4000, T = 16384:  64 x 4 21.4   128 x 4 23.9   128 x 8 35.3
+//   V = 8000, T = 8192:   128 x 8 21.7  64 x 4 22.4    256 x 4 22.7
+//   V = 16000, T = 8192:  256 x 8 38.6  64 x 8 43.4    512 x 4 43.1
+//   V = 32000, T = 4096:  512 x 8 37.3  256 x 8 41.9   1024 x 4 46.5
+template <bool BF16, bool ENT>
+void logp_fwd(const LogitRows &a, float *logp, float *stats, float *entropy, hipStream_t s) {
+#define ROWS(threads, NG)                                                                     \
+  hipLaunchKernelGGL((logp_fwd_kernel<BF16, ENT, threads, NG>), row_grid(a.T), dim3(threads), \
+                     0, s, a, logp, stats, entropy)
+  if (a.V <= 4096) ROWS(64, 4);
+  else if (a.V <= 8192) ROWS(128, 8);
+  else if (a.V <= 16384) ROWS(256, 8);
+  else ROWS(512, 8);
+#undef ROWS
+}
+
+// 32 bytes of a row to a lane: bf16, T = 4096, V = 32000: 2 groups 80.0 us, one
+// 90.7, four 89.1; fp32, T = 509, V = 50001: 1 group 40.1, two 41.7, four 44.4.
+template <bool BF16, bool ENT>
+void logp_bwd(const LogitRows &a, const float *stats, const float *entropy, const float *g,
+              const float *g_entropy, void *dx, int64_t ldd, hipStream_t s) {
+  constexpr int threads = 256, NG = BF16 ? 2 : 1;
+  const int64_t segments = (a.V + threads * 8 * NG - 1) / (threads * 8 * NG);
+  hipLaunchKernelGGL((logp_bwd_kernel<BF16, ENT, threads, NG>), row_grid(a.T, segments),
+                     dim3(threads), 0, s, a, stats, entropy, g, g_entropy, dx, ldd);
+}
+
+// As in logp_fwd, but the row has to stay in registers, up to 65536 words
+// (1024 lanes of 8 groups).  Measured, us (bf16, a quarter of the rows dead):
+//   V = 4000, T = 16384:  128 x 4 49.5  64 x 8 52.4   256 x 2 57.2
+//   V = 8000, T = 8192:   256 x 4 47.9  128 x 8 51.5  64 x 16 53.7
+//   V = 16000, T = 8192:  512 x 4 89.0  256 x 8 89.7  128 x 16 94.6
+//   V = 32000, T = 4096:  512 x 8 93.2  256 x 16 95.7 1024 x 4 100.2
+//   V = 60000, T = 1024:  1024 x 8 54.4, read twice by 1024 x 4 58.9
+template <bool BF16, bool ENT>
+void policy_logits(const LogitRows &a, const PolicyTokens &t, const PolicyParams &p, float *terms,
+                   float *logp, void *dx, int64_t ldd, hipStream_t s) {
+#define ROWS(ONE, threads, NG)                                                            \
+  hipLaunchKernelGGL((policy_logits_kernel<BF16, ENT, ONE, threads, NG>), row_grid(a.T), \
+                     dim3(threads), 0, s, a, t, p, terms, logp, dx, ldd)
+  if (a.V <= 2048) ROWS(true, 64, 4);
+  else if (a.V <= 4096) ROWS(true, 128, 4);
+  else if (a.V <= 8192) ROWS(true, 256, 4);
+  else if (a.V <= 16384) ROWS(true, 512, 4);
+  else if (a.V <= 32768) ROWS(true, 512, 8);
+  else if (a.V <= 65536) ROWS(true, 1024, 8);
+  else ROWS(false, 1024, 8);
+#undef ROWS
 }
 
 }  // namespace
 
 hipError_t launch_logp_fwd(const LogitRows &a, float *logp, float *stats, float *entropy,
                            hipStream_t s) {
-  const dim3 grid{unsigned(min64(a.T, kMaxBlocks))};
-  if (a.bf16)
-    hipLaunchKernelGGL((logp_fwd_kernel<true, 256>), grid, dim3(256), 0, s, a, logp, stats,
-                       entropy);
-  else
-    hipLaunchKernelGGL((logp_fwd_kernel<false, 256>), grid, dim3(256), 0, s, a, logp, stats,
-                       entropy);
+#define GO(B) (entropy ? logp_fwd<B, true>(a, logp, stats, entropy, s) \
+                       : logp_fwd<B, false>(a, logp, stats, entropy, s))
+  a.bf16 ? GO(true) : GO(false);
+#undef GO
   return hipGetLastError();
 }
 
 hipError_t launch_logp_bwd(const LogitRows &a, const float *stats, const float *entropy,
                            const float *g, const float *g_entropy, void *dx, int64_t ldd,
                            hipStream_t s) {
-  const dim3 grid{unsigned(min64(a.T, kMaxBlocks))};
-  if (a.bf16)
-    hipLaunchKernelGGL((logp_bwd_kernel<true, 256>), grid, dim3(256), 0, s, a, stats, entropy, g,
-                       g_entropy, dx, ldd);
-  else
-    hipLaunchKernelGGL((logp_bwd_kernel<false, 256>), grid, dim3(256), 0, s, a, stats, entropy, g,
-                       g_entropy, dx, ldd);
+#define GO(B) (entropy ? logp_bwd<B, true>(a, stats, entropy, g, g_entropy, dx, ldd, s) \
+                       : logp_bwd<B, false>(a, stats, entropy, g, g_entropy, dx, ldd, s))
+  a.bf16 ? GO(true) : GO(false);
+#undef GO
   return hipGetLastError();
 }
 
 hipError_t launch_policy_logits(const LogitRows &a, const PolicyTokens &t,
                                 const PolicyParams &p, float *terms, float *logp, void *dx,
                                 int64_t ldd, hipStream_t s) {
-  const dim3 grid{unsigned(min64(a.T, kMaxBlocks))};
-  if (a.bf16)
-    hipLaunchKernelGGL((policy_logits_kernel<true, 256>), grid, dim3(256), 0, s, a, t, p, terms,
-                       logp, dx, ldd);
-  else
-    hipLaunchKernelGGL((policy_logits_kernel<false, 256>), grid, dim3(256), 0, s, a, t, p, terms,
-                       logp, dx, ldd);
-  return hipGetLastError();
-}
-
-hipError_t launch_sum4(const float *terms, int64_t n, float *out, hipStream_t s) {
-  hipLaunchKernelGGL(sum4_kernel, dim3(1), dim3(1024), 0, s, terms, n, out);
+#define GO(B) (p.ent != 0.0f ? policy_logits<B, true>(a, t, p, terms, logp, dx, ldd, s) \
+                             : policy_logits<B, false>(a, t, p, terms, logp, dx, ldd, s))
+  a.bf16 ? GO(true) : GO(false);
+#undef GO
   return hipGetLastError();
 }
 

@@ -11,18 +11,17 @@ struct PolicyToken {
   float dlogp;            // d loss / d logp (that of the entropy is -ent)
 };
 
-// One token of the objective (qlora_policy_loss in qlora.h has the formulas).
-// The branch is chosen on d = logp - old against rounded logs of the bounds:
+// One token of the objective (qlora_policy_loss in qlora.h has the formulas),
+// d = logp - old or 0.  The branch is chosen on d against rounded logs of the bounds:
 // d is one fp32 subtraction, so the choice does not hang on how exp rounds.
 // k = expm1(q) - q keeps its digits where the two policies nearly agree.
-__device__ __forceinline__ PolicyToken policy_token(const PolicyParams &p, const PolicyTokens &k,
-                                                    int64_t i, float logp, float ent) {
-  const float adv = k.adv ? k.adv[i] : 1.0f;
+__device__ __forceinline__ PolicyToken policy_token(const PolicyParams &p, float logp, float ent,
+                                                    float adv, float d, bool has_ref,
+                                                    float ref) {
   PolicyToken t;
   float f = adv * logp, df = adv;
   t.bound = 0.0f;
   if (p.clip) {
-    const float d = k.old ? logp - k.old[i] : 0.0f;
     df = expf(d) * adv;
     f = df;
     if (adv > 0.0f && d > p.log_hi) { f = p.hi * adv; t.bound = 1.0f; }
@@ -33,8 +32,8 @@ __device__ __forceinline__ PolicyToken policy_token(const PolicyParams &p, const
   t.loss = -f;
   t.dlogp = -df;
   t.k = 0.0f;
-  if (k.ref) {
-    const float q = k.ref[i] - logp, em = expm1f(q);
+  if (has_ref) {
+    const float q = ref - logp, em = expm1f(q);
     t.k = em - q;
     t.loss += p.kl * t.k;
     t.dlogp -= p.kl * em;
@@ -43,21 +42,75 @@ __device__ __forceinline__ PolicyToken policy_token(const PolicyParams &p, const
   return t;
 }
 
-// Sum over a workgroup of `threads` (a multiple of 64) in a fixed order; the
-// result is valid in every thread.  red: threads / 64 doubles of LDS, free
-// again after the next barrier.
-template <int threads>
-__device__ __forceinline__ double block_sum(double v, double *red) {
+// Sum (maximum) over a wavefront's 64 lanes through data-parallel moves within
+// rows of 16 lanes and broadcasts between rows: six dependent vector
+// instructions, no LDS.  The total is in lane 63 and is returned as a scalar.
+template <int ctrl, int rows>
+__device__ __forceinline__ float dpp(float fill, float v) {
+  return __uint_as_float(uint32_t(__builtin_amdgcn_update_dpp(
+      int(__float_as_uint(fill)), int(__float_as_uint(v)), ctrl, rows, 0xf, false)));
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(v)), 63)));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0x111, 0xf>(0.0f, v);   // from 1, 2, 4 and 8 lanes below in the row
+  v += dpp<0x112, 0xf>(0.0f, v);
+  v += dpp<0x114, 0xf>(0.0f, v);
+  v += dpp<0x118, 0xf>(0.0f, v);
+  v += dpp<0x142, 0xa>(0.0f, v);   // row 0 to row 1, row 2 to row 3
+  v += dpp<0x143, 0xc>(0.0f, v);   // rows 0 and 1 to rows 2 and 3
+  return last_lane(v);
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp<0x111, 0xf>(-INFINITY, v));
+  v = fmaxf(v, dpp<0x112, 0xf>(-INFINITY, v));
+  v = fmaxf(v, dpp<0x114, 0xf>(-INFINITY, v));
+  v = fmaxf(v, dpp<0x118, 0xf>(-INFINITY, v));
+  v = fmaxf(v, dpp<0x142, 0xa>(-INFINITY, v));
+  v = fmaxf(v, dpp<0x143, 0xc>(-INFINITY, v));
+  return last_lane(v);
+}
+
+template <int ctrl, int rows>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), ctrl, rows, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(u >> 32)), ctrl, rows, 0xf, false);
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += dpp<0x111, 0xf>(v);
+  v += dpp<0x112, 0xf>(v);
+  v += dpp<0x114, 0xf>(v);
+  v += dpp<0x118, 0xf>(v);
+  v += dpp<0x142, 0xa>(v);
+  v += dpp<0x143, 0xc>(v);
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(int(uint32_t(u)), 63);
+  const uint32_t hi = __builtin_amdgcn_readlane(int(uint32_t(u >> 32)), 63);
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+
+// Sums of N values over a workgroup of `threads`, in every lane, in an order
+// that `threads` alone fixes.  red: N * threads / 64 doubles of LDS, used by
+// this call alone.
+template <int N, int threads>
+__device__ __forceinline__ void block_sums(double (&v)[N], double *red) {
+  constexpr int W = threads / 64;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  const int wave = threadIdx.x / 64;
-  __syncthreads();
-  if (threadIdx.x % 64 == 0) red[wave] = v;
-  __syncthreads();
-  double s = 0.0;
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if (W == 1) return;
+  const int lane = threadIdx.x % 64;
 #pragma unroll
-  for (int w = 0; w < threads / 64; ++w) s += red[w];
-  return s;
+  for (int i = 0; i < N; ++i)
+    if (lane == i) red[i * W + threadIdx.x / 64] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = lane < W ? red[i * W + lane] : 0.0;
+    v[i] = wave_sum(v[i]);
+  }
 }
 
 }  // namespace qlora

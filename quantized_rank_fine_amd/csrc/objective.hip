@@ -9,52 +9,93 @@ namespace {
 
 // ------------------------------------------------------------ policy loss
 
+// Tokens of one workgroup, four to a lane: up to kPolicyLone the tokens are
+// one workgroup's and its sums are the result; past that there is a second
+// launch.
 constexpr int kPolicyThreads = 256;
-constexpr int64_t kPolicyChunk = 4096;   // tokens of one workgroup
+constexpr int64_t kPolicyLone = 4096;
 
-__global__ __launch_bounds__(kPolicyThreads) void policy_kernel(
-    const float *logp, const float *entropy, int64_t T, PolicyTokens k, PolicyParams p, float *out,
-    float *dlogp, float *dentropy, double *partial) {
-  __shared__ double red[kPolicyThreads / 64];
-  double s[4] = {};
-  const int64_t first = int64_t(blockIdx.x) * kPolicyChunk;
-  const int64_t last = min64(first + kPolicyChunk, T);
-  for (int64_t i = first + threadIdx.x; i < last; i += kPolicyThreads) {
-    const float w = k.weight ? k.weight[i] : 1.0f;
-    float g = 0.0f, gh = 0.0f;
-    if (w != 0.0f) {
-      const float h = entropy ? entropy[i] : 0.0f;
-      const PolicyToken t = policy_token(p, k, i, logp[i], h);
-      g = w * t.dlogp;
-      gh = -w * p.ent;
-      s[0] += w * t.loss; s[1] += w * t.k; s[2] += w * t.bound; s[3] += w * h;
-    }
-    dlogp[i] = g;
-    if (dentropy) dentropy[i] = gh;
-  }
+__device__ __forceinline__ void put_sums(const double (&s)[4], float *out, double *partial) {
+  if (threadIdx.x != 0) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const double v = block_sum<kPolicyThreads>(s[j], red);
-    if (threadIdx.x == 0) {
-      if (partial) partial[int64_t(blockIdx.x) * 4 + j] = v;
-      else out[j] = float(v);
-    }
+    if (partial) partial[int64_t(blockIdx.x) * 4 + j] = s[j];
+    else out[j] = float(s[j]);
   }
 }
 
-__global__ __launch_bounds__(1024) void policy_sum_kernel(const double *partial, int64_t n,
-                                                          float *out) {
-  __shared__ double red[16];
-  double s[4] = {};
-  for (int64_t i = threadIdx.x; i < n; i += 1024)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] += partial[i * 4 + j];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const double v = block_sum<1024>(s[j], red);
-    if (threadIdx.x == 0) out[j] = float(v);
+// n <= 4 values from `i` on, or `fill` where there is no array.
+__device__ __forceinline__ f32x4_t take4(const float *v, int64_t i, int n, float fill) {
+  f32x4_t x = {fill, fill, fill, fill};
+  if (!v) return x;
+  if (n == 4) {
+    __builtin_memcpy(&x, v + i, 16);
+  } else {
+    for (int j = 0; j < n; ++j) x[j] = v[i + j];
+  }
+  return x;
+}
+
+__device__ __forceinline__ void give4(float *v, int64_t i, int n, const f32x4_t &x) {
+  if (n == 4) {
+    __builtin_memcpy(v + i, &x, 16);
+  } else {
+    for (int j = 0; j < n; ++j) v[i + j] = x[j];
   }
 }
+
+template <int threads>
+__global__ __launch_bounds__(threads) void policy_kernel(const float *logp, const float *entropy,
+                                                         int64_t T, PolicyTokens k,
+                                                         PolicyParams p, float *out, float *dlogp,
+                                                         float *dentropy, double *partial) {
+  __shared__ double red[4 * threads / 64];
+  double s[4] = {};
+  const int64_t step = int64_t(gridDim.x) * threads * 4;
+  for (int64_t i = (int64_t(blockIdx.x) * threads + threadIdx.x) * 4; i < T; i += step) {
+    const int n = int(min64(T - i, 4));
+    const f32x4_t w = take4(k.weight, i, n, 1.0f), lp = take4(logp, i, n, 0.0f);
+    const f32x4_t h = take4(entropy, i, n, 0.0f), adv = take4(k.adv, i, n, 1.0f);
+    const f32x4_t old = take4(k.old, i, n, 0.0f), ref = take4(k.ref, i, n, 0.0f);
+    f32x4_t g, gh;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool on = j < n && w[j] != 0.0f;
+      const PolicyToken t = policy_token(p, lp[j], h[j], adv[j], k.old ? lp[j] - old[j] : 0.0f,
+                                         k.ref, ref[j]);
+      g[j] = on ? w[j] * t.dlogp : 0.0f;
+      gh[j] = on ? -w[j] * p.ent : 0.0f;
+      s[0] += on ? w[j] * t.loss : 0.0f;
+      s[1] += on ? w[j] * t.k : 0.0f;
+      s[2] += on ? w[j] * t.bound : 0.0f;
+      s[3] += on ? w[j] * h[j] : 0.0f;
+    }
+    give4(dlogp, i, n, g);
+    if (dentropy) give4(dentropy, i, n, gh);
+  }
+  block_sums<4, threads>(s, red);
+  put_sums(s, out, partial);
+}
+
+// Column sums of v [n x 4].
+template <class F>
+__global__ __launch_bounds__(1024) void sum4_kernel(const F *v, int64_t n, float *out,
+                                                    double *partial) {
+  __shared__ double red[4 * 16];
+  double s[4] = {};
+  const int64_t step = int64_t(gridDim.x) * 1024;
+#pragma unroll 8
+  for (int64_t i = int64_t(blockIdx.x) * 1024 + threadIdx.x; i < n; i += step) {
+    F x[4];
+    __builtin_memcpy(x, v + 4 * i, sizeof(x));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] += double(x[j]);
+  }
+  block_sums<4, 1024>(s, red);
+  put_sums(s, out, partial);
+}
+
+constexpr int64_t kTermsLone = 16384;   // terms that one workgroup adds up
 
 // -------------------------------------------------------- preference loss
 //
@@ -62,7 +103,14 @@ __global__ __launch_bounds__(1024) void policy_sum_kernel(const double *partial,
 // h = S_chosen - S_rejected, dl / dh gives every counted token of the chosen
 // answer dl/dh / P (/ its number), of the rejected one the opposite.
 
-constexpr int kPrefThreads = 256;
+// A unit of work is one wavefront's: a slice of one answer.  The slices' sums
+// and counts ("partials") join the two passes.  Few tokens: one workgroup holds
+// the partials in LDS between its two passes.  Many: two launches, partials in
+// the workspace.
+constexpr int kPrefThreads = 256;        // of the two launches
+constexpr int64_t kPrefLoneTokens = 8192, kPrefLonePairs = 128;
+constexpr int64_t kPrefSlice = 1024;     // tokens of a slice, four quads to a lane
+constexpr int64_t kPrefUnits = 16384;    // slices, when answers are cut at all
 
 struct PairLoss {
   float loss, dh;
@@ -83,139 +131,260 @@ __device__ __forceinline__ PairLoss pair_loss(const PrefParams &p, float h) {
           p.beta * (p.smoothing * (1.0f - neg) - (1.0f - p.smoothing) * neg)};
 }
 
-struct Answer {
+struct PrefArgs {
+  const float *logp, *ref;
+  const uint8_t *mask;
+  const int64_t *cu;
+  int64_t P, T;
+  PrefParams p;
+  float *loss, *rewards, *dlogp;
+};
+
+struct Span {
   int64_t first, last;
 };
 
-__device__ __forceinline__ Answer answer(const int64_t *cu, int64_t i, int64_t T) {
-  const int64_t a = cu[i], b = cu[i + 1];
-  const int64_t first = a < 0 ? 0 : min64(a, T);
-  return {first, b < first ? first : min64(b, T)};
+__device__ __forceinline__ Span answer(const PrefArgs &a, int64_t i) {
+  const int64_t lo = a.cu[i], hi = a.cu[i + 1];
+  const int64_t first = lo < 0 ? 0 : min64(lo, a.T);
+  return {first, hi < first ? first : min64(hi, a.T)};
 }
 
-// Sum and number of one thread's counted tokens of [first, last).
-__device__ __forceinline__ void pref_add(const float *logp, const float *ref, const uint8_t *mask,
-                                         int64_t first, int64_t last, int step, int at, double &s,
-                                         double &n) {
-  for (int64_t t = first + at; t < last; t += step)
-    if (!mask || mask[t]) {
-      s += ref ? double(logp[t] - ref[t]) : double(logp[t]);
-      n += 1.0;
+// Slice j of n of an answer, its inner ends on multiples of four tokens.
+__device__ __forceinline__ Span slice(const Span &s, int64_t j, int64_t n) {
+  const int64_t base = s.first & ~int64_t(3);
+  const int64_t each = ((s.last - base + n - 1) / n + 3) & ~int64_t(3);
+  const int64_t lo = base + j * each;
+  const Span r = {lo < s.first ? s.first : lo, min64(lo + each, s.last)};
+  return r.first < r.last ? r : Span{s.last, s.last};
+}
+
+struct Partial {
+  double sum, count;
+};
+
+// Which of tokens t .. t + 3 count, bit by bit.
+__device__ __forceinline__ uint32_t counted4(const PrefArgs &a, const Span &s, int64_t t) {
+  uint32_t m = 0x01010101u;
+  if (a.mask) {
+    if (t + 4 <= a.T) {
+      __builtin_memcpy(&m, a.mask + t, 4);
+    } else {
+      m = 0;
+      for (int j = 0; t + j < a.T; ++j) m |= uint32_t(a.mask[t + j]) << (8 * j);
     }
+  }
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if ((m >> (8 * j) & 0xffu) && t + j >= s.first && t + j < s.last) bits |= 1u << j;
+  return bits;
 }
 
-__global__ __launch_bounds__(kPrefThreads) void pref_sum_kernel(const float *logp,
-                                                                const float *ref,
-                                                                const uint8_t *mask,
-                                                                const int64_t *cu, int64_t T,
-                                                                double *partial) {
-  __shared__ double red[kPrefThreads / 64];
-  const int64_t i = blockIdx.x, j = blockIdx.y, n = gridDim.y;
-  const Answer a = answer(cu, i, T);
-  const int64_t len = a.last - a.first, each = (len + n - 1) / n;
-  const int64_t first = a.first + min64(j * each, len), last = min64(first + each, a.last);
-  double s = 0.0, c = 0.0;
-  pref_add(logp, ref, mask, first, last, kPrefThreads, threadIdx.x, s, c);
-  s = block_sum<kPrefThreads>(s, red);
-  c = block_sum<kPrefThreads>(c, red);
-  if (threadIdx.x == 0) {
-    partial[(i * n + j) * 2] = s;
-    partial[(i * n + j) * 2 + 1] = c;
+// One wavefront's sum over a slice: quads of tokens, neighbours' tokens in the
+// first and last quad left out.
+__device__ __forceinline__ Partial slice_sum(const PrefArgs &a, const Span &s) {
+  double sum = 0.0;
+  int count = 0;
+#pragma unroll 4
+  for (int64_t t = (s.first & ~int64_t(3)) + 4 * (threadIdx.x % 64); t < s.last; t += 256) {
+    const uint32_t bits = counted4(a, s, t);
+    f32x4_t lp = {0.0f, 0.0f, 0.0f, 0.0f}, rf = lp;
+    if (t + 4 <= a.T) {
+      __builtin_memcpy(&lp, a.logp + t, 16);
+      if (a.ref) __builtin_memcpy(&rf, a.ref + t, 16);
+    } else {
+      for (int j = 0; t + j < a.T; ++j) {
+        lp[j] = a.logp[t + j];
+        if (a.ref) rf[j] = a.ref[t + j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum += (bits >> j & 1u) ? lp[j] - rf[j] : 0.0f;
+    count += __builtin_popcount(bits);
+  }
+  return {wave_sum(sum), wave_sum(double(count))};
+}
+
+// dlogp of a slice: g where a token counts, 0 elsewhere in the answer.
+__device__ __forceinline__ void slice_grad(const PrefArgs &a, const Span &s, float g) {
+#pragma unroll 4
+  for (int64_t t = (s.first & ~int64_t(3)) + 4 * (threadIdx.x % 64); t < s.last; t += 256) {
+    const uint32_t bits = counted4(a, s, t);
+    f32x4_t d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = (bits >> j & 1u) ? g : 0.0f;
+    if (t >= s.first && t + 4 <= s.last) {
+      __builtin_memcpy(a.dlogp + t, &d, 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (t + j >= s.first && t + j < s.last) a.dlogp[t + j] = d[j];
+    }
   }
 }
 
-// S and the number of answer i from its partials.
-__device__ __forceinline__ void pref_total(const PrefParams &p, const double *partial, int64_t i,
-                                           int n, float &S, float &count) {
-  double s = 0.0, c = 0.0;
-  for (int j = 0; j < n; ++j) {
-    s += partial[(i * n + j) * 2];
-    c += partial[(i * n + j) * 2 + 1];
+// An answer's S and count from its n partials; lane `at` of `lanes` (a power of
+// two, neighbours in a wavefront) adds every lanes-th of them.
+__device__ __forceinline__ Partial total(const PrefArgs &a, const Partial *partial, int64_t i,
+                                         int n, int at, int lanes) {
+  Partial r = {0.0, 0.0};
+  for (int j = at; j < n; j += lanes) {
+    r.sum += partial[i * n + j].sum;
+    r.count += partial[i * n + j].count;
   }
-  if (p.average) s = c > 0.0 ? s / c : 0.0;
-  S = float(s);
-  count = float(c);
+  for (int o = lanes / 2; o > 0; o >>= 1) {
+    r.sum += __shfl_xor(r.sum, o);
+    r.count += __shfl_xor(r.count, o);
+  }
+  if (a.p.average) r.sum = r.count > 0.0 ? r.sum / r.count : 0.0;
+  return r;
 }
 
-// Zero for this workgroup's share of the tokens outside every answer.
-__device__ __forceinline__ void pref_outside(const int64_t *cu, int64_t P, int64_t T,
-                                             float *dlogp, int64_t b, int64_t blocks) {
-  const int64_t lo = answer(cu, 0, T).first, hi = answer(cu, 2 * P - 1, T).last;
-  const int64_t step = blocks * kPrefThreads;
-  for (int64_t t = b * kPrefThreads + threadIdx.x; t < lo; t += step) dlogp[t] = 0.0f;
-  for (int64_t t = hi + b * kPrefThreads + threadIdx.x; t < T; t += step) dlogp[t] = 0.0f;
+__device__ __forceinline__ int lanes_for(int n) {
+  return n <= 1 ? 1 : n >= 33 ? 64 : 1 << (32 - __builtin_clz(n - 1));
 }
 
-// Workgroup (i, j) writes slice j of answer i's gradient; the last column's
-// extra workgroups (j = n) hold the mean loss and the rewards.
-__global__ __launch_bounds__(kPrefThreads) void pref_grad_kernel(
-    const uint8_t *mask, const int64_t *cu, int64_t P, int64_t T, PrefParams p,
-    const double *partial, int n, float *loss, float *rewards, float *dlogp) {
+// Unit (i, j)'s gradient; slice 0 also writes the answer's reward.
+__device__ __forceinline__ void unit_grad(const PrefArgs &a, const Partial *partial, int64_t i,
+                                          int j, int n) {
+  const int lane = threadIdx.x % 64, lanes = lanes_for(n);
+  const int64_t k = i < a.P ? i : i - a.P;
+  const Partial c = total(a, partial, k, n, lane % lanes, lanes);
+  const Partial r = total(a, partial, a.P + k, n, lane % lanes, lanes);
+  const Partial &own = i < a.P ? c : r;
+  float g = pair_loss(a.p, float(c.sum) - float(r.sum)).dh / float(a.P);
+  if (i >= a.P) g = -g;
+  if (a.p.average && own.count > 0.0) g /= float(own.count);
+  if (j == 0 && lane == 0) a.rewards[i] = a.p.beta * float(own.sum);
+  slice_grad(a, slice(answer(a, i), j, n), g);
+}
+
+// The mean loss, by one workgroup: a pair to `lanes` lanes.
+template <int threads>
+__device__ __forceinline__ void mean_loss(const PrefArgs &a, const Partial *partial, int n,
+                                          double *red) {
+  const int lanes = lanes_for(n), at = threadIdx.x % lanes;
+  double sum[1] = {};
+  for (int64_t first = 0; first < a.P; first += threads / lanes) {
+    const int64_t k = first + threadIdx.x / lanes;
+    const int64_t kk = k < a.P ? k : a.P - 1;     // every lane takes part in the shuffles
+    const Partial c = total(a, partial, kk, n, at, lanes);
+    const Partial r = total(a, partial, a.P + kk, n, at, lanes);
+    if (k < a.P && at == 0) sum[0] += pair_loss(a.p, float(c.sum) - float(r.sum)).loss;
+  }
+  block_sums<1, threads>(sum, red);
+  if (threadIdx.x == 0) a.loss[0] = float(sum[0] / double(a.P));
+}
+
+// Zeros for the tokens outside every answer, by thread `at` of `all`.
+__device__ __forceinline__ void zero_outside(const PrefArgs &a, int64_t at, int64_t all) {
+  const int64_t lo = answer(a, 0).first, hi = answer(a, 2 * a.P - 1).last;
+  for (int64_t t = at; t < lo; t += all) a.dlogp[t] = 0.0f;
+  for (int64_t t = hi + at; t < a.T; t += all) a.dlogp[t] = 0.0f;
+}
+
+__global__ __launch_bounds__(1024) void pref_lone_kernel(PrefArgs a, int n) {
+  __shared__ Partial partial[2 * kPrefLonePairs];
+  __shared__ double red[16];
+  const int units = int(2 * a.P) * n, wave = threadIdx.x / 64;
+  for (int u = wave; u < units; u += 16) {
+    const Partial s = slice_sum(a, slice(answer(a, u / n), u % n, n));
+    if (threadIdx.x % 64 == 0) partial[u] = s;
+  }
+  __syncthreads();
+  for (int u = wave; u < units; u += 16) unit_grad(a, partial, u / n, u % n, n);
+  zero_outside(a, threadIdx.x, 1024);
+  mean_loss<1024>(a, partial, n, red);
+}
+
+__global__ __launch_bounds__(kPrefThreads) void pref_sum_kernel(PrefArgs a, int n, int64_t units,
+                                                                Partial *partial) {
+  const int64_t u = int64_t(blockIdx.x) * (kPrefThreads / 64) + threadIdx.x / 64;
+  if (u >= units) return;
+  const Partial s = slice_sum(a, slice(answer(a, u / n), u % n, n));
+  if (threadIdx.x % 64 == 0) partial[u] = s;
+}
+
+// The last workgroup takes the mean loss.
+__global__ __launch_bounds__(kPrefThreads) void pref_grad_kernel(PrefArgs a, int n, int64_t units,
+                                                                 const Partial *partial) {
   __shared__ double red[kPrefThreads / 64];
-  const int64_t i = blockIdx.x, j = blockIdx.y;
-  if (j == n) {
-    if (i != 0) return;
-    double sum = 0.0;
-    for (int64_t k = threadIdx.x; k < P; k += kPrefThreads) {
-      float a, b, ca, cb;
-      pref_total(p, partial, k, n, a, ca);
-      pref_total(p, partial, P + k, n, b, cb);
-      rewards[k] = p.beta * a;
-      rewards[P + k] = p.beta * b;
-      sum += pair_loss(p, a - b).loss;
-    }
-    sum = block_sum<kPrefThreads>(sum, red);
-    if (threadIdx.x == 0) loss[0] = float(sum / double(P));
+  const int64_t work = int64_t(gridDim.x) - 1;
+  if (blockIdx.x == work) {
+    mean_loss<kPrefThreads>(a, partial, n, red);
     return;
   }
-  pref_outside(cu, P, T, dlogp, i * n + j, 2 * P * n);
-  const int64_t k = i < P ? i : i - P;
-  float a, b, ca, cb;
-  pref_total(p, partial, k, n, a, ca);
-  pref_total(p, partial, P + k, n, b, cb);
-  float g = pair_loss(p, a - b).dh / float(P);
-  if (i >= P) g = -g;
-  const float count = i < P ? ca : cb;
-  if (p.average && count > 0.0f) g /= count;
-  const Answer q = answer(cu, i, T);
-  const int64_t len = q.last - q.first, each = (len + n - 1) / n;
-  const int64_t first = q.first + min64(j * each, len), last = min64(first + each, q.last);
-  for (int64_t t = first + threadIdx.x; t < last; t += kPrefThreads)
-    dlogp[t] = !mask || mask[t] ? g : 0.0f;
+  const int64_t u = int64_t(blockIdx.x) * (kPrefThreads / 64) + threadIdx.x / 64;
+  if (u < units) unit_grad(a, partial, u / n, int(u % n), n);
+  zero_outside(a, int64_t(blockIdx.x) * kPrefThreads + threadIdx.x, work * kPrefThreads);
 }
 
 }  // namespace
 
-int64_t policy_blocks(int64_t T) { return T > 0 ? (T + kPolicyChunk - 1) / kPolicyChunk : 1; }
+int64_t policy_blocks(int64_t T) {
+  return T <= kPolicyLone ? 1 : min64((T + 4 * kPolicyThreads - 1) / (4 * kPolicyThreads), 2048);
+}
 
 hipError_t launch_policy(const float *logp, const float *entropy, int64_t T,
                          const PolicyTokens &t, const PolicyParams &p, float *out, float *dlogp,
                          float *dentropy, double *partial, hipStream_t s) {
   const int64_t n = policy_blocks(T);
-  hipLaunchKernelGGL(policy_kernel, dim3(unsigned(n)), dim3(kPolicyThreads), 0, s, logp, entropy,
-                     T, t, p, out, dlogp, dentropy, n > 1 ? partial : nullptr);
-  if (n > 1)
-    hipLaunchKernelGGL(policy_sum_kernel, dim3(1), dim3(1024), 0, s, partial, n, out);
+  if (n == 1) {
+    hipLaunchKernelGGL((policy_kernel<1024>), dim3(1), dim3(1024), 0, s, logp, entropy, T, t, p,
+                       out, dlogp, dentropy, nullptr);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((policy_kernel<kPolicyThreads>), dim3(unsigned(n)), dim3(kPolicyThreads), 0,
+                     s, logp, entropy, T, t, p, out, dlogp, dentropy, partial);
+  hipLaunchKernelGGL((sum4_kernel<double>), dim3(1), dim3(1024), 0, s, partial, n, out, nullptr);
   return hipGetLastError();
 }
 
-// Slices of an answer: enough workgroups to fill the chip for a few long
-// answers, and at least a few thousand tokens each on average.
+int64_t terms_blocks(int64_t n) {
+  return n <= kTermsLone ? 1 : min64((n + kTermsLone - 1) / kTermsLone, 1024);
+}
+
+hipError_t launch_sum_terms(const float *terms, int64_t n, float *out, double *partial,
+                            hipStream_t s) {
+  const int64_t b = terms_blocks(n);
+  hipLaunchKernelGGL((sum4_kernel<float>), dim3(unsigned(b)), dim3(1024), 0, s, terms, n, out,
+                     b > 1 ? partial : nullptr);
+  if (b > 1)
+    hipLaunchKernelGGL((sum4_kernel<double>), dim3(1), dim3(1024), 0, s, partial, b, out, nullptr);
+  return hipGetLastError();
+}
+
+namespace {
+
+bool pref_lone(int64_t P, int64_t T) { return T <= kPrefLoneTokens && P <= kPrefLonePairs; }
+
+}  // namespace
+
 int64_t pref_splits(int64_t P, int64_t T) {
-  const int64_t by_size = T / (2 * P) / 2048, by_chip = 1024 / (2 * P);
-  const int64_t n = by_size < by_chip ? by_size : by_chip;
+  if (pref_lone(P, T)) return 0;
+  const int64_t by_size = (T / (2 * P) + kPrefSlice - 1) / kPrefSlice, most = kPrefUnits / (2 * P);
+  const int64_t n = min64(by_size, most);
   return n < 1 ? 1 : n;
 }
 
 hipError_t launch_pref(const float *logp, const float *ref, const uint8_t *mask,
                        const int64_t *cu, int64_t P, int64_t T, const PrefParams &p, float *loss,
                        float *rewards, float *dlogp, double *partial, hipStream_t s) {
-  const int64_t n = pref_splits(P, T);
-  hipLaunchKernelGGL(pref_sum_kernel, dim3(unsigned(2 * P), unsigned(n)), dim3(kPrefThreads), 0,
-                     s, logp, ref, mask, cu, T, partial);
-  hipLaunchKernelGGL(pref_grad_kernel, dim3(unsigned(2 * P), unsigned(n) + 1),
-                     dim3(kPrefThreads), 0, s, mask, cu, P, T, p, partial, int(n), loss, rewards,
-                     dlogp);
+  const PrefArgs a = {logp, ref, mask, cu, P, T, p, loss, rewards, dlogp};
+  if (pref_lone(P, T)) {
+    // 16 wavefronts: several to an answer when there are few answers
+    const int n = 2 * P >= 16 ? 1 : int(16 / (2 * P));
+    hipLaunchKernelGGL(pref_lone_kernel, dim3(1), dim3(1024), 0, s, a, n);
+    return hipGetLastError();
+  }
+  const int64_t n = pref_splits(P, T), units = 2 * P * n;
+  const unsigned blocks = unsigned((units + kPrefThreads / 64 - 1) / (kPrefThreads / 64));
+  Partial *part = reinterpret_cast<Partial *>(partial);
+  hipLaunchKernelGGL(pref_sum_kernel, dim3(blocks), dim3(kPrefThreads), 0, s, a, int(n), units,
+                     part);
+  hipLaunchKernelGGL(pref_grad_kernel, dim3(blocks + 1), dim3(kPrefThreads), 0, s, a, int(n),
+                     units, part);
   return hipGetLastError();
 }
 
