@@ -140,98 +140,149 @@ struct PrefArgs {
   float *loss, *rewards, *dlogp;
 };
 
+// The wavefront's number in its workgroup, as a scalar.
+__device__ __forceinline__ int wave_index() {
+  return __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64);
+}
+
+// Tokens number at most 2^30: a place fits 32 bits.
 struct Span {
-  int64_t first, last;
+  int32_t first, last;
 };
 
-__device__ __forceinline__ Span answer(const PrefArgs &a, int64_t i) {
+__device__ __forceinline__ Span answer(const PrefArgs &a, int32_t i) {
   const int64_t lo = a.cu[i], hi = a.cu[i + 1];
   const int64_t first = lo < 0 ? 0 : min64(lo, a.T);
-  return {first, hi < first ? first : min64(hi, a.T)};
+  return {int32_t(first), int32_t(hi < first ? first : min64(hi, a.T))};
 }
 
 // Slice j of n of an answer, its inner ends on multiples of four tokens.
-__device__ __forceinline__ Span slice(const Span &s, int64_t j, int64_t n) {
-  const int64_t base = s.first & ~int64_t(3);
-  const int64_t each = ((s.last - base + n - 1) / n + 3) & ~int64_t(3);
-  const int64_t lo = base + j * each;
-  const Span r = {lo < s.first ? s.first : lo, min64(lo + each, s.last)};
-  return r.first < r.last ? r : Span{s.last, s.last};
+__device__ __forceinline__ Span slice(const Span &s, int32_t j, int32_t n) {
+  const int32_t base = s.first & ~3;
+  const int32_t each = n == 1 ? s.last - base : int32_t((uint32_t(s.last - base + n - 1) / uint32_t(n) + 3u) & ~3u);
+  // (the last slices of a short answer are empty: j * each can pass 2^31)
+  const int64_t from = base + int64_t(j) * each;
+  const int32_t lo = int32_t(min64(from, s.last));
+  return {lo < s.first ? s.first : lo, int32_t(min64(from + each, s.last))};
 }
 
 struct Partial {
   double sum, count;
 };
 
-// Which of tokens t .. t + 3 count, bit by bit.
-__device__ __forceinline__ uint32_t counted4(const PrefArgs &a, const Span &s, int64_t t) {
-  uint32_t m = 0x01010101u;
-  if (a.mask) {
-    if (t + 4 <= a.T) {
-      __builtin_memcpy(&m, a.mask + t, 4);
-    } else {
-      m = 0;
-      for (int j = 0; t + j < a.T; ++j) m |= uint32_t(a.mask[t + j]) << (8 * j);
-    }
-  }
-  uint32_t bits = 0;
+// A quad's four tokens as they are loaded: from t on, or, at the end of the
+// arrays, the last four, of which those before t are another quad's.
+struct Quad {
+  int32_t t, at;
+  __device__ __forceinline__ Quad(const PrefArgs &a, int32_t from)
+      : t(from), at(from + 4 <= int32_t(a.T) ? from : int32_t(a.T) - 4) {}
+  // bit j: token at + j is the quad's own, lies in s and counts
+  __device__ __forceinline__ uint32_t counted(const Span &s, uint32_t mask) const {
+    const int32_t lo = t > s.first ? t : s.first, hi = t + 4 < s.last ? t + 4 : s.last;
+    uint32_t bits = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if ((m >> (8 * j) & 0xffu) && t + j >= s.first && t + j < s.last) bits |= 1u << j;
-  return bits;
+    for (int j = 0; j < 4; ++j)
+      if ((mask >> (8 * j) & 0xffu) && at + j >= lo && at + j < hi) bits |= 1u << j;
+    return bits;
+  }
+};
+
+// Arrays of less than four tokens take the byte and the word one by one.
+__device__ __forceinline__ uint32_t load_mask(const PrefArgs &a, const Quad &q) {
+  uint32_t m = 0x01010101u;
+  if (a.mask && q.at >= 0) __builtin_memcpy(&m, a.mask + q.at, 4);
+  if (a.mask && q.at < 0)
+    for (int j = 0; j < 4; ++j)
+      if (q.at + j >= 0) m = (m & ~(0xffu << 8 * j)) | uint32_t(a.mask[q.at + j]) << 8 * j;
+  return m;
+}
+__device__ __forceinline__ f32x4_t load_quad(const float *v, const Quad &q) {
+  f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (q.at >= 0) {
+    __builtin_memcpy(&x, v + q.at, 16);
+  } else {
+    for (int j = 0; j < 4; ++j)
+      if (q.at + j >= 0) x[j] = v[q.at + j];
+  }
+  return x;
 }
 
-// One wavefront's sum over a slice: quads of tokens, neighbours' tokens in the
-// first and last quad left out.
+// The quads of a slice, N of a lane at a time: straight-line loads (past the
+// slice's end the last quad again, nothing of it counted).
+constexpr int kPrefQuads = kPrefSlice / 256;
+
+__device__ __forceinline__ int32_t quad_at(const Span &s, int32_t t, int i) {
+  return t + 256 * i < s.last ? t + 256 * i : s.last;
+}
+
+// One wavefront's sum over a slice.
+template <int N>
 __device__ __forceinline__ Partial slice_sum(const PrefArgs &a, const Span &s) {
   double sum = 0.0;
   int count = 0;
-#pragma unroll 4
-  for (int64_t t = (s.first & ~int64_t(3)) + 4 * (threadIdx.x % 64); t < s.last; t += 256) {
-    const uint32_t bits = counted4(a, s, t);
-    f32x4_t lp = {0.0f, 0.0f, 0.0f, 0.0f}, rf = lp;
-    if (t + 4 <= a.T) {
-      __builtin_memcpy(&lp, a.logp + t, 16);
-      if (a.ref) __builtin_memcpy(&rf, a.ref + t, 16);
-    } else {
-      for (int j = 0; t + j < a.T; ++j) {
-        lp[j] = a.logp[t + j];
-        if (a.ref) rf[j] = a.ref[t + j];
-      }
+  for (int32_t t = (s.first & ~3) + 4 * int32_t(threadIdx.x % 64); t < s.last;
+       t += 256 * N) {
+    f32x4_t lp[N], rf[N] = {};
+    uint32_t m[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const Quad q(a, quad_at(s, t, i));
+      lp[i] = load_quad(a.logp, q);
+      if (a.ref) rf[i] = load_quad(a.ref, q);
+      m[i] = load_mask(a, q);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sum += (bits >> j & 1u) ? lp[j] - rf[j] : 0.0f;
-    count += __builtin_popcount(bits);
+    for (int i = 0; i < N; ++i) {
+      const uint32_t bits = Quad(a, quad_at(s, t, i)).counted(s, m[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum += (bits >> j & 1u) ? lp[i][j] - rf[i][j] : 0.0f;
+      count += __builtin_popcount(bits);
+    }
   }
   return {wave_sum(sum), wave_sum(double(count))};
 }
 
 // dlogp of a slice: g where a token counts, 0 elsewhere in the answer.
+template <int N>
 __device__ __forceinline__ void slice_grad(const PrefArgs &a, const Span &s, float g) {
-#pragma unroll 4
-  for (int64_t t = (s.first & ~int64_t(3)) + 4 * (threadIdx.x % 64); t < s.last; t += 256) {
-    const uint32_t bits = counted4(a, s, t);
-    f32x4_t d;
+  for (int32_t t = (s.first & ~3) + 4 * int32_t(threadIdx.x % 64); t < s.last;
+       t += 256 * N) {
+    uint32_t m[N];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] = (bits >> j & 1u) ? g : 0.0f;
-    if (t >= s.first && t + 4 <= s.last) {
-      __builtin_memcpy(a.dlogp + t, &d, 16);
-    } else {
+    for (int i = 0; i < N; ++i) m[i] = load_mask(a, Quad(a, quad_at(s, t, i)));
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (t + j >= s.first && t + j < s.last) a.dlogp[t + j] = d[j];
+    for (int i = 0; i < N; ++i) {
+      const Quad q(a, quad_at(s, t, i));
+      const uint32_t bits = q.counted(s, m[i]);
+      f32x4_t d;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = (bits >> j & 1u) ? g : 0.0f;
+      if (q.t >= s.first && q.t + 4 <= s.last) {
+        __builtin_memcpy(a.dlogp + q.t, &d, 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (q.at + j >= q.t && q.at + j >= s.first && q.at + j < s.last) a.dlogp[q.at + j] = d[j];
+      }
     }
   }
 }
 
+// Unit u: slice u % n of answer u / n.
+template <int N>
+__device__ __forceinline__ Partial unit_sum(const PrefArgs &a, int32_t u, int n) {
+  const int32_t i = n == 1 ? u : u / n;
+  return slice_sum<N>(a, slice(answer(a, i), u - i * n, n));
+}
+
 // An answer's S and count from its n partials; lane `at` of `lanes` (a power of
 // two, neighbours in a wavefront) adds every lanes-th of them.
-__device__ __forceinline__ Partial total(const PrefArgs &a, const Partial *partial, int64_t i,
+__device__ __forceinline__ Partial total(const PrefArgs &a, const Partial *partial, int32_t i,
                                          int n, int at, int lanes) {
   Partial r = {0.0, 0.0};
   for (int j = at; j < n; j += lanes) {
-    r.sum += partial[i * n + j].sum;
-    r.count += partial[i * n + j].count;
+    r.sum += partial[int64_t(i) * n + j].sum;
+    r.count += partial[int64_t(i) * n + j].count;
   }
   for (int o = lanes / 2; o > 0; o >>= 1) {
     r.sum += __shfl_xor(r.sum, o);
@@ -245,19 +296,24 @@ __device__ __forceinline__ int lanes_for(int n) {
   return n <= 1 ? 1 : n >= 33 ? 64 : 1 << (32 - __builtin_clz(n - 1));
 }
 
-// Unit (i, j)'s gradient; slice 0 also writes the answer's reward.
-__device__ __forceinline__ void unit_grad(const PrefArgs &a, const Partial *partial, int64_t i,
-                                          int j, int n) {
+// Unit u's gradient; slice 0 also writes the answer's reward.  Its pair's loss.
+template <int N>
+__device__ __forceinline__ float unit_grad(const PrefArgs &a, const Partial *partial, int32_t u,
+                                          int n) {
+  const int32_t i = n == 1 ? u : u / n, j = u - i * n, P = int32_t(a.P);
+  const Span own_slice = slice(answer(a, i), j, n);
   const int lane = threadIdx.x % 64, lanes = lanes_for(n);
-  const int64_t k = i < a.P ? i : i - a.P;
+  const int32_t k = i < P ? i : i - P;
   const Partial c = total(a, partial, k, n, lane % lanes, lanes);
-  const Partial r = total(a, partial, a.P + k, n, lane % lanes, lanes);
-  const Partial &own = i < a.P ? c : r;
-  float g = pair_loss(a.p, float(c.sum) - float(r.sum)).dh / float(a.P);
-  if (i >= a.P) g = -g;
+  const Partial r = total(a, partial, P + k, n, lane % lanes, lanes);
+  const Partial &own = i < P ? c : r;
+  const PairLoss l = pair_loss(a.p, float(c.sum - r.sum));
+  float g = l.dh / float(a.P);
+  if (i >= P) g = -g;
   if (a.p.average && own.count > 0.0) g /= float(own.count);
-  if (j == 0 && lane == 0) a.rewards[i] = a.p.beta * float(own.sum);
-  slice_grad(a, slice(answer(a, i), j, n), g);
+  if (j == 0 && lane == 0) a.rewards[i] = float(a.p.beta * own.sum);
+  slice_grad<N>(a, own_slice, g);
+  return l.loss;
 }
 
 // The mean loss, by one workgroup: a pair to `lanes` lanes.
@@ -266,12 +322,13 @@ __device__ __forceinline__ void mean_loss(const PrefArgs &a, const Partial *part
                                           double *red) {
   const int lanes = lanes_for(n), at = threadIdx.x % lanes;
   double sum[1] = {};
-  for (int64_t first = 0; first < a.P; first += threads / lanes) {
-    const int64_t k = first + threadIdx.x / lanes;
-    const int64_t kk = k < a.P ? k : a.P - 1;     // every lane takes part in the shuffles
+  const int32_t P = int32_t(a.P);
+  for (int32_t first = 0; first < P; first += threads / lanes) {
+    const int32_t k = first + int32_t(threadIdx.x) / lanes;
+    const int32_t kk = k < P ? k : P - 1;     // every lane takes part in the shuffles
     const Partial c = total(a, partial, kk, n, at, lanes);
-    const Partial r = total(a, partial, a.P + kk, n, at, lanes);
-    if (k < a.P && at == 0) sum[0] += pair_loss(a.p, float(c.sum) - float(r.sum)).loss;
+    const Partial r = total(a, partial, P + kk, n, at, lanes);
+    if (k < P && at == 0) sum[0] += pair_loss(a.p, float(c.sum - r.sum)).loss;
   }
   block_sums<1, threads>(sum, red);
   if (threadIdx.x == 0) a.loss[0] = float(sum[0] / double(a.P));
@@ -279,35 +336,44 @@ __device__ __forceinline__ void mean_loss(const PrefArgs &a, const Partial *part
 
 // Zeros for the tokens outside every answer, by thread `at` of `all`.
 __device__ __forceinline__ void zero_outside(const PrefArgs &a, int64_t at, int64_t all) {
-  const int64_t lo = answer(a, 0).first, hi = answer(a, 2 * a.P - 1).last;
+  const int64_t lo = answer(a, 0).first, hi = answer(a, 2 * int32_t(a.P) - 1).last;
   for (int64_t t = at; t < lo; t += all) a.dlogp[t] = 0.0f;
   for (int64_t t = hi + at; t < a.T; t += all) a.dlogp[t] = 0.0f;
 }
 
 __global__ __launch_bounds__(1024) void pref_lone_kernel(PrefArgs a, int n) {
   __shared__ Partial partial[2 * kPrefLonePairs];
-  __shared__ double red[16];
-  const int units = int(2 * a.P) * n, wave = threadIdx.x / 64;
+  __shared__ float loss[kPrefLonePairs];
+  const int units = int(2 * a.P) * n, wave = wave_index(), lane = threadIdx.x % 64;
   for (int u = wave; u < units; u += 16) {
-    const Partial s = slice_sum(a, slice(answer(a, u / n), u % n, n));
-    if (threadIdx.x % 64 == 0) partial[u] = s;
+    const Partial s = unit_sum<1>(a, u, n);
+    if (lane == 0) partial[u] = s;
   }
   __syncthreads();
-  for (int u = wave; u < units; u += 16) unit_grad(a, partial, u / n, u % n, n);
+  for (int u = wave; u < units; u += 16) {
+    const float l = unit_grad<1>(a, partial, u, n);
+    if (lane == 0 && u < int(a.P) * n && u % n == 0) loss[u / n] = l;
+  }
   zero_outside(a, threadIdx.x, 1024);
-  mean_loss<1024>(a, partial, n, red);
+  __syncthreads();
+  if (wave == 0) {
+    double sum = 0.0;
+    for (int k = lane; k < int(a.P); k += 64) sum += loss[k];
+    sum = wave_sum(sum);
+    if (lane == 0) a.loss[0] = float(sum / double(a.P));
+  }
 }
 
-__global__ __launch_bounds__(kPrefThreads) void pref_sum_kernel(PrefArgs a, int n, int64_t units,
+__global__ __launch_bounds__(kPrefThreads) void pref_sum_kernel(PrefArgs a, int n, int32_t units,
                                                                 Partial *partial) {
-  const int64_t u = int64_t(blockIdx.x) * (kPrefThreads / 64) + threadIdx.x / 64;
+  const int32_t u = int32_t(blockIdx.x) * (kPrefThreads / 64) + wave_index();
   if (u >= units) return;
-  const Partial s = slice_sum(a, slice(answer(a, u / n), u % n, n));
+  const Partial s = unit_sum<kPrefQuads>(a, u, n);
   if (threadIdx.x % 64 == 0) partial[u] = s;
 }
 
 // The last workgroup takes the mean loss.
-__global__ __launch_bounds__(kPrefThreads) void pref_grad_kernel(PrefArgs a, int n, int64_t units,
+__global__ __launch_bounds__(kPrefThreads) void pref_grad_kernel(PrefArgs a, int n, int32_t units,
                                                                  const Partial *partial) {
   __shared__ double red[kPrefThreads / 64];
   const int64_t work = int64_t(gridDim.x) - 1;
@@ -315,8 +381,8 @@ __global__ __launch_bounds__(kPrefThreads) void pref_grad_kernel(PrefArgs a, int
     mean_loss<kPrefThreads>(a, partial, n, red);
     return;
   }
-  const int64_t u = int64_t(blockIdx.x) * (kPrefThreads / 64) + threadIdx.x / 64;
-  if (u < units) unit_grad(a, partial, u / n, int(u % n), n);
+  const int32_t u = int32_t(blockIdx.x) * (kPrefThreads / 64) + wave_index();
+  if (u < units) unit_grad<kPrefQuads>(a, partial, u, n);
   zero_outside(a, int64_t(blockIdx.x) * kPrefThreads + threadIdx.x, work * kPrefThreads);
 }
 
@@ -381,10 +447,10 @@ hipError_t launch_pref(const float *logp, const float *ref, const uint8_t *mask,
   const int64_t n = pref_splits(P, T), units = 2 * P * n;
   const unsigned blocks = unsigned((units + kPrefThreads / 64 - 1) / (kPrefThreads / 64));
   Partial *part = reinterpret_cast<Partial *>(partial);
-  hipLaunchKernelGGL(pref_sum_kernel, dim3(blocks), dim3(kPrefThreads), 0, s, a, int(n), units,
-                     part);
+  hipLaunchKernelGGL(pref_sum_kernel, dim3(blocks), dim3(kPrefThreads), 0, s, a, int(n),
+                     int32_t(units), part);
   hipLaunchKernelGGL(pref_grad_kernel, dim3(blocks + 1), dim3(kPrefThreads), 0, s, a, int(n),
-                     units, part);
+                     int32_t(units), part);
   return hipGetLastError();
 }
 

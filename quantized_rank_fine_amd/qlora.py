@@ -177,9 +177,7 @@ def header_functions():
 # ------------------------------------------------------------------ helpers
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or type(t) is int:
         return t
     return t.data_ptr()
 
@@ -188,6 +186,9 @@ def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
+    if torch.cuda.is_initialized():
+        # the same handle as below without building a Stream object (0.2 us, not 2.7)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return torch.cuda.current_stream().cuda_stream
 
 
