@@ -358,17 +358,25 @@ qlora_status check_logits(int64_t ld, int64_t T, int64_t V, qlora_dtype dt, floa
   return QLORA_OK;
 }
 
-// Workspace of the objective from the logits: every token's terms, and the
-// partial sums of many.
+// Workspace of the objective from the logits: every token's terms, the partial
+// sums of many, and the scratch of rows cut into segments.
 struct TermsPlan {
-  size_t off_partial = 0, total = 0;
+  size_t off_partial = 0, off_split = 0, off_rows = 0, total = 0;
 };
 
-TermsPlan plan_terms(int64_t T) {
+size_t part_bytes(int64_t T, int64_t segments) {
+  return size_t(T * segments) * kStatFloats * sizeof(float);
+}
+
+TermsPlan plan_terms(int64_t T, int64_t V) {
   TermsPlan p;
   Layout L;
   L.take(size_t(T) * 4 * sizeof(float));
   if (terms_blocks(T) > 1) p.off_partial = L.take(size_t(terms_blocks(T)) * 4 * sizeof(double));
+  if (const size_t n = part_bytes(T, policy_segments(T, V))) {
+    p.off_split = L.take(n);
+    p.off_rows = L.take(size_t(T) * 5 * sizeof(float));
+  }
   p.total = L.o;
   return p;
 }
@@ -677,24 +685,28 @@ qlora_status qlora_adam_step(float *theta, const float *grad, float *m, float *v
 }
 
 size_t qlora_token_logp_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt) {
-  (void)T; (void)V; (void)dt;
-  return 0;
+  if (check_logits(V, T, V, dt, 1.0f) != QLORA_OK) return 0;
+  return part_bytes(T, forward_segments(T, V, dt == QLORA_BF16));
 }
 
 qlora_status qlora_token_logp_fwd(const void *logits, int64_t ld, int64_t T, int64_t V,
                                   qlora_dtype dt, const int64_t *labels, float scale,
                                   float *logp, float *stats, float *entropy, void *ws,
                                   size_t ws_bytes, hipStream_t stream) {
-  (void)ws; (void)ws_bytes;
   qlora_status st = check_logits(ld, T, V, dt, scale);
   if (st != QLORA_OK || T == 0) return st;
   if (!logits || !labels || !logp || !stats) return QLORA_ERR_NULL;
   if (!aligned_el(logits, dt) || !aligned_to(labels, 8) || !aligned_to(logp, 4) ||
       !aligned_to(stats, 4) || !aligned_to(entropy, 4))
     return QLORA_ERR_ALIGN;
+  const size_t need = qlora_token_logp_workspace_bytes(T, V, dt);
+  if (need && !ws) return QLORA_ERR_NULL;
+  if (!aligned_to(ws, 4)) return QLORA_ERR_ALIGN;
+  if (ws_bytes < need) return QLORA_ERR_WORKSPACE;
   const LogitRows a{logits, ld, T, V, dt == QLORA_BF16, labels, scale};
-  return dev(timed(QLORA_KERNEL_LOGP, stream,
-                   [&] { return launch_logp_fwd(a, logp, stats, entropy, stream); }));
+  return dev(timed(QLORA_KERNEL_LOGP, stream, [&] {
+    return launch_logp_fwd(a, logp, stats, entropy, static_cast<float *>(ws), stream);
+  }));
 }
 
 qlora_status qlora_token_logp_bwd(const void *logits, int64_t ld, int64_t T, int64_t V,
@@ -779,7 +791,7 @@ qlora_status qlora_policy_loss(const float *logp, const float *entropy, int64_t 
 
 size_t qlora_policy_logits_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt) {
   if (check_logits(V, T, V, dt, 1.0f) != QLORA_OK) return 0;
-  return plan_terms(T).total;
+  return plan_terms(T, V).total;
 }
 
 qlora_status qlora_policy_logits(const void *logits, int64_t ld, int64_t T, int64_t V,
@@ -801,15 +813,20 @@ qlora_status qlora_policy_logits(const void *logits, int64_t ld, int64_t T, int6
   for (const float *v : {weight, adv, old, ref, static_cast<const float *>(out),
                          static_cast<const float *>(logp)})
     if (!aligned_to(v, 4)) return QLORA_ERR_ALIGN;
-  const TermsPlan plan = plan_terms(T);
+  const TermsPlan plan = plan_terms(T, V);
   if (ws_bytes < plan.total) return QLORA_ERR_WORKSPACE;
   float *terms = static_cast<float *>(ws);
   double *partial = plan.off_partial ? at<double>(ws, plan.off_partial) : nullptr;
+  PolicySplit split{};
+  if (plan.off_split) {
+    float *rows = at<float>(ws, plan.off_rows);
+    split = {at<float>(ws, plan.off_split), rows, rows + 2 * T, rows + 3 * T, rows + 4 * T};
+  }
   if (T > 0) {
     const LogitRows a{logits, ld, T, V, dt == QLORA_BF16, labels, scale};
     const hipError_t e = timed(QLORA_KERNEL_POLICY, stream, [&] {
       return launch_policy_logits(a, PolicyTokens{weight, adv, old, ref}, p, terms, logp,
-                                  dlogits, ldd, stream);
+                                  dlogits, ldd, split, stream);
     });
     if (e != hipSuccess) return QLORA_ERR_DEVICE;
   }

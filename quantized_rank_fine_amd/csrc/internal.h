@@ -301,17 +301,28 @@ struct PolicyTokens {
   const float *weight, *adv, *old, *ref;   // each may be null
 };
 
+// Segments that rows are cut into, 0 if they are not: few rows (too few to
+// fill the chip) that are long.  Each segment leaves kStatFloats floats.
+constexpr int64_t kStatFloats = 3;
+int64_t forward_segments(int64_t T, int64_t V, bool bf16);
+int64_t policy_segments(int64_t T, int64_t V);
+
 // log p of the labels: logp, stats [T x 2] = (m, z), entropy (may be null).
 hipError_t launch_logp_fwd(const LogitRows &a, float *logp, float *stats, float *entropy,
-                           hipStream_t s);
+                           float *part, hipStream_t s);
 hipError_t launch_logp_bwd(const LogitRows &a, const float *stats, const float *entropy,
                            const float *g, const float *g_entropy, void *dx, int64_t ldd,
                            hipStream_t s);
 // The objective from the logits to their gradient; terms [T x 4] fp32 receives
-// each token's weighted (loss, k, bound, entropy) for launch_sum_terms.
+// each token's weighted (loss, k, bound, entropy) for launch_sum_terms.  The
+// scratch of rows that are cut (else unused): part, and by row (m, z), entropy
+// and the gradients of logp and of the entropy.
+struct PolicySplit {
+  float *part, *stats, *entropy, *g, *gh;
+};
 hipError_t launch_policy_logits(const LogitRows &a, const PolicyTokens &t,
                                 const PolicyParams &p, float *terms, float *logp, void *dx,
-                                int64_t ldd, hipStream_t s);
+                                int64_t ldd, const PolicySplit &o, hipStream_t s);
 // out[4] = the columns' sums of terms [n x 4], fp64, in an order that n fixes.
 // partial: terms_blocks(n) * 4 doubles, unused (may be null) when that is 1.
 int64_t terms_blocks(int64_t n);

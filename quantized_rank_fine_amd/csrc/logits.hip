@@ -269,16 +269,31 @@ __device__ __forceinline__ RowResult row_result(const Stat &a, float off, float 
 // row read again.  Such rows are all but -inf; speed does not matter here.
 template <bool BF16, int threads>
 __device__ __forceinline__ Stat careful_row(const char *row, int32_t V, float m, float c,
-                                         Stat *red) {
+                                            Stat *red) {
   Stat a = {0.0f, 0.0f, 0.0f};
-  for (int32_t v = int32_t(threadIdx.x); v < V; v += threads) {
+  for (int32_t v = int32_t(threadIdx.x) % threads; v < V; v += threads) {
     const float L = c * (load1<BF16>(row, v) - m);
     const float p = __builtin_amdgcn_exp2f(L);
     a.t += p;
     a.w = __builtin_fmaf(p, fmaxf(L, kLeast), a.w);
   }
-  __syncthreads();
+  if (threads > 64) __syncthreads();
   return joined_block<threads>(a, c, red);
+}
+
+// Results of a row from its words' joined sums.
+template <bool BF16, int threads>
+__device__ __forceinline__ RowResult finished(Stat a, const char *row, int32_t V,
+                                              float xy, float scale, Stat *red) {
+  const float c = scale * kLog2e;
+  float off = __builtin_fmaf(c, a.m, -reference(a.m, c));
+  if (!(a.t > 0.0f && a.t < INFINITY) && fabsf(a.m) < INFINITY) {
+    const float m = a.m;
+    a = careful_row<BF16, threads>(row, V, m, c, red);
+    a.m = m;
+    off = 0.0f;
+  }
+  return row_result(a, off, xy, scale);
 }
 
 // A row's results: its chunks summed one after the other.  h holds the last
@@ -297,14 +312,7 @@ __device__ __forceinline__ RowResult row_stat(Held<BF16, threads, NG> &h, const 
     add_chunk<ENT>(a, h, c);
   }
   a = joined_block<threads>(a, c, red);
-  float off = __builtin_fmaf(c, a.m, -reference(a.m, c));
-  if (!(a.t > 0.0f && a.t < INFINITY) && fabsf(a.m) < INFINITY) {
-    const float m = a.m;
-    a = careful_row<BF16, threads>(row, V, m, c, red);
-    a.m = m;
-    off = 0.0f;
-  }
-  return row_result(a, off, xy, scale);
+  return finished<BF16, threads>(a, row, V, xy, scale, red);
 }
 
 // Coefficients of a row's gradient: with L = log2 p,
@@ -491,10 +499,131 @@ __global__ __launch_bounds__(threads) void policy_logits_kernel(
   }
 }
 
+// ---------------------------------------------------- few, very long rows
+//
+// Few long rows are cut into segments: a workgroup sums a segment, a wavefront joins a row's
+// segments, and the gradient is logp_bwd_kernel's, by segments too.
+
+constexpr int kPartThreads = 256, kPartNG = 4;
+
+template <bool BF16, bool ENT>
+__global__ __launch_bounds__(kPartThreads) void part_kernel(LogitRows a, const float *weight,
+                                                            Stat *part) {
+  __shared__ Stat red[kPartThreads / 64];
+  const int64_t t = row_index();
+  if (t >= a.T) return;
+  const int64_t y = a.labels[t];
+  if (y < 0 || y >= a.V || (weight && weight[t] == 0.0f)) return;   // nor will it be joined
+  const char *row = row_at<BF16>(a.x, t * a.ld);
+  const float c = a.scale * kLog2e;
+  Held<BF16, kPartThreads, kPartNG> h;
+  const Cut<BF16> k(row, int32_t(a.V));
+  const int32_t from = int32_t(blockIdx.x) * h.words;
+  Stat s = {-INFINITY, 0.0f, 0.0f};
+  if (from == 0 || from < k.whole) {
+    h.load(row, k, from);
+    add_chunk<ENT>(s, h, c);
+  }
+  s = joined_block<kPartThreads>(s, c, red);
+  if (threadIdx.x == 0) part[t * gridDim.x + blockIdx.x] = s;
+}
+
+// A row to a wavefront.
+template <bool BF16>
+__device__ __forceinline__ RowResult join_row(const LogitRows &a, const Stat *part, int segments,
+                                              int64_t t, int64_t y) {
+  const float c = a.scale * kLog2e;
+  Stat s = {-INFINITY, 0.0f, 0.0f};
+  for (int j = threadIdx.x % 64; j < segments; j += 64) {
+    const Stat b = part[t * segments + j];
+    const float top = fmaxf(s.m, b.m);
+    const Stat x = raised(s, top, c), z = raised(b, top, c);
+    s = {top, x.t + z.t, x.w + z.w};
+  }
+  const char *row = row_at<BF16>(a.x, t * a.ld);
+  return finished<BF16, 64>(joined(s, c), row, int32_t(a.V), load1<BF16>(row, uint32_t(y)),
+                            a.scale, nullptr);
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(64) void logp_join_kernel(LogitRows a, const Stat *part, int segments,
+                                                       float *logp, float *stats,
+                                                       float *entropy) {
+  const int64_t t = row_index();
+  if (t >= a.T) return;
+  const int64_t y = a.labels[t];
+  RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (y >= 0 && y < a.V) r = join_row<BF16>(a, part, segments, t, y);
+  if (threadIdx.x == 0) {
+    logp[t] = r.logp;
+    stats[2 * t] = r.m;
+    stats[2 * t + 1] = r.z;
+    if (entropy) entropy[t] = r.ent;
+  }
+}
+
+// Also the token's objective: what logp_bwd_kernel needs of it, and its terms.
+template <bool BF16>
+__global__ __launch_bounds__(64) void policy_join_kernel(LogitRows a, PolicyTokens k,
+                                                         PolicyParams p, const Stat *part,
+                                                         int segments, PolicySplit o,
+                                                         float *terms, float *logp) {
+  const int64_t t = row_index();
+  if (t >= a.T) return;
+  const int64_t y = a.labels[t];
+  const float w = k.weight ? k.weight[t] : 1.0f;
+  RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4_t term = {0.0f, 0.0f, 0.0f, 0.0f};
+  float g = 0.0f, gh = 0.0f;
+  if (y >= 0 && y < a.V && w != 0.0f) {
+    r = join_row<BF16>(a, part, segments, t, y);
+    const PolicyToken q = policy_token(p, r.logp, r.ent, k.adv ? k.adv[t] : 1.0f,
+                                       k.old ? r.logp - k.old[t] : 0.0f, k.ref,
+                                       k.ref ? k.ref[t] : 0.0f);
+    term = f32x4_t{w * q.loss, w * q.k, w * q.bound, w * r.ent};
+    g = w * q.dlogp;
+    gh = -p.ent * w;
+  }
+  if (threadIdx.x == 0) {
+    reinterpret_cast<f32x4_t *>(terms)[t] = term;
+    if (logp) logp[t] = r.logp;
+    o.stats[2 * t] = r.m;
+    o.stats[2 * t + 1] = r.z;
+    o.entropy[t] = r.ent;
+    o.g[t] = g;
+    o.gh[t] = gh;
+  }
+}
+
 dim3 row_grid(int64_t T, int64_t segments = 1) {
   return dim3(unsigned(segments), unsigned(min64(T, kRowsY)),
               unsigned((T + kRowsY - 1) / kRowsY));
 }
+
+constexpr int64_t kFewRows = 64;
+
+int64_t segments_of(int64_t V) {
+  constexpr int64_t words = int64_t(kPartThreads) * 8 * kPartNG;
+  return (V + words - 1) / words;
+}
+
+}  // namespace
+
+// A second launch costs about 3 us.  Measured, us a call back to back, cut and
+// whole (T = 1 / 64): V = 131072 bf16 (256 KiB a row) 10.2 / 10.2, 9.1 / 10.1;
+// V = 200000 fp32 (800 KB) 10.1 / 13.2, 11.6 / 14.3.
+int64_t forward_segments(int64_t T, int64_t V, bool bf16) {
+  return T <= kFewRows && V * (bf16 ? 2 : 4) > (int64_t(256) << 10) ? segments_of(V) : 0;
+}
+
+// Rows that a workgroup would have to read twice.  Cut and whole (T = 1 / 64 /
+// 128): V = 70000 bf16 17.9 / 18.7 / 22.5, 19.0 / 20.7 / 22.4; V = 200000 fp32
+// 17.8 / 36.9 / 67.0, 38.6 / 51.0 / 75.3.
+int64_t policy_segments(int64_t T, int64_t V) {
+  return T <= kFewRows && V > 65536 ? segments_of(V) : 0;
+}
+
+namespace {
 
 // Lanes and groups to a row.  A lane wants 4 to 8 groups of 8 words in flight,
 // and every wavefront of a row repeats the row's last reductions, so a row
@@ -504,7 +633,16 @@ dim3 row_grid(int64_t T, int64_t segments = 1) {
 //   V = 16000, T = 8192:  256 x 8 38.6  64 x 8 43.4    512 x 4 43.1
 //   V = 32000, T = 4096:  512 x 8 37.3  256 x 8 41.9   1024 x 4 46.5
 template <bool BF16, bool ENT>
-void logp_fwd(const LogitRows &a, float *logp, float *stats, float *entropy, hipStream_t s) {
+void logp_fwd(const LogitRows &a, float *logp, float *stats, float *entropy, float *part,
+              hipStream_t s) {
+  if (const int64_t n = forward_segments(a.T, a.V, BF16)) {
+    Stat *q = reinterpret_cast<Stat *>(part);
+    hipLaunchKernelGGL((part_kernel<BF16, ENT>), row_grid(a.T, n), dim3(kPartThreads), 0, s, a,
+                       nullptr, q);
+    hipLaunchKernelGGL((logp_join_kernel<BF16>), row_grid(a.T), dim3(64), 0, s, a, q, int(n),
+                       logp, stats, entropy);
+    return;
+  }
 #define ROWS(threads, NG)                                                                     \
   hipLaunchKernelGGL((logp_fwd_kernel<BF16, ENT, threads, NG>), row_grid(a.T), dim3(threads), \
                      0, s, a, logp, stats, entropy)
@@ -535,7 +673,16 @@ void logp_bwd(const LogitRows &a, const float *stats, const float *entropy, cons
 //   V = 60000, T = 1024:  1024 x 8 54.4, read twice by 1024 x 4 58.9
 template <bool BF16, bool ENT>
 void policy_logits(const LogitRows &a, const PolicyTokens &t, const PolicyParams &p, float *terms,
-                   float *logp, void *dx, int64_t ldd, hipStream_t s) {
+                   float *logp, void *dx, int64_t ldd, const PolicySplit &o, hipStream_t s) {
+  if (const int64_t n = policy_segments(a.T, a.V)) {
+    Stat *q = reinterpret_cast<Stat *>(o.part);
+    hipLaunchKernelGGL((part_kernel<BF16, true>), row_grid(a.T, n), dim3(kPartThreads), 0, s, a,
+                       t.weight, q);
+    hipLaunchKernelGGL((policy_join_kernel<BF16>), row_grid(a.T), dim3(64), 0, s, a, t, p, q,
+                       int(n), o, terms, logp);
+    logp_bwd<BF16, ENT>(a, o.stats, o.entropy, o.g, o.gh, dx, ldd, s);
+    return;
+  }
 #define ROWS(ONE, threads, NG)                                                            \
   hipLaunchKernelGGL((policy_logits_kernel<BF16, ENT, ONE, threads, NG>), row_grid(a.T), \
                      dim3(threads), 0, s, a, t, p, terms, logp, dx, ldd)
@@ -552,9 +699,9 @@ void policy_logits(const LogitRows &a, const PolicyTokens &t, const PolicyParams
 }  // namespace
 
 hipError_t launch_logp_fwd(const LogitRows &a, float *logp, float *stats, float *entropy,
-                           hipStream_t s) {
-#define GO(B) (entropy ? logp_fwd<B, true>(a, logp, stats, entropy, s) \
-                       : logp_fwd<B, false>(a, logp, stats, entropy, s))
+                           float *part, hipStream_t s) {
+#define GO(B) (entropy ? logp_fwd<B, true>(a, logp, stats, entropy, part, s) \
+                       : logp_fwd<B, false>(a, logp, stats, entropy, part, s))
   a.bf16 ? GO(true) : GO(false);
 #undef GO
   return hipGetLastError();
@@ -572,9 +719,9 @@ hipError_t launch_logp_bwd(const LogitRows &a, const float *stats, const float *
 
 hipError_t launch_policy_logits(const LogitRows &a, const PolicyTokens &t,
                                 const PolicyParams &p, float *terms, float *logp, void *dx,
-                                int64_t ldd, hipStream_t s) {
-#define GO(B) (p.ent != 0.0f ? policy_logits<B, true>(a, t, p, terms, logp, dx, ldd, s) \
-                             : policy_logits<B, false>(a, t, p, terms, logp, dx, ldd, s))
+                                int64_t ldd, const PolicySplit &o, hipStream_t s) {
+#define GO(B) (p.ent != 0.0f ? policy_logits<B, true>(a, t, p, terms, logp, dx, ldd, o, s) \
+                             : policy_logits<B, false>(a, t, p, terms, logp, dx, ldd, o, s))
   a.bf16 ? GO(true) : GO(false);
 #undef GO
   return hipGetLastError();

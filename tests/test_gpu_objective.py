@@ -83,6 +83,7 @@ SHAPES = [  # T, V, ld, dt, s, elements before the first row
     (70, 1000, 1000, "bf16", 1.0, 0), (2, 4096, 4097, "bf16", 1.0, 0),
     (6, 32000, 32000, "bf16", 1.0, 0), (2, 50001, 50016, "f32", 1.25, 1),
     (3, 131077, 131077, "bf16", 1.0, 0), (1, 300007, 300007, "f32", 1.0, 0),
+    (66, 70003, 70003, "bf16", 1.0, 0),          # more rows than are cut into segments
 ]
 
 
