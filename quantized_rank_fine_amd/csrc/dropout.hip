@@ -33,83 +33,116 @@ __device__ __forceinline__ u32x4_t philox(uint64_t n, uint64_t counter, uint64_t
   return u32x4_t{a, b, c, d};
 }
 
+// 8 elements from `p` on, of which n are there (n < 8 at a row's end only).
 template <bool BF16>
-__device__ __forceinline__ float load1(const void *x, int64_t at) {
-  if (BF16)
-    return __uint_as_float(uint32_t(static_cast<const uint16_t *>(x)[at]) << 16);
-  return static_cast<const float *>(x)[at];
+__device__ __forceinline__ void load8(const void *p, int64_t at, int n, float (&e)[8]) {
+  if (BF16) {
+    const uint16_t *x = static_cast<const uint16_t *>(p) + at;
+    if (n >= 8) {
+      u32x4_t u;
+      __builtin_memcpy(&u, x, 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        e[2 * i] = bf16_lo_to_f32(u[i]);
+        e[2 * i + 1] = bf16_hi_to_f32(u[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = i < n ? __uint_as_float(uint32_t(x[i]) << 16) : 0.0f;
+    }
+  } else {
+    const float *x = static_cast<const float *>(p) + at;
+    if (n >= 8) {
+      __builtin_memcpy(e, x, 32);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = i < n ? x[i] : 0.0f;
+    }
+  }
 }
 
 template <bool BF16>
-__device__ __forceinline__ void load8(const void *x, int64_t at, float (&e)[8]) {
+__device__ __forceinline__ void store8(void *p, int64_t at, int n, const float (&e)[8]) {
   if (BF16) {
-    u32x4_t u;
-    __builtin_memcpy(&u, static_cast<const uint16_t *>(x) + at, 16);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      e[2 * i] = bf16_lo_to_f32(u[i]);
-      e[2 * i + 1] = bf16_hi_to_f32(u[i]);
-    }
-  } else {
-    __builtin_memcpy(e, static_cast<const float *>(x) + at, 32);
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void dropout8(const DropoutArgs &a, int64_t groups, int64_t n) {
-  const int64_t row = n / groups, j = (n - row * groups) * 8;
-  const u32x4_t w = philox(uint64_t(n), a.counter, a.seed);
-  const int64_t ix = row * a.ldx + j, ir = row * a.ldr + j, iy = row * a.ldy + j;
-  const int left = int(a.cols - j < 8 ? a.cols - j : 8);
-  float e[8] = {}, r[8] = {};
-  if (left == 8) {
-    load8<BF16>(a.x, ix, e);
-    if (a.res) load8<BF16>(a.res, ir, r);
-  } else {
-    for (int i = 0; i < left; ++i) {
-      e[i] = load1<BF16>(a.x, ix + i);
-      if (a.res) r[i] = load1<BF16>(a.res, ir + i);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t bits = (w[i / 2] >> (16 * (i % 2))) & 0xffffu;
-    e[i] = (bits >= a.p16 ? a.c * e[i] : 0.0f) + r[i];
-  }
-  if (BF16) {
-    uint16_t *y = static_cast<uint16_t *>(a.y) + iy;
+    uint16_t *y = static_cast<uint16_t *>(p) + at;
     const u32x4_t u = {pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
                        pack_bf16x2(e[6], e[7])};
-    if (left == 8)
+    if (n >= 8) {
       __builtin_memcpy(y, &u, 16);
-    else
-      for (int i = 0; i < left; ++i) y[i] = uint16_t(u[i / 2] >> (16 * (i % 2)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) y[i] = uint16_t(u[i / 2] >> (16 * (i % 2)));
+    }
   } else {
-    float *y = static_cast<float *>(a.y) + iy;
-    if (left == 8)
+    float *y = static_cast<float *>(p) + at;
+    if (n >= 8) {
       __builtin_memcpy(y, e, 32);
-    else
-      for (int i = 0; i < left; ++i) y[i] = e[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) y[i] = e[i];
+    }
   }
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, int64_t groups) {
-  const int64_t all = a.rows * groups, step = int64_t(gridDim.x) * 256;
-  for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < all; n += step)
-    dropout8<BF16>(a, groups, n);
+// Group n of `count` to a lane, the first of them the matrix's group `base`.
+// FLAT: dense rows of a multiple of 8, group n is elements 8 n .. 8 n + 7 (the
+// division by the groups of a row is about a quarter of the lane's work).
+template <bool BF16, bool RES, bool FLAT>
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, uint32_t groups,
+                                                      uint32_t count, uint64_t base) {
+  const uint32_t n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= count) return;
+  const uint32_t row = FLAT ? 0 : n / groups;
+  const int64_t j = FLAT ? int64_t(n) * 8 : int64_t(n - row * groups) * 8;
+  const int left = FLAT ? 8 : int(min64(a.cols - j, 8));
+  float e[8], r[8];
+  load8<BF16>(a.x, row * a.ldx + j, left, e);
+  if (RES) load8<BF16>(a.res, row * a.ldr + j, left, r);
+  const u32x4_t w = philox(base + n, a.counter, a.seed);
+  // a half h is kept where h >= p16, compared in a word's upper half
+  const uint32_t least = a.p16 << 16;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool keep = i % 2 ? w[i / 2] >= least : w[i / 2] << 16 >= least;
+    e[i] = keep ? a.c * e[i] : 0.0f;
+    if (RES) e[i] += r[i];
+  }
+  store8<BF16>(a.y, row * a.ldy + j, left, e);
+}
+
+template <bool BF16, bool RES>
+void dropout(DropoutArgs a, hipStream_t s) {
+  const int64_t groups = (a.cols + 7) / 8;
+  const bool flat = a.cols % 8 == 0 && a.ldx == a.cols && a.ldy == a.cols &&
+                    (!RES || a.ldr == a.cols);
+  // a launch counts its groups in 32 bits, and holds less than 2^32 threads
+  const int64_t rows_each = ((int64_t(1) << 31) / groups);
+  const int64_t size = BF16 ? 2 : 4;
+  for (int64_t row = 0; row < a.rows; row += rows_each) {
+    const int64_t count = min64(a.rows - row, rows_each) * groups;
+    DropoutArgs b = a;
+    b.x = static_cast<const char *>(a.x) + row * a.ldx * size;
+    b.y = static_cast<char *>(a.y) + row * a.ldy * size;
+    if (RES) b.res = static_cast<const char *>(a.res) + row * a.ldr * size;
+    const dim3 grid{unsigned((count + 255) / 256)};
+    if (flat)
+      hipLaunchKernelGGL((dropout_kernel<BF16, RES, true>), grid, dim3(256), 0, s, b,
+                         uint32_t(groups), uint32_t(count), uint64_t(row * groups));
+    else
+      hipLaunchKernelGGL((dropout_kernel<BF16, RES, false>), grid, dim3(256), 0, s, b,
+                         uint32_t(groups), uint32_t(count), uint64_t(row * groups));
+  }
 }
 
 }  // namespace
 
 hipError_t launch_dropout(const DropoutArgs &a, bool bf16, hipStream_t s) {
-  const int64_t groups = (a.cols + 7) / 8;
-  // a launch holds less than 2^32 threads: larger arrays go round
-  const dim3 grid{unsigned(min64((a.rows * groups + 255) / 256, int64_t(1) << 22))};
   if (bf16)
-    hipLaunchKernelGGL((dropout_kernel<true>), grid, dim3(256), 0, s, a, groups);
+    a.res ? dropout<true, true>(a, s) : dropout<true, false>(a, s);
   else
-    hipLaunchKernelGGL((dropout_kernel<false>), grid, dim3(256), 0, s, a, groups);
+    a.res ? dropout<false, true>(a, s) : dropout<false, false>(a, s);
   return hipGetLastError();
 }
 

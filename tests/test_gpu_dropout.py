@@ -113,6 +113,19 @@ def test_dropout_far_into_memory():
     assert bool((x[rows - 1, cols:] == 1).all()) and bool((x[0, cols:] == 1).all())
 
 
+def test_dropout_of_more_groups_than_a_launch_counts():
+    """2^31 groups to a launch: rows on both sides of the second one's start."""
+    torch, dev = torch_dev()
+    rows, cols = (1 << 30) + 1000, 9                     # two groups a row
+    say(f"[dropout many] {rows}x{cols}")
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device=dev)
+    _run(x, cols, None, 0, rows, cols, "bf16", 0.5, 11, 12, x, cols)
+    some = [0, (1 << 30) - 1, 1 << 30, (1 << 30) + 1, rows - 1]
+    keep, p16 = ob.dropout_keep(rows, cols, 0.5, 11, 12, only=some)
+    got = np.stack([out_to_f64(x[r].contiguous(), "bf16") for r in some])
+    assert np.array_equal(got, keep * 2.0)
+
+
 def test_dropout_in_a_graph():
     torch, dev = torch_dev()
     x = torch.randn(40, 300, device=dev).to(torch.bfloat16)
