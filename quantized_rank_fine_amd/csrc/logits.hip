@@ -125,10 +125,11 @@ struct Held {
   __device__ __forceinline__ static int32_t first(int g) {
     return (g * threads + int(threadIdx.x)) * 8;
   }
-  // the groups [from, from + words) of a row, from < whole or 0
-  __device__ __forceinline__ void load(const char *row, const Cut<BF16> &k, int32_t from) {
-    const int32_t last = k.whole - 8;
-    if (last >= 0) {
+  // the words [from, end) of the groups of a row, at most `words` of them
+  __device__ __forceinline__ void load(const char *row, const Cut<BF16> &k, int32_t from,
+                                       int32_t end) {
+    const int32_t last = end - 8;
+    if (from < end) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const int32_t v = from + first(g);
@@ -146,7 +147,7 @@ struct Held {
       const int32_t v = k.one(int32_t(threadIdx.x));
       if (v < k.V) one = load1<BF16>(row, v);
     }
-    if (from + words > last) {
+    if (from + words > end) {
 #pragma unroll
       for (int g = 0; g < NG; ++g)
         if (from + first(g) > last) {
@@ -296,20 +297,29 @@ __device__ __forceinline__ RowResult finished(Stat a, const char *row, int32_t V
   return row_result(a, off, xy, scale);
 }
 
+// The first words of a row that Held takes in chunks: what remains past whole
+// chunks, so that the last chunk is a full one.
+template <int32_t words>
+__device__ __forceinline__ int32_t first_chunk(int32_t whole) {
+  return whole <= words ? whole : (whole - 1) % words + 1;
+}
+
 // A row's results: its chunks summed one after the other.  h holds the last
-// chunk afterwards (the whole row where it is the only one).
+// chunk afterwards (ONE: the row).
 template <bool ENT, bool ONE, bool BF16, int threads, int NG>
 __device__ __forceinline__ RowResult row_stat(Held<BF16, threads, NG> &h, const char *row,
                                               int32_t V, int32_t y, float scale, Stat *red) {
   const float c = scale * kLog2e;
   Stat a = {-INFINITY, 0.0f, 0.0f};
   const Cut<BF16> k(row, V);
-  h.load(row, k, 0);
+  int32_t end = ONE ? k.whole : first_chunk<Held<BF16, threads, NG>::words>(k.whole);
+  h.load(row, k, 0, end);
   const float xy = load1<BF16>(row, uint32_t(y));
   add_chunk<ENT>(a, h, c);
-  for (int32_t from = h.words; !ONE && from < k.whole; from += h.words) {
-    h.load(row, k, from);
+  while (!ONE && end < k.whole) {
+    h.load(row, k, end, end + h.words);
     add_chunk<ENT>(a, h, c);
+    end += h.words;
   }
   a = joined_block<threads>(a, c, red);
   return finished<BF16, threads>(a, row, V, xy, scale, red);
@@ -422,29 +432,29 @@ __global__ __launch_bounds__(threads) void logp_bwd_kernel(LogitRows a, const fl
   }
 }
 
-// The gradient of a row whose words h holds, or, where the row is longer than
-// that, of the row read again (each word by the lane that then overwrites it).
+// The gradient of a row.  h holds its last chunk (ONE: the row); the words
+// before that are read again, each by the lane that then overwrites it.
 template <bool ENT, bool ONE, bool BF16, int threads, int NG>
 __device__ __forceinline__ void row_grad(Held<BF16, threads, NG> &h, const char *row, char *out,
                                          int32_t V, int32_t y, float m, float c,
                                          const GradCoef &k) {
   const Cut<BF16> q(row, V);
-  if (ONE) {
-    h.keep();
+  const int32_t from = ONE || q.whole <= h.words ? 0 : q.whole - h.words;
+  h.keep();
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int32_t v = h.first(i);
-      if (v < q.whole) {
-        float e[8];
-        h.get(i, e);
-        grad<ENT>(e, y - q.head - v, m, c, k);
-        store8<BF16>(out, q.head + v, e);
-      }
-      // one group's words unpacked at a time
-      __builtin_amdgcn_sched_barrier(0);
+  for (int i = 0; i < NG; ++i) {
+    const int32_t v = from + h.first(i);
+    if (v < q.whole) {
+      float e[8];
+      h.get(i, e);
+      grad<ENT>(e, y - q.head - v, m, c, k);
+      store8<BF16>(out, q.head + v, e);
     }
-  } else {
-    for (int32_t v = int32_t(threadIdx.x) * 8; v < q.whole; v += threads * 8) {
+    // one group's words unpacked at a time
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (!ONE) {
+    for (int32_t v = int32_t(threadIdx.x) * 8; v < from; v += threads * 8) {
       float e[8];
       load8<BF16>(row, q.head + v, e);
       grad<ENT>(e, y - q.head - v, m, c, k);
@@ -521,7 +531,7 @@ __global__ __launch_bounds__(kPartThreads) void part_kernel(LogitRows a, const f
   const int32_t from = int32_t(blockIdx.x) * h.words;
   Stat s = {-INFINITY, 0.0f, 0.0f};
   if (from == 0 || from < k.whole) {
-    h.load(row, k, from);
+    h.load(row, k, from, from + h.words < k.whole ? from + h.words : k.whole);
     add_chunk<ENT>(s, h, c);
   }
   s = joined_block<kPartThreads>(s, c, red);
