@@ -732,7 +732,7 @@ qlora_status qlora_token_logp_bwd(const void *logits, int64_t ld, int64_t T, int
 
 size_t qlora_pref_workspace_bytes(int64_t P, int64_t T) {
   if (P < 1 || P > kMaxPairs || T < 0 || T > kMaxVec) return 0;
-  return size_t(2 * P) * size_t(pref_splits(P, T)) * 2 * sizeof(double);
+  return size_t(pref_partials(P, T)) * sizeof(double);
 }
 
 qlora_status qlora_pref_loss(const float *logp, const float *ref, const uint8_t *mask,

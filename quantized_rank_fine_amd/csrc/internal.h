@@ -336,14 +336,14 @@ hipError_t launch_policy(const float *logp, const float *entropy, int64_t T,
                          const PolicyTokens &t, const PolicyParams &p, float *out, float *dlogp,
                          float *dentropy, double *partial, hipStream_t s);
 
-// Preference loss.  partial: 2 P pref_splits(P, T) (sum, count) pairs of
-// doubles, unused (may be null) when pref_splits is 0 (one workgroup).
+// Preference loss.  partial: pref_partials(P, T) doubles, unused (may be null)
+// when that is 0 (one workgroup).
 struct PrefParams {
   int kind;
   float beta, margin, smoothing;
   int average;
 };
-int64_t pref_splits(int64_t P, int64_t T);
+int64_t pref_partials(int64_t P, int64_t T);
 hipError_t launch_pref(const float *logp, const float *ref, const uint8_t *mask,
                        const int64_t *cu, int64_t P, int64_t T, const PrefParams &p, float *loss,
                        float *rewards, float *dlogp, double *partial, hipStream_t s);

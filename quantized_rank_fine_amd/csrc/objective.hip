@@ -105,11 +105,13 @@ constexpr int64_t kTermsLone = 16384;   // terms that one workgroup adds up
 
 // A unit of work is one wavefront's: a slice of one answer.  The slices' sums
 // and counts ("partials") join the two passes.  Few tokens: one workgroup holds
-// the partials in LDS between its two passes.  Many: two launches, partials in
-// the workspace.
+// the partials in LDS between its two passes.  Many pairs of some length: a
+// workgroup to a pair, and a second launch for the mean loss.  Else: one launch
+// for the sums and one for the gradients, partials in the workspace.
 constexpr int kPrefThreads = 256;        // of the two launches
 constexpr int64_t kPrefLoneTokens = 8192, kPrefLonePairs = 128;
 constexpr int64_t kPrefSlice = 1024;     // tokens of a slice, four quads to a lane
+constexpr int64_t kPrefMeanPairs = 512;
 constexpr int64_t kPrefUnits = 16384;    // slices, when answers are cut at all
 
 struct PairLoss {
@@ -209,8 +211,6 @@ __device__ __forceinline__ f32x4_t load_quad(const float *v, const Quad &q) {
 
 // The quads of a slice, N of a lane at a time: straight-line loads (past the
 // slice's end the last quad again, nothing of it counted).
-constexpr int kPrefQuads = kPrefSlice / 256;
-
 __device__ __forceinline__ int32_t quad_at(const Span &s, int32_t t, int i) {
   return t + 256 * i < s.last ? t + 256 * i : s.last;
 }
@@ -296,6 +296,13 @@ __device__ __forceinline__ int lanes_for(int n) {
   return n <= 1 ? 1 : n >= 33 ? 64 : 1 << (32 - __builtin_clz(n - 1));
 }
 
+// dloss / dlogp of an answer's counted tokens.
+__device__ __forceinline__ float answer_grad(const PrefArgs &a, const PairLoss &l, double count,
+                                             bool rejected) {
+  const float g = (rejected ? -l.dh : l.dh) / float(a.P);
+  return a.p.average && count > 0.0 ? g / float(count) : g;
+}
+
 // Unit u's gradient; slice 0 also writes the answer's reward.  Its pair's loss.
 template <int N>
 __device__ __forceinline__ float unit_grad(const PrefArgs &a, const Partial *partial, int32_t u,
@@ -308,9 +315,7 @@ __device__ __forceinline__ float unit_grad(const PrefArgs &a, const Partial *par
   const Partial r = total(a, partial, P + k, n, lane % lanes, lanes);
   const Partial &own = i < P ? c : r;
   const PairLoss l = pair_loss(a.p, float(c.sum - r.sum));
-  float g = l.dh / float(a.P);
-  if (i >= P) g = -g;
-  if (a.p.average && own.count > 0.0) g /= float(own.count);
+  const float g = answer_grad(a, l, own.count, i >= P);
   if (j == 0 && lane == 0) a.rewards[i] = float(a.p.beta * own.sum);
   slice_grad<N>(a, own_slice, g);
   return l.loss;
@@ -364,25 +369,61 @@ __global__ __launch_bounds__(1024) void pref_lone_kernel(PrefArgs a, int n) {
   }
 }
 
+// A pair to a workgroup: half of its wavefronts to each answer.  losses [P]
+// receives the pairs' losses for pref_mean_kernel.
+__global__ __launch_bounds__(1024) void pref_pair_kernel(PrefArgs a, double *losses) {
+  __shared__ Partial partial[16];
+  const int wave = wave_index(), lane = threadIdx.x % 64, side = wave / 8;
+  const int32_t k = int32_t(blockIdx.x), i = side ? int32_t(a.P) + k : k;
+  const Span s = slice(answer(a, i), wave % 8, 8);
+  const Partial mine = slice_sum<2>(a, s);
+  if (lane == 0) partial[wave] = mine;
+  __syncthreads();
+  const Partial c = total(a, partial, 0, 8, lane % 8, 8), r = total(a, partial, 1, 8, lane % 8, 8);
+  const PairLoss l = pair_loss(a.p, float(c.sum - r.sum));
+  const Partial &own = side ? r : c;
+  slice_grad<2>(a, s, answer_grad(a, l, own.count, side));
+  if (wave % 8 == 0 && lane == 0) a.rewards[i] = float(a.p.beta * own.sum);
+  if (threadIdx.x == 0) losses[k] = l.loss;
+  zero_outside(a, int64_t(blockIdx.x) * 1024 + threadIdx.x, int64_t(gridDim.x) * 1024);
+}
+
+__global__ __launch_bounds__(1024) void pref_mean_kernel(const double *losses, int64_t P,
+                                                         float *loss) {
+  __shared__ double red[16];
+  double s[1] = {};
+#pragma unroll 4
+  for (int64_t k = threadIdx.x; k < P; k += 1024) s[0] += losses[k];
+  block_sums<1, 1024>(s, red);
+  if (threadIdx.x == 0) loss[0] = float(s[0] / double(P));
+}
+
+template <int N>
 __global__ __launch_bounds__(kPrefThreads) void pref_sum_kernel(PrefArgs a, int n, int32_t units,
                                                                 Partial *partial) {
   const int32_t u = int32_t(blockIdx.x) * (kPrefThreads / 64) + wave_index();
   if (u >= units) return;
-  const Partial s = unit_sum<kPrefQuads>(a, u, n);
+  const Partial s = unit_sum<N>(a, u, n);
   if (threadIdx.x % 64 == 0) partial[u] = s;
 }
 
-// The last workgroup takes the mean loss.
+// losses != null: the pairs' losses go there, for pref_mean_kernel; else an
+// extra, last workgroup takes the mean.
+template <int N>
 __global__ __launch_bounds__(kPrefThreads) void pref_grad_kernel(PrefArgs a, int n, int32_t units,
-                                                                 const Partial *partial) {
+                                                                 const Partial *partial,
+                                                                 double *losses) {
   __shared__ double red[kPrefThreads / 64];
-  const int64_t work = int64_t(gridDim.x) - 1;
+  const int64_t work = losses ? int64_t(gridDim.x) : int64_t(gridDim.x) - 1;
   if (blockIdx.x == work) {
     mean_loss<kPrefThreads>(a, partial, n, red);
     return;
   }
   const int32_t u = int32_t(blockIdx.x) * (kPrefThreads / 64) + wave_index();
-  if (u < units) unit_grad<kPrefQuads>(a, partial, u, n);
+  if (u < units) {
+    const float l = unit_grad<N>(a, partial, u, n);
+    if (losses && u < int32_t(a.P) * n && u % n == 0 && threadIdx.x % 64 == 0) losses[u / n] = l;
+  }
   zero_outside(a, int64_t(blockIdx.x) * kPrefThreads + threadIdx.x, work * kPrefThreads);
 }
 
@@ -423,15 +464,32 @@ hipError_t launch_sum_terms(const float *terms, int64_t n, float *out, double *p
 
 namespace {
 
+// Enough pairs to fill the chip with one workgroup each, and enough tokens in
+// a pair for its 16 wavefronts.  Measured, us a call, by pairs and by slices:
+// 256 pairs of 4608 tokens 9.6, 13.3; 64 of 18000 13.6, 14.7; 2048 of 563
+// 30.6, 16.5.
+bool pref_paired(int64_t P, int64_t T) {
+  return P >= 64 && T / P >= 1024 && T / P <= 65536;
+}
+
 bool pref_lone(int64_t P, int64_t T) { return T <= kPrefLoneTokens && P <= kPrefLonePairs; }
 
 }  // namespace
 
+namespace {
+
 int64_t pref_splits(int64_t P, int64_t T) {
-  if (pref_lone(P, T)) return 0;
   const int64_t by_size = (T / (2 * P) + kPrefSlice - 1) / kPrefSlice, most = kPrefUnits / (2 * P);
   const int64_t n = min64(by_size, most);
   return n < 1 ? 1 : n;
+}
+
+}  // namespace
+
+int64_t pref_partials(int64_t P, int64_t T) {
+  if (pref_lone(P, T)) return 0;
+  if (pref_paired(P, T)) return P;
+  return 4 * P * pref_splits(P, T) + (P > kPrefMeanPairs ? P : 0);
 }
 
 hipError_t launch_pref(const float *logp, const float *ref, const uint8_t *mask,
@@ -444,13 +502,29 @@ hipError_t launch_pref(const float *logp, const float *ref, const uint8_t *mask,
     hipLaunchKernelGGL(pref_lone_kernel, dim3(1), dim3(1024), 0, s, a, n);
     return hipGetLastError();
   }
+  if (pref_paired(P, T)) {
+    hipLaunchKernelGGL(pref_pair_kernel, dim3(unsigned(P)), dim3(1024), 0, s, a, partial);
+    hipLaunchKernelGGL(pref_mean_kernel, dim3(1), dim3(1024), 0, s, partial, P, loss);
+    return hipGetLastError();
+  }
   const int64_t n = pref_splits(P, T), units = 2 * P * n;
   const unsigned blocks = unsigned((units + kPrefThreads / 64 - 1) / (kPrefThreads / 64));
   Partial *part = reinterpret_cast<Partial *>(partial);
-  hipLaunchKernelGGL(pref_sum_kernel, dim3(blocks), dim3(kPrefThreads), 0, s, a, int(n),
-                     int32_t(units), part);
-  hipLaunchKernelGGL(pref_grad_kernel, dim3(blocks + 1), dim3(kPrefThreads), 0, s, a, int(n),
-                     int32_t(units), part);
+  // one workgroup's mean over the partials of many pairs would outlast the rest
+  double *losses = P > kPrefMeanPairs ? partial + 2 * units : nullptr;
+#define SLICES(N)                                                                               \
+  do {                                                                                          \
+    hipLaunchKernelGGL((pref_sum_kernel<N>), dim3(blocks), dim3(kPrefThreads), 0, s, a, int(n), \
+                       int32_t(units), part);                                                   \
+    hipLaunchKernelGGL((pref_grad_kernel<N>), dim3(blocks + !losses), dim3(kPrefThreads), 0, s, \
+                       a, int(n), int32_t(units), part, losses);                                \
+  } while (0)
+  // quads of a lane in flight: as a slice of average length needs
+  if (T / units <= 256) SLICES(1);
+  else SLICES(kPrefSlice / 256);
+#undef SLICES
+  if (losses)
+    hipLaunchKernelGGL(pref_mean_kernel, dim3(1), dim3(1024), 0, s, losses, P, loss);
   return hipGetLastError();
 }
 

@@ -414,6 +414,8 @@ LENGTHS = {
     "one token": [1, 1], "empty": [0, 0], "half empty": [5, 0, 0, 7],
     "short": [3, 1, 64, 65, 200, 17], "many": list(range(0, 200)),
     "long": [9001, 1, 30000, 4097], "very long": [150000, 70001],
+    "pairs": [700 + 11 * i for i in range(130)], "many short": [i % 90 for i in range(700)],
+    "crowd": [i % 5 for i in range(1400)],
 }
 
 
@@ -425,7 +427,7 @@ def test_pref_loss(name, kind, average, ref, masked):
     say(f"[pref] {name} {kind} average={average} ref={ref} mask={masked}")
     g = np.random.default_rng(len(name) + 10 * average)
     lens = np.array(LENGTHS[name])
-    if name == "many":
+    if name in ("many", "pairs", "many short", "crowd"):
         lens = g.permutation(lens)
     before, after = (3, 5) if masked else (0, 0)        # tokens outside every answer
     cu = before + np.concatenate([[0], np.cumsum(lens)])
