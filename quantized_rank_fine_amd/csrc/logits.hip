@@ -88,9 +88,13 @@ __device__ __forceinline__ void store8(char *row, uint32_t v, const float (&e)[8
   if (BF16) {
     const u32x4_t u = {pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
                        pack_bf16x2(e[6], e[7])};
-    __builtin_memcpy(row + v * 2u, &u, 16);
+    store16_past(row + v * 2u, u);
   } else {
-    __builtin_memcpy(row + v * 4u, e, 32);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      store16_past(row + v * 4u + 16 * i,
+                   u32x4_t{__float_as_uint(e[4 * i]), __float_as_uint(e[4 * i + 1]),
+                           __float_as_uint(e[4 * i + 2]), __float_as_uint(e[4 * i + 3])});
   }
 }
 
