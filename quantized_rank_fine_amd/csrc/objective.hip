@@ -95,7 +95,7 @@ __global__ __launch_bounds__(1024) void sum4_kernel(const F *v, int64_t n, float
   put_sums(s, out, partial);
 }
 
-constexpr int64_t kTermsLone = 16384;   // terms that one workgroup adds up
+constexpr int64_t kTermsLone = 8192;    // terms that one workgroup adds up alone
 
 // -------------------------------------------------------- preference loss
 //
@@ -280,6 +280,7 @@ __device__ __forceinline__ Partial unit_sum(const PrefArgs &a, int32_t u, int n)
 __device__ __forceinline__ Partial total(const PrefArgs &a, const Partial *partial, int32_t i,
                                          int n, int at, int lanes) {
   Partial r = {0.0, 0.0};
+#pragma unroll 4
   for (int j = at; j < n; j += lanes) {
     r.sum += partial[int64_t(i) * n + j].sum;
     r.count += partial[int64_t(i) * n + j].count;
@@ -321,11 +322,14 @@ __device__ __forceinline__ float unit_grad(const PrefArgs &a, const Partial *par
   return l.loss;
 }
 
-// The mean loss, by one workgroup: a pair to `lanes` lanes.
+// The mean loss, by one workgroup: a pair to so many lanes that every pair has
+// some at once, up to one for each of its slices.
 template <int threads>
 __device__ __forceinline__ void mean_loss(const PrefArgs &a, const Partial *partial, int n,
                                           double *red) {
-  const int lanes = lanes_for(n), at = threadIdx.x % lanes;
+  int lanes = lanes_for(n);
+  while (lanes > 1 && int64_t(lanes) * a.P > threads) lanes /= 2;
+  const int at = threadIdx.x % lanes;
   double sum[1] = {};
   const int32_t P = int32_t(a.P);
   for (int32_t first = 0; first < P; first += threads / lanes) {
@@ -449,7 +453,7 @@ hipError_t launch_policy(const float *logp, const float *entropy, int64_t T,
 }
 
 int64_t terms_blocks(int64_t n) {
-  return n <= kTermsLone ? 1 : min64((n + kTermsLone - 1) / kTermsLone, 1024);
+  return n <= kTermsLone ? 1 : min64((n + 1023) / 1024, 1024);
 }
 
 hipError_t launch_sum_terms(const float *terms, int64_t n, float *out, double *partial,
