@@ -110,7 +110,10 @@ constexpr int64_t kTermsLone = 8192;    // terms that one workgroup adds up alon
 // for the sums and one for the gradients, partials in the workspace.
 constexpr int kPrefThreads = 256;        // of the two launches
 constexpr int64_t kPrefLoneTokens = 8192, kPrefLonePairs = 128;
-constexpr int64_t kPrefSlice = 1024;     // tokens of a slice, four quads to a lane
+// Tokens of a slice, two quads to a lane.  us a call, 256 / 512 / 1024 / 2048:
+// 53 pairs of 44000 tokens 19.1 / 15.8 / 15.5 / 19.0, two of 147000 10.1 /
+// 10.4 / 11.4 / 15.1, 16 of 67000 12.2 / 11.2 / 11.8 / 15.9.
+constexpr int64_t kPrefSlice = 512;
 constexpr int64_t kPrefMeanPairs = 512;
 constexpr int64_t kPrefUnits = 16384;    // slices, when answers are cut at all
 
