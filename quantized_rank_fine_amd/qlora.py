@@ -182,14 +182,20 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_raw = None      # (device index -> stream handle, current device), once initialised
+
+
 def _stream(stream):
+    global _current_raw
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    if torch.cuda.is_initialized():
-        # the same handle as below without building a Stream object (0.2 us, not 2.7)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return torch.cuda.current_stream().cuda_stream
+    if _current_raw is None:
+        import torch
+        torch.cuda.current_stream()          # initialises the runtime, or says that there is none
+        _current_raw = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    # torch.cuda.current_stream().cuda_stream without the Stream object (0.2 us, not 2.7)
+    handle, device = _current_raw
+    return handle(device())
 
 
 def _check(status, where):
