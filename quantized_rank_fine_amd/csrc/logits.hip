@@ -15,8 +15,8 @@
 //
 // HBM-bound: the forward reads each scored row once, the gradient also writes
 // each row once.  Rows of an odd V start at any element: a row is cut into up
-// to 7 words before its first 16-byte boundary, groups of 8, and up to 7 after
-// the last whole group.
+// to 7 words before its first 16-byte boundary, groups of 16 bytes, and up to 7
+// words after the last whole group.
 #include "objective.h"
 
 namespace qlora {
@@ -44,8 +44,8 @@ __device__ __forceinline__ int64_t row_index() {
   return int64_t(blockIdx.z) * kRowsY + blockIdx.y;
 }
 
-// Word v of a row, and words v .. v + 7 at their element's alignment (V is at
-// most 2^24, so a row's offsets fit 32 bits).
+// Word v of a row, at its alignment (V is at most 2^24, so a row's offsets fit
+// 32 bits).
 template <bool BF16>
 __device__ __forceinline__ float load1(const char *row, uint32_t v) {
   if (BF16) {
@@ -58,19 +58,29 @@ __device__ __forceinline__ float load1(const char *row, uint32_t v) {
   return f;
 }
 
+// A group: the 16 bytes that one load or store of a lane moves.
 template <bool BF16>
-__device__ __forceinline__ void load8(const char *row, uint32_t v, float (&e)[8]) {
-  if (BF16) {
-    u32x4_t u;
-    __builtin_memcpy(&u, row + v * 2u, 16);
+constexpr int kGroup = BF16 ? 8 : 4;
+
+template <bool BF16>
+__device__ __forceinline__ void unpack(u32x4_t u, float (&e)[kGroup<BF16>]) {
+  if constexpr (BF16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       e[2 * i] = bf16_lo_to_f32(u[i]);
       e[2 * i + 1] = bf16_hi_to_f32(u[i]);
     }
   } else {
-    __builtin_memcpy(e, row + v * 4u, 32);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = __uint_as_float(u[i]);
   }
+}
+
+template <bool BF16>
+__device__ __forceinline__ u32x4_t load_group(const char *row, uint32_t v) {
+  u32x4_t u;
+  __builtin_memcpy(&u, row + v * (BF16 ? 2u : 4u), 16);
+  return u;
 }
 
 template <bool BF16>
@@ -84,22 +94,21 @@ __device__ __forceinline__ void store1(char *row, uint32_t v, float e) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store8(char *row, uint32_t v, const float (&e)[8]) {
-  if (BF16) {
-    const u32x4_t u = {pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
-                       pack_bf16x2(e[6], e[7])};
-    store16_past(row + v * 2u, u);
+__device__ __forceinline__ void store_group(char *row, uint32_t v,
+                                            const float (&e)[kGroup<BF16>]) {
+  u32x4_t u;
+  if constexpr (BF16) {
+    u = u32x4_t{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                pack_bf16x2(e[6], e[7])};
   } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      store16_past(row + v * 4u + 16 * i,
-                   u32x4_t{__float_as_uint(e[4 * i]), __float_as_uint(e[4 * i + 1]),
-                           __float_as_uint(e[4 * i + 2]), __float_as_uint(e[4 * i + 3])});
+    for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(e[i]);
   }
+  store16_past(row + v * (BF16 ? 2u : 4u), u);
 }
 
-// The cut of a row of V words at address `row`: `head` words, groups of 8 words
-// from there on, `whole` words in all, and the rest.  Head and rest ("ones")
+// The cut of a row of V words at address `row`: `head` words, groups from there
+// on, `whole` words in all, and the rest.  Head and rest ("ones")
 // are one word to a lane, the rest in lanes 0 .. 7, the head in 8 .. 15.
 template <bool BF16>
 struct Cut {
@@ -107,7 +116,7 @@ struct Cut {
   __device__ __forceinline__ Cut(const char *row, int32_t words) : V(words) {
     const int32_t off = int32_t(-reinterpret_cast<uintptr_t>(row) & 15u) / (BF16 ? 2 : 4);
     head = off < V ? off : V;
-    whole = (V - head) / 8 * 8;
+    whole = (V - head) / kGroup<BF16> * kGroup<BF16>;
   }
   // the word of lane `at` among the ones, or V
   __device__ __forceinline__ int32_t one(int32_t at) const {
@@ -116,34 +125,29 @@ struct Cut {
   }
 };
 
-// Words of a row in registers: group g of a lane is the 8 words from
-// head + from + 8 (g threads + lane) on, as they lie in memory.  Groups past
+// Words of a row in registers, 8 NG to a lane: group g of a lane is the one
+// g threads + lane groups after head + from, as it lies in memory.  Groups past
 // the last whole one load that one again and are masked to -inf, so every load
 // is whole and none leaves the row.  The ones come with the row's first chunk.
 template <bool BF16, int threads, int NG>
 struct Held {
   static constexpr int32_t words = threads * 8 * NG;
-  u32x4_t q[BF16 ? NG : 2 * NG];
+  static constexpr int W = kGroup<BF16>, G = 8 * NG / W;
+  u32x4_t q[G];
   float one;
 
   __device__ __forceinline__ static int32_t first(int g) {
-    return (g * threads + int(threadIdx.x)) * 8;
+    return (g * threads + int(threadIdx.x)) * W;
   }
   // the words [from, end) of the groups of a row, at most `words` of them
   __device__ __forceinline__ void load(const char *row, const Cut<BF16> &k, int32_t from,
                                        int32_t end) {
-    const int32_t last = end - 8;
+    const int32_t last = end - W;
     if (from < end) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+      for (int g = 0; g < G; ++g) {
         const int32_t v = from + first(g);
-        const uint32_t at = uint32_t(k.head + (v <= last ? v : last));
-        if (BF16) {
-          __builtin_memcpy(&q[g], row + at * 2u, 16);
-        } else {
-          __builtin_memcpy(&q[2 * g], row + at * 4u, 16);
-          __builtin_memcpy(&q[2 * g + 1], row + at * 4u + 16u, 16);
-        }
+        q[g] = load_group<BF16>(row, uint32_t(k.head + (v <= last ? v : last)));
       }
     }
     one = -INFINITY;
@@ -153,11 +157,10 @@ struct Held {
     }
     if (from + words > end) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+      for (int g = 0; g < G; ++g)
         if (from + first(g) > last) {
           const uint32_t w = BF16 ? 0xff80ff80u : 0xff800000u;
-          q[BF16 ? g : 2 * g] = u32x4_t{w, w, w, w};
-          if (!BF16) q[2 * g + 1] = u32x4_t{w, w, w, w};
+          q[g] = u32x4_t{w, w, w, w};
         }
     }
   }
@@ -165,19 +168,7 @@ struct Held {
   // unpacked words of one pass for the next, twice the registers and more.
   __device__ __forceinline__ void keep() {
 #pragma unroll
-    for (int i = 0; i < (BF16 ? NG : 2 * NG); ++i) asm volatile("" : "+v"(q[i]));
-  }
-  __device__ __forceinline__ void get(int g, float (&e)[8]) const {
-    if (BF16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[2 * i] = bf16_lo_to_f32(q[g][i]);
-        e[2 * i + 1] = bf16_hi_to_f32(q[g][i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = __uint_as_float(q[2 * g + i / 4][i % 4]);
-    }
+    for (int i = 0; i < G; ++i) asm volatile("" : "+v"(q[i]));
   }
 };
 
@@ -213,24 +204,25 @@ __device__ __forceinline__ Stat raised(const Stat &a, float top, float c) {
 // A lane's share of a chunk into its running sums.
 template <bool ENT, bool BF16, int threads, int NG>
 __device__ __forceinline__ void add_chunk(Stat &a, Held<BF16, threads, NG> &h, float c) {
+  constexpr int W = kGroup<BF16>, G = 8 * NG / W;
   float top = fmaxf(a.m, h.one);
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    float e[8];
-    h.get(g, e);
+  for (int g = 0; g < G; ++g) {
+    float e[W];
+    unpack<BF16>(h.q[g], e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, e[i]);
+    for (int i = 0; i < W; ++i) top = fmaxf(top, e[i]);
   }
   a = raised(a, top, c);
   h.keep();
   const float M = reference(top, c);
   add<ENT>(a, h.one, c, M);
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    float e[8];
-    h.get(g, e);
+  for (int g = 0; g < G; ++g) {
+    float e[W];
+    unpack<BF16>(h.q[g], e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) add<ENT>(a, e[i], c, M);
+    for (int i = 0; i < W; ++i) add<ENT>(a, e[i], c, M);
   }
 }
 
@@ -360,10 +352,11 @@ __device__ __forceinline__ void grad(float (&e)[N], int32_t label, float m, floa
 // Zeros, a row's gradient where there is none.
 template <bool BF16, int threads>
 __device__ __forceinline__ void zero_row(char *out, int32_t V) {
-  const float e[8] = {};
+  constexpr int W = kGroup<BF16>;
+  const float e[W] = {};
   const Cut<BF16> k(out, V);
-  for (int32_t v = int32_t(threadIdx.x) * 8; v < k.whole; v += threads * 8)
-    store8<BF16>(out, k.head + v, e);
+  for (int32_t v = int32_t(threadIdx.x) * W; v < k.whole; v += threads * W)
+    store_group<BF16>(out, k.head + v, e);
   const int32_t one = k.one(int32_t(threadIdx.x));
   if (one < V) store1<BF16>(out, one, 0.0f);
 }
@@ -402,24 +395,27 @@ __global__ __launch_bounds__(threads) void logp_bwd_kernel(LogitRows a, const fl
   const char *row = row_at<BF16>(a.x, t * a.ld);
   char *out = row_at<BF16>(dx, t * ldd);
   const Cut<BF16> q(row, V);
-  const int32_t from = (int32_t(blockIdx.x) * threads * NG + int32_t(threadIdx.x)) * 8;
+  constexpr int W = kGroup<BF16>, G = 8 * NG / W;
+  const int32_t from = (int32_t(blockIdx.x) * threads * G + int32_t(threadIdx.x)) * W;
   const int32_t one = blockIdx.x == 0 ? q.one(int32_t(threadIdx.x)) : V;
   const int64_t y = a.labels[t];
   const float m = stats[2 * t], z = stats[2 * t + 1];
   const float gt = g[t], gh = ENT ? g_entropy[t] : 0.0f;
   if (y >= 0 && y < V && m != -INFINITY && (gt != 0.0f || gh != 0.0f)) {
-    float e[NG][8];
+    u32x4_t u[G];
 #pragma unroll
-    for (int i = 0; i < NG; ++i)
-      if (from + i * threads * 8 < q.whole)
-        load8<BF16>(row, q.head + from + i * threads * 8, e[i]);
+    for (int i = 0; i < G; ++i)
+      if (from + i * threads * W < q.whole)
+        u[i] = load_group<BF16>(row, q.head + from + i * threads * W);
     const GradCoef k = grad_coef(a.scale, gt, gh, ENT ? entropy[t] : 0.0f, z);
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int32_t v = q.head + from + i * threads * 8;
-      if (from + i * threads * 8 < q.whole) {
-        grad<ENT>(e[i], int32_t(y) - v, m, c, k);
-        store8<BF16>(out, v, e[i]);
+    for (int i = 0; i < G; ++i) {
+      const int32_t v = q.head + from + i * threads * W;
+      if (from + i * threads * W < q.whole) {
+        float e[W];
+        unpack<BF16>(u[i], e);
+        grad<ENT>(e, int32_t(y) - v, m, c, k);
+        store_group<BF16>(out, v, e);
       }
     }
     if (one < V) {
@@ -428,10 +424,11 @@ __global__ __launch_bounds__(threads) void logp_bwd_kernel(LogitRows a, const fl
       store1<BF16>(out, one, d[0]);
     }
   } else {
-    const float e[8] = {};
+    const float e[W] = {};
 #pragma unroll
-    for (int i = 0; i < NG; ++i)
-      if (from + i * threads * 8 < q.whole) store8<BF16>(out, q.head + from + i * threads * 8, e);
+    for (int i = 0; i < G; ++i)
+      if (from + i * threads * W < q.whole)
+        store_group<BF16>(out, q.head + from + i * threads * W, e);
     if (one < V) store1<BF16>(out, one, 0.0f);
   }
 }
@@ -443,26 +440,27 @@ __device__ __forceinline__ void row_grad(Held<BF16, threads, NG> &h, const char 
                                          int32_t V, int32_t y, float m, float c,
                                          const GradCoef &k) {
   const Cut<BF16> q(row, V);
+  constexpr int W = kGroup<BF16>, G = 8 * NG / W;
   const int32_t from = ONE || q.whole <= h.words ? 0 : q.whole - h.words;
   h.keep();
 #pragma unroll
-  for (int i = 0; i < NG; ++i) {
+  for (int i = 0; i < G; ++i) {
     const int32_t v = from + h.first(i);
     if (v < q.whole) {
-      float e[8];
-      h.get(i, e);
+      float e[W];
+      unpack<BF16>(h.q[i], e);
       grad<ENT>(e, y - q.head - v, m, c, k);
-      store8<BF16>(out, q.head + v, e);
+      store_group<BF16>(out, q.head + v, e);
     }
     // one group's words unpacked at a time
     __builtin_amdgcn_sched_barrier(0);
   }
   if (!ONE) {
-    for (int32_t v = int32_t(threadIdx.x) * 8; v < from; v += threads * 8) {
-      float e[8];
-      load8<BF16>(row, q.head + v, e);
+    for (int32_t v = int32_t(threadIdx.x) * W; v < from; v += threads * W) {
+      float e[W];
+      unpack<BF16>(load_group<BF16>(row, q.head + v), e);
       grad<ENT>(e, y - q.head - v, m, c, k);
-      store8<BF16>(out, q.head + v, e);
+      store_group<BF16>(out, q.head + v, e);
     }
   }
   const int32_t one = q.one(int32_t(threadIdx.x));
