@@ -402,20 +402,18 @@ __global__ __launch_bounds__(threads) void logp_bwd_kernel(LogitRows a, const fl
   const float m = stats[2 * t], z = stats[2 * t + 1];
   const float gt = g[t], gh = ENT ? g_entropy[t] : 0.0f;
   if (y >= 0 && y < V && m != -INFINITY && (gt != 0.0f || gh != 0.0f)) {
-    u32x4_t u[G];
+    float f[G][W];
 #pragma unroll
     for (int i = 0; i < G; ++i)
       if (from + i * threads * W < q.whole)
-        u[i] = load_group<BF16>(row, q.head + from + i * threads * W);
+        unpack<BF16>(load_group<BF16>(row, q.head + from + i * threads * W), f[i]);
     const GradCoef k = grad_coef(a.scale, gt, gh, ENT ? entropy[t] : 0.0f, z);
 #pragma unroll
     for (int i = 0; i < G; ++i) {
       const int32_t v = q.head + from + i * threads * W;
       if (from + i * threads * W < q.whole) {
-        float e[W];
-        unpack<BF16>(u[i], e);
-        grad<ENT>(e, int32_t(y) - v, m, c, k);
-        store_group<BF16>(out, v, e);
+        grad<ENT>(f[i], int32_t(y) - v, m, c, k);
+        store_group<BF16>(out, v, f[i]);
       }
     }
     if (one < V) {
