@@ -544,7 +544,8 @@ size_t qlora_policy_workspace_bytes(int64_t T);
  * qlora_token_logp_fwd, the gradient as in qlora_token_logp_bwd).  With NLL,
  * adv = NULL and weight = 1 / N it is the cross-entropy of N tokens.
  *   logp [T] (output, or NULL; 0 where a token is not scored or its weight is
- *   0); dlogits as in qlora_token_logp_bwd, also in place.
+ *   0); dlogits as in qlora_token_logp_bwd, also in place, and 0 in the rows
+ *   whose coefficients come out 0.
  */
 qlora_status qlora_policy_logits(const void *logits, int64_t ld, int64_t T, int64_t V,
                                  qlora_dtype dt, const int64_t *labels, float scale,

