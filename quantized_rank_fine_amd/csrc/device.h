@@ -44,17 +44,7 @@ __device__ __forceinline__ f32x16_t mfma32x32x16(u32x4_t a, u32x4_t b, f32x16_t 
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
-__host__ __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
-
-// 16 bytes at an element's alignment past the caches' usual order, for large
-// results that are read once, later.  Alone and with a reader of the result
-// behind it (us; the gradient of T x 32000 bf16 logits, T = 1024 / 2048 /
-// 4096): 21.6 / 46.4 / 87.2 and 39.5 / 70.9 / 132, ordinary stores 26.8 / 47.8
-// / 89.9 and 38.8 / 71.2 / 143.
-__device__ __forceinline__ void store16_past(void *p, u32x4_t v) {
-  typedef u32x4_t any_u32x4_t __attribute__((aligned(2)));
-  __builtin_nontemporal_store(v, static_cast<any_u32x4_t *>(p));
-}
+__device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // One Adam (AdamW) step of one element, fp32 (Kingma & Ba, Algorithm 1, with
 // decoupled weight decay):

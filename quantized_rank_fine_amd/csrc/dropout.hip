@@ -16,7 +16,7 @@
 // TB/s); 8192 x 4096 fp32 49.7 us (5.4 TB/s).  Rows off the 16-byte boundary
 // (odd widths) move 3.8 TB/s: a lane's 8 elements are those of its draws, not
 // those of an aligned line.
-#include "device.h"
+#include "objective.h"
 
 namespace qlora {
 namespace {
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, uint32_t gr
   if (n >= count) return;
   const uint32_t row = FLAT ? 0 : n / groups;
   const int64_t j = FLAT ? int64_t(n) * 8 : int64_t(n - row * groups) * 8;
-  const int left = FLAT ? 8 : int(min64(a.cols - j, 8));
+  const int left = FLAT ? 8 : int(least64(a.cols - j, 8));
   float e[8], r[8];
   load8<BF16>(a.x, row * a.ldx + j, left, e);
   if (RES) load8<BF16>(a.res, row * a.ldr + j, left, r);
@@ -126,7 +126,7 @@ void dropout(DropoutArgs a, hipStream_t s) {
   const int64_t rows_each = ((int64_t(1) << 31) / groups);
   const int64_t size = BF16 ? 2 : 4;
   for (int64_t row = 0; row < a.rows; row += rows_each) {
-    const int64_t count = min64(a.rows - row, rows_each) * groups;
+    const int64_t count = least64(a.rows - row, rows_each) * groups;
     DropoutArgs b = a;
     b.x = static_cast<const char *>(a.x) + row * a.ldx * size;
     b.y = static_cast<char *>(a.y) + row * a.ldy * size;

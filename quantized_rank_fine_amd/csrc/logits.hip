@@ -612,7 +612,7 @@ __global__ __launch_bounds__(64) void policy_join_kernel(LogitRows a, PolicyToke
 }
 
 dim3 row_grid(int64_t T, int64_t segments = 1) {
-  return dim3(unsigned(segments), unsigned(min64(T, kRowsY)),
+  return dim3(unsigned(segments), unsigned(least64(T, kRowsY)),
               unsigned((T + kRowsY - 1) / kRowsY));
 }
 

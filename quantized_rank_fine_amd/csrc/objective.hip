@@ -58,7 +58,7 @@ __global__ __launch_bounds__(threads) void policy_kernel(const float *logp, cons
   double s[4] = {};
   const int64_t step = int64_t(gridDim.x) * threads * 4;
   for (int64_t i = (int64_t(blockIdx.x) * threads + threadIdx.x) * 4; i < T; i += step) {
-    const int n = int(min64(T - i, 4));
+    const int n = int(least64(T - i, 4));
     const f32x4_t w = take4(k.weight, i, n, 1.0f), lp = take4(logp, i, n, 0.0f);
     const f32x4_t h = take4(entropy, i, n, 0.0f), adv = take4(k.adv, i, n, 1.0f);
     const f32x4_t old = take4(k.old, i, n, 0.0f), ref = take4(k.ref, i, n, 0.0f);
@@ -162,8 +162,8 @@ struct Span {
 
 __device__ __forceinline__ Span answer(const PrefArgs &a, int32_t i) {
   const int64_t lo = a.cu[i], hi = a.cu[i + 1];
-  const int64_t first = lo < 0 ? 0 : min64(lo, a.T);
-  return {int32_t(first), int32_t(hi < first ? first : min64(hi, a.T))};
+  const int64_t first = lo < 0 ? 0 : least64(lo, a.T);
+  return {int32_t(first), int32_t(hi < first ? first : least64(hi, a.T))};
 }
 
 // Slice j of n of an answer, its inner ends on multiples of four tokens.
@@ -173,8 +173,8 @@ __device__ __forceinline__ Span slice(const Span &s, int32_t j, int32_t n) {
   const int32_t each = int32_t(n == 1 ? tokens : ((tokens + cut - 1) / cut + 3u) & ~3u);
   // (the last slices of a short answer are empty: j * each can pass 2^31)
   const int64_t from = base + int64_t(j) * each;
-  const int32_t lo = int32_t(min64(from, s.last));
-  return {lo < s.first ? s.first : lo, int32_t(min64(from + each, s.last))};
+  const int32_t lo = int32_t(least64(from, s.last));
+  return {lo < s.first ? s.first : lo, int32_t(least64(from + each, s.last))};
 }
 
 struct Partial {
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(kPrefThreads) void pref_grad_kernel(PrefArgs a, int
 }  // namespace
 
 int64_t policy_blocks(int64_t T) {
-  return T <= kPolicyLone ? 1 : min64((T + 4 * kPolicyThreads - 1) / (4 * kPolicyThreads), 2048);
+  return T <= kPolicyLone ? 1 : least64((T + 4 * kPolicyThreads - 1) / (4 * kPolicyThreads), 2048);
 }
 
 hipError_t launch_policy(const float *logp, const float *entropy, int64_t T,
@@ -462,7 +462,7 @@ hipError_t launch_policy(const float *logp, const float *entropy, int64_t T,
 }
 
 int64_t terms_blocks(int64_t n) {
-  return n <= kTermsLone ? 1 : min64((n + 1023) / 1024, 1024);
+  return n <= kTermsLone ? 1 : least64((n + 1023) / 1024, 1024);
 }
 
 hipError_t launch_sum_terms(const float *terms, int64_t n, float *out, double *partial,
@@ -493,7 +493,7 @@ namespace {
 
 int64_t pref_splits(int64_t P, int64_t T) {
   const int64_t by_size = (T / (2 * P) + kPrefSlice - 1) / kPrefSlice, most = kPrefUnits / (2 * P);
-  const int64_t n = min64(by_size, most);
+  const int64_t n = least64(by_size, most);
   return n < 1 ? 1 : n;
 }
 
