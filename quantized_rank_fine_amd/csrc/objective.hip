@@ -14,11 +14,11 @@ namespace {
 
 // ------------------------------------------------------------ policy loss
 
-// Tokens of one workgroup, four to a lane: up to kPolicyLone the tokens are
-// one workgroup's and its sums are the result; past that there is a second
-// launch.
+// Up to kPolicyLone the tokens are one workgroup's and its sums are the result;
+// past that there is a second launch.  us a call, one launch and two: 5000
+// tokens 7.9 and 11.6, 8000 8.7 and 11.5, 12000 10.9 and 11.2.
 constexpr int kPolicyThreads = 256;
-constexpr int64_t kPolicyLone = 4096;
+constexpr int64_t kPolicyLone = 8192;
 
 __device__ __forceinline__ void put_sums(const double (&s)[4], float *out, double *partial) {
   if (threadIdx.x != 0) return;
@@ -114,7 +114,10 @@ constexpr int64_t kTermsLone = 8192;    // terms that one workgroup adds up alon
 // workgroup to a pair, and a second launch for the mean loss.  Else: one launch
 // for the sums and one for the gradients, partials in the workspace.
 constexpr int kPrefThreads = 256;        // of the two launches
-constexpr int64_t kPrefLoneTokens = 8192, kPrefLonePairs = 128;
+// One workgroup where each of its 16 wavefronts has an answer at most.  us a
+// call, so and in two launches: 4 pairs of 2800 tokens 9.0 and 10.1, of 4500
+// 10.4 and 10.0; 16 of 450 10.3 and 10.2; 100 of 112 44.4 and 10.1.
+constexpr int64_t kPrefLoneTokens = 16384, kPrefLonePairs = 8;
 // Tokens of a slice, two quads to a lane.  us a call, 256 / 512 / 1024 / 2048:
 // 53 pairs of 44000 tokens 19.1 / 15.8 / 15.5 / 19.0, two of 147000 10.1 /
 // 10.4 / 11.4 / 15.1, 16 of 67000 12.2 / 11.2 / 11.8 / 15.9.

@@ -415,6 +415,24 @@ def test_policy_logits(T, V, ld, dt, s, at, kind, ent):
     assert np.array_equal(out_to_f64(dx2.contiguous(), dt).reshape(T, V), got)
 
 
+@pytest.mark.parametrize("V", [50, 70001])
+def test_policy_logits_of_nothing(V):
+    """No tokens, and tokens of which none is scored or weighted: zeros."""
+    torch, dev = torch_dev()
+    pol = q.policy_struct(q.OBJ_CLIP, kl_coef=0.1, ent_coef=0.1)
+    out = torch.full((4,), 9.0, device=dev)
+    q.qlora_policy_logits(None, V, 0, V, q.BF16, None, 1.0, None, None, None, None, pol, out, None,
+                          None, V, None, 0)
+    assert not out.any()
+    x, _ = _rows(4, V, V, "f32", 3)
+    x[:] = float("nan")
+    y, w = np.array([-100, V, 0, 5]), np.array([1, 1, 0, 0], np.float32)
+    out, lp, dx, _ = _policy_logits(x, V, "f32", y, 1.0, pol, w, adv=np.full(4, np.nan, np.float32))
+    assert not out.any() and not lp.any() and not dx.any()
+    lp, st, h = _fwd(x[:2].contiguous(), V, "f32", _dev(y[:2]), 1.0)
+    assert not lp.any() and not st.any() and not h.any()
+
+
 def test_policy_logits_gradient_is_the_difference_quotient():
     """Against central differences of the oracle's loss (float64), by logit."""
     T, V = 3, 11
