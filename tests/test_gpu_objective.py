@@ -573,7 +573,7 @@ def test_pref_without_tokens():
 
 # ----------------------------------------------------- graphs and streams
 
-@pytest.mark.parametrize("T,V", [(5, 1000), (3, 40000)])
+@pytest.mark.parametrize("T,V", [(5, 1000), (3, 40000), (3, 140001)])
 def test_graph_replays_and_another_stream(T, V):
     """The whole chain (scoring, preference loss, gradient; policy loss from
     tokens and from logits) captured on a side stream: every replay gives the
