@@ -21,7 +21,8 @@ def _run(x, ldx, res, ldr, rows, cols, dt, p, seed, ctr, y, ldy):
 
 @pytest.mark.parametrize("rows,cols,pad,at", [
     (1, 1, 0, 0), (3, 7, 0, 1), (2, 8, 0, 0), (5, 9, 2, 3), (17, 64, 0, 0), (4, 1000, 24, 0),
-    (33, 257, 0, 0), (2, 4096, 1, 0), (300, 40, 0, 0),
+    (33, 257, 0, 0), (2, 4096, 1, 0), (300, 40, 0, 0), (9, 64, 3, 2), (40, 65, 0, 7), (5, 505, 0, 1),
+    (8, 511, 1, 0), (17, 1002, 0, 5),
 ])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("p,residual", [(0.1, True), (0.5, False), (0.0, True)])
