@@ -182,12 +182,19 @@ struct Stat {
 };
 
 // L is taken as c x - M with M = c m rounded once, in one fused operation:
-// whatever M is, it cancels from log p.  M is 0 where there is no word yet and
-// where c m is too large for it; t then comes out 0 or infinite with m finite
-// and the row is summed again by careful_row.
+// whatever M is, it cancels from log p.  The rounding leaves off = c m - M, at
+// most half an ulp of M, and the largest e is 2^off: below kFar it lies in
+// 2^-64 .. 2^64, so that no sum of 2^24 words and no product of one with a
+// difference of two references (2^32 at most) leaves fp32.  Past kFar, and
+// where there is no word yet, M is 0: a lane of words so far down (a mask of
+// -1e10, say) sums to 0, which is its share of any row with a maximum that is
+// not far, and a row whose own maximum is far is summed again by careful_row.
+constexpr float kFar = 2147483648.0f;   // 2^31
+
+__device__ __forceinline__ bool is_near(float m, float c) { return fabsf(c * m) < kFar; }
+
 __device__ __forceinline__ float reference(float m, float c) {
-  const float M = c * m;
-  return fabsf(M) < 1e30f ? M : 0.0f;
+  return is_near(m, c) ? c * m : 0.0f;
 }
 
 template <bool ENT>
@@ -201,8 +208,9 @@ __device__ __forceinline__ void add(Stat &a, float x, float c, float M) {
 // a's sums brought from their own reference to that of `top` >= a.m.
 __device__ __forceinline__ Stat raised(const Stat &a, float top, float c) {
   const float d = reference(a.m, c) - reference(top, c);
-  // nothing summed yet: t and w are 0, or NaN from NaN logits alone
-  const float f = a.m > -INFINITY ? __builtin_amdgcn_exp2f(d) : 0.0f;
+  // nothing summed yet, or words far down: t and w are 0, or NaN from NaN
+  // logits alone (and what a row with a far top sums to is not used)
+  const float f = is_near(a.m, c) ? __builtin_amdgcn_exp2f(d) : 0.0f;
   return {top, f * a.t, f * __builtin_fmaf(d, a.t, a.w)};
 }
 
@@ -267,8 +275,10 @@ __device__ __forceinline__ RowResult row_result(const Stat &a, float off, float 
   return {a.m, z, scale * (xy - a.m) - z, l - kLn2 * (a.w / a.t)};
 }
 
-// The sums of a row whose c m is out of reach: L = c (x - m) in two steps, the
-// row read again.  Such rows are all but -inf; speed does not matter here.
+// The sums of a row whose maximum is far: L = c (x - m) in two steps, the row
+// read again word by word (for rows that are cut, by one wavefront), several
+// times slower than the sums above.  Every word of such a row but -inf is a
+// mask of a large finite value, or its logits pass 10^9.
 template <bool BF16, int threads>
 __device__ __forceinline__ Stat careful_row(const char *row, int32_t V, float m, float c,
                                             Stat *red) {
@@ -289,7 +299,7 @@ __device__ __forceinline__ RowResult finished(Stat a, const char *row, int32_t V
                                               float xy, float scale, Stat *red) {
   const float c = scale * kLog2e;
   float off = __builtin_fmaf(c, a.m, -reference(a.m, c));
-  if (!(a.t > 0.0f && a.t < INFINITY) && fabsf(a.m) < INFINITY) {
+  if (!is_near(a.m, c) && fabsf(a.m) < INFINITY) {
     const float m = a.m;
     a = careful_row<BF16, threads>(row, V, m, c, red);
     a.m = m;
@@ -503,7 +513,7 @@ __global__ __launch_bounds__(threads) void policy_logits_kernel(
     const float g = w * q.dlogp, gh = -p.ent * w;
     some = r.m != -INFINITY && (g != 0.0f || gh != 0.0f);
     if (some) {
-      const GradCoef kc = grad_coef(a.scale, g, gh, r.ent, r.z);
+      const GradCoef kc = grad_coef(a.scale, g, gh, ENT ? r.ent : 0.0f, r.z);
       row_grad<ENT, ONE>(h, row, out, V, int32_t(y), r.m, a.scale * kLog2e, kc);
     }
   }
