@@ -18,6 +18,21 @@ __device__ __forceinline__ void store16_past(void *p, u32x4_t v) {
   __builtin_nontemporal_store(v, static_cast<any_u32x4_t *>(p));
 }
 
+// k = e^q - q - 1, em = e^q - 1.  Near 0 the difference em - q would keep only
+// the digits of em past those of q, so k is summed from its series (|q| < 1/2:
+// the first term left out is q^9 / 9!, 2^-24.2 of k at most); where e^q is past
+// fp32 k is infinite, also for an infinite q.
+__device__ __forceinline__ float kl_estimate(float q, float em) {
+  float s = __builtin_fmaf(q, 1.0f / 40320.0f, 1.0f / 5040.0f);
+  s = __builtin_fmaf(q, s, 1.0f / 720.0f);
+  s = __builtin_fmaf(q, s, 1.0f / 120.0f);
+  s = __builtin_fmaf(q, s, 1.0f / 24.0f);
+  s = __builtin_fmaf(q, s, 1.0f / 6.0f);
+  s = __builtin_fmaf(q, s, 0.5f);
+  const float far = em < INFINITY ? em - q : em;
+  return fabsf(q) < 0.5f ? q * q * s : far;
+}
+
 struct PolicyToken {
   float loss, k, bound;   // -f + kl k - ent H, the KL estimate, [a bound holds]
   float dlogp;            // d loss / d logp (that of the entropy is -ent)
@@ -26,8 +41,7 @@ struct PolicyToken {
 // One token of the objective (qlora_policy_loss in qlora.h has the formulas),
 // d = logp - old or 0.  The branch is chosen on d against rounded logs of the
 // bounds: d is one fp32 subtraction, so the choice does not hang on how exp
-// rounds.  k = expm1(q) - q keeps its digits where the two policies nearly
-// agree.
+// rounds.
 __device__ __forceinline__ PolicyToken policy_token(const PolicyParams &p, float logp, float ent,
                                                     float adv, float d, bool has_ref,
                                                     float ref) {
@@ -47,7 +61,7 @@ __device__ __forceinline__ PolicyToken policy_token(const PolicyParams &p, float
   t.k = 0.0f;
   if (has_ref) {
     const float q = ref - logp, em = expm1f(q);
-    t.k = em - q;
+    t.k = kl_estimate(q, em);
     t.loss += p.kl * t.k;
     t.dlogp -= p.kl * em;
   }

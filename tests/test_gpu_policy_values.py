@@ -1,0 +1,68 @@
+"""The policy objective where its terms nearly vanish or overflow: the KL
+estimate's digits, infinite log-ratios."""
+
+import math
+
+import numpy as np
+import pytest
+
+from quantized_rank_fine_amd import qlora as q
+
+from gpu_harness import say, torch_dev
+from test_gpu_objective import U, _dev
+
+pytestmark = pytest.mark.gpu
+
+
+def _loss(pol, logp, adv=None, old=None, ref=None, weight=None):
+    """out, dlogp of qlora_policy_loss."""
+    torch, dev = torch_dev()
+    T = len(logp)
+    out, d = torch.full((4,), 9.0, device=dev), torch.full((T,), 9.0, device=dev)
+    n = q.qlora_policy_workspace_bytes(T)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    a = [None if v is None else _dev(np.asarray(v, np.float32)) for v in (logp, weight, adv, old,
+                                                                         ref)]
+    q.qlora_policy_loss(a[0], None, T, a[1], a[2], a[3], a[4], pol, out, d, None, ws, n)
+    return out.cpu().numpy().astype(float), d.cpu().numpy().astype(float)
+
+
+def _k(v):
+    """exp(v) - v - 1 in float64, by its series where it cancels."""
+    if abs(v) > 1.0:
+        return math.expm1(v) - v
+    return sum(v ** n / math.factorial(n) for n in range(2, 24))
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_kl_estimate_keeps_its_digits(sign):
+    """Relative to k itself, and never below 0.  q = ref - logp is exact here
+    for |q| <= 1/2 (logp = -1), else rounded once (at most 3 u of k).  In fp32
+    the product q q, the polynomial beside it (its constant 1/2 and a first
+    term of at most a sixth of it, five roundings of half an ulp and less) and
+    their product err by at most 6 u;
+    for larger |q| expm1 (an ulp, 2 u, of its value) and the difference err by
+    2 u (e^q + |q|) + u k.  The weight is 1: the sums add a rounding."""
+    for size in [2.0 ** -23, 2.0 ** -20, 1e-6, 1e-5, 1e-4, 1e-3, 1e-2, 0.05, 0.1, 0.2, 0.3, 0.4,
+                 0.49, 0.499999, 0.5, 0.500001, 0.6, 0.75, 0.99]:
+        ref = np.float32(-1.0 + sign * size)
+        v = float(ref) + 1.0
+        say(f"[kl digits] q={v}")
+        out, d = _loss(q.policy_struct(q.OBJ_NLL, kl_coef=1.0), [-1.0], adv=[0.0], ref=[ref])
+        want = _k(v)
+        rel = 8 * U if abs(v) < 0.5 else 2 * U * (math.exp(v) + abs(v)) / want + 4 * U
+        assert out[1] >= 0 and abs(out[1] - want) <= rel * want, v
+        assert abs(out[0] - want) <= rel * want
+        assert abs(d[0] + math.expm1(v)) <= 4 * U * abs(math.expm1(v))
+    out, d = _loss(q.policy_struct(q.OBJ_NLL, kl_coef=1.0), [-1.0], adv=[0.0], ref=[-1.0])
+    assert out[1] == 0 and out[0] == 0 and d[0] == 0
+
+
+def test_kl_estimate_of_far_ratios():
+    """exp(q) past fp32, and q infinite, give an infinite estimate, not NaN:
+    exp(q) - q - 1 has that limit at both ends."""
+    inf = math.inf
+    for logp, old, ref in ((-100.0, -100.0, -1.0), (-inf, -1.0, -1.0), (-1.0, -1.0, -inf)):
+        out, _ = _loss(q.policy_struct(q.OBJ_CLIP, kl_coef=1.0), [logp, -1.0], old=[old, -1.0],
+                       ref=[ref, -1.0])
+        assert out[1] == inf and out[0] == inf, (logp, ref)
