@@ -62,8 +62,10 @@ __device__ __forceinline__ PolicyToken policy_token(const PolicyParams &p, float
   if (has_ref) {
     const float q = ref - logp, em = expm1f(q);
     t.k = kl_estimate(q, em);
-    t.loss += p.kl * t.k;
-    t.dlogp -= p.kl * em;
+    if (p.kl != 0.0f) {   // else k is reported only, and may be infinite
+      t.loss += p.kl * t.k;
+      t.dlogp -= p.kl * em;
+    }
   }
   if (p.ent != 0.0f) t.loss -= p.ent * ent;
   return t;

@@ -1,5 +1,6 @@
-"""The policy objective where its terms nearly vanish or overflow: the KL
-estimate's digits, infinite log-ratios."""
+"""The policy objective where its terms nearly vanish, overflow or are
+switched off: the KL estimate's digits, infinite log-ratios, a coefficient of
+0."""
 
 import math
 
@@ -66,3 +67,19 @@ def test_kl_estimate_of_far_ratios():
         out, _ = _loss(q.policy_struct(q.OBJ_CLIP, kl_coef=1.0), [logp, -1.0], old=[old, -1.0],
                        ref=[ref, -1.0])
         assert out[1] == inf and out[0] == inf, (logp, ref)
+
+
+@pytest.mark.parametrize("kind", [q.OBJ_NLL, q.OBJ_CLIP])
+def test_no_kl_coefficient_takes_nothing_from_the_ratio(kind):
+    """kl_coef = 0 with a reference (the estimate is reported only): the loss
+    and the gradient are those without one, however far the reference is."""
+    logp, ref = [-2.0, -100.0, -1.0, -math.inf], [-1.0, -1.0, -math.inf, -1.0]
+    old, adv = [-2.1, -100.0, -1.0, -1.0], [1.0, -0.5, 2.0, 0.75]
+    w = [0.25, 0.5, 0.125, 0.0625]
+    if kind == q.OBJ_NLL:                        # a log-likelihood of -inf is an infinite loss
+        logp, ref, old, adv, w = (v[:3] for v in (logp, ref, old, adv, w))
+    pol = q.policy_struct(kind)
+    a, da = _loss(pol, logp, adv, old, None, w)
+    b, db = _loss(pol, logp, adv, old, ref, w)
+    assert np.isfinite(a).all() and np.isfinite(da).all()
+    assert b[0] == a[0] and np.array_equal(da, db) and b[1] == math.inf
