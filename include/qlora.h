@@ -516,7 +516,8 @@ size_t qlora_pref_workspace_bytes(int64_t P, int64_t T);
  *   dlogp = weight (-f' + kl_coef (1 - exp(q))),
  *   dentropy = -weight ent_coef (NULL: not wanted).
  * A term whose coefficient is 0 is left out of loss and dlogp, whatever it
- * holds (with kl_coef = 0 and a ref, k is reported only).
+ * holds: with adv = 0, f = f' = 0 for any logp and d; with kl_coef = 0 and a
+ * ref, k is reported only.
  *   out [4]: loss, sum weight k, sum weight [a bound holds], sum weight
  *   entropy.
  * 0 <= clip_lo <= 1, clip_hi >= 0 (may be infinite), clip_dual = 0 or > 1,

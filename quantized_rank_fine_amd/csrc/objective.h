@@ -33,6 +33,15 @@ __device__ __forceinline__ float kl_estimate(float q, float em) {
   return fabsf(q) < 0.5f ? q * q * s : far;
 }
 
+// v times its coefficient c: 0 where c is 0, also for an infinite or NaN v
+// (one instruction; with v selected before ordinary products the policy loss of
+// 8000 tokens took 8.6 us, not 8.4).
+__device__ __forceinline__ float scaled(float c, float v) {
+  float r;
+  asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(c), "v"(v));
+  return r;
+}
+
 struct PolicyToken {
   float loss, k, bound;   // -f + kl k - ent H, the KL estimate, [a bound holds]
   float dlogp;            // d loss / d logp (that of the entropy is -ent)
@@ -46,10 +55,10 @@ __device__ __forceinline__ PolicyToken policy_token(const PolicyParams &p, float
                                                     float adv, float d, bool has_ref,
                                                     float ref) {
   PolicyToken t;
-  float f = adv * logp, df = adv;
+  float f = scaled(adv, logp), df = adv;
   t.bound = 0.0f;
   if (p.clip) {
-    df = expf(d) * adv;
+    df = scaled(adv, expf(d));
     f = df;
     if (adv > 0.0f && d > p.log_hi) { f = p.hi * adv; t.bound = 1.0f; }
     if (adv < 0.0f && d < p.log_lo) { f = p.lo * adv; t.bound = 1.0f; }
@@ -62,10 +71,8 @@ __device__ __forceinline__ PolicyToken policy_token(const PolicyParams &p, float
   if (has_ref) {
     const float q = ref - logp, em = expm1f(q);
     t.k = kl_estimate(q, em);
-    if (p.kl != 0.0f) {   // else k is reported only, and may be infinite
-      t.loss += p.kl * t.k;
-      t.dlogp -= p.kl * em;
-    }
+    t.loss += scaled(p.kl, t.k);
+    t.dlogp -= scaled(p.kl, em);
   }
   if (p.ent != 0.0f) t.loss -= p.ent * ent;
   return t;

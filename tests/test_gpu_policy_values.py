@@ -1,6 +1,6 @@
 """The policy objective where its terms nearly vanish, overflow or are
-switched off: the KL estimate's digits, infinite log-ratios, a coefficient of
-0."""
+switched off: the KL estimate's digits, infinite log-ratios, coefficients and
+advantages of 0."""
 
 import math
 
@@ -10,7 +10,7 @@ import pytest
 from quantized_rank_fine_amd import qlora as q
 
 from gpu_harness import say, torch_dev
-from test_gpu_objective import U, _dev
+from test_gpu_objective import U, _dev, _policy_logits
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,36 @@ def test_no_kl_coefficient_takes_nothing_from_the_ratio(kind):
     b, db = _loss(pol, logp, adv, old, ref, w)
     assert np.isfinite(a).all() and np.isfinite(da).all()
     assert b[0] == a[0] and np.array_equal(da, db) and b[1] == math.inf
+
+
+def test_no_advantage_takes_nothing_from_the_policy():
+    """An advantage of 0 (all answers of a prompt rewarded alike): no loss, no
+    bound and no gradient, whatever the ratio or the log-probability."""
+    far = [-1.0, -1.0, -1.0, -math.inf]
+    out, d = _loss(q.policy_struct(q.OBJ_CLIP), far, [0.0] * 4, [-101.0, -1.0, -0.5, -1.0])
+    assert not out.any() and not d.any()
+    out, d = _loss(q.policy_struct(q.OBJ_CLIP, clip_hi=math.inf), far, [0.0, -0.0] * 2,
+                   [-200.0, -90.0, -math.inf, -1.0])
+    assert not out.any() and not d.any()
+    out, d = _loss(q.policy_struct(q.OBJ_NLL), far, [0.0] * 4)
+    assert not out.any() and not d.any()
+
+
+@pytest.mark.parametrize("V", [9, 70001])
+def test_policy_logits_of_masked_labels_and_far_ratios(V):
+    """The same through the logits: a label at -inf beside kl_coef = 0 and
+    beside an advantage of 0, and a ratio past fp32."""
+    torch, dev = torch_dev()
+    g = np.random.default_rng(V)
+    x = g.standard_normal((4, V)).astype(np.float32)
+    y = np.array([3, 4, 5, 6])
+    x[1, 4] = x[2, 5] = -np.inf
+    adv, w = np.array([1.0, 0.0, 0.5, 0.0], np.float32), np.full(4, 0.25, np.float32)
+    old = np.array([-math.log(V), -1.0, -1.0, -200.0], np.float32)
+    ref = np.full(4, -1.0, np.float32)
+    pol = q.policy_struct(q.OBJ_CLIP, 0.2, math.inf, 0.0, 0.0, 0.0)
+    out, lp, dx, _ = _policy_logits(_dev(x), V, "f32", y, 1.0, pol, w, adv, old, ref)
+    assert np.isfinite(out[0]) and out[1] == math.inf and out[2] == 0
+    assert lp[1] == -math.inf and lp[2] == -math.inf
+    got = dx.cpu().numpy()
+    assert np.isfinite(got).all() and not got[1:].any() and got[0].any()
