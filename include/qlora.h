@@ -471,6 +471,7 @@ qlora_status qlora_token_logp_bwd(const void *logits, int64_t ld, int64_t T, int
  * their number if `average`; 0 for an answer without any), h = S_k - S_(P+k):
  *   SIGMOID  u = beta h - margin,
  *            l = -(1 - smoothing) log sigma(u) - smoothing log sigma(-u)
+ *            (without smoothing the first term alone, also for an infinite u)
  *   SQUARED  l = (h - 1 / (2 beta))^2
  *   HINGE    l = max(0, 1 - (beta h - margin))
  *   loss [1] = mean l;  rewards [2P] = beta S_i;

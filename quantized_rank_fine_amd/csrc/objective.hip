@@ -140,7 +140,9 @@ __device__ __forceinline__ PairLoss pair_loss(const PrefParams &p, float h) {
   const float e = expf(-fabsf(u)), l = log1pf(e);
   const float neg = u > 0.0f ? e / (1.0f + e) : 1.0f / (1.0f + e);
   const float down = fmaxf(-u, 0.0f) + l, up = fmaxf(u, 0.0f) + l;
-  return {(1.0f - p.smoothing) * down + p.smoothing * up,
+  // (an infinite u, from an answer that the model cannot give, has an infinite
+  // `up`, of which no smoothing takes nothing)
+  return {(1.0f - p.smoothing) * down + (p.smoothing > 0.0f ? p.smoothing * up : 0.0f),
           p.beta * (p.smoothing * (1.0f - neg) - (1.0f - p.smoothing) * neg)};
 }
 
