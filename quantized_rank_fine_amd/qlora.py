@@ -177,7 +177,7 @@ def header_functions():
 # ------------------------------------------------------------------ helpers
 
 def _ptr(t):
-    if t is None or type(t) is int:
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
