@@ -185,15 +185,24 @@ def _ptr(t):
 _current_raw = None      # (device index -> stream handle, current device), once initialised
 
 
+def _stream_getters():
+    import torch
+    torch.cuda.current_stream()          # initialises the runtime, or says that there is none
+    # torch.cuda.current_stream().cuda_stream without the Stream object (0.2 us, not 2.7),
+    # where this torch has the two calls for it
+    handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if handle is None or device is None:
+        return lambda d: torch.cuda.current_stream(d).cuda_stream, torch.cuda.current_device
+    return handle, device
+
+
 def _stream(stream):
     global _current_raw
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     if _current_raw is None:
-        import torch
-        torch.cuda.current_stream()          # initialises the runtime, or says that there is none
-        _current_raw = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    # torch.cuda.current_stream().cuda_stream without the Stream object (0.2 us, not 2.7)
+        _current_raw = _stream_getters()
     handle, device = _current_raw
     return handle(device())
 
