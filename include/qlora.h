@@ -435,8 +435,9 @@ size_t qlora_loftq_workspace_bytes(int64_t in, int64_t out, int32_t k);
  * qlora_token_logp_fwd: logp[t] = log p_y of each row.
  *   stats [T, 2]  fp32 (output): m and z, which the backward reads.
  *   entropy [T]   fp32 (output) H, or NULL.
- * scale > 0 is s.  ws: qlora_token_logp_workspace_bytes(T, V, dt) bytes (may
- * be 0, ws then NULL).  T = 0 is a no-op.
+ * scale is s, 0 < s <= 2.3e38 (s log2 e is finite in fp32; QLORA_ERR_VALUE).
+ * ws: qlora_token_logp_workspace_bytes(T, V, dt) bytes (may be 0, ws then
+ * NULL).  T = 0 is a no-op.
  */
 qlora_status qlora_token_logp_fwd(const void *logits, int64_t ld, int64_t T, int64_t V,
                                   qlora_dtype dt, const int64_t *labels, float scale,

@@ -354,7 +354,8 @@ bool aligned_el(const void *p, qlora_dtype dt) { return aligned_to(p, dt == QLOR
 qlora_status check_logits(int64_t ld, int64_t T, int64_t V, qlora_dtype dt, float scale) {
   if (!tokens_ok(T) || V < 1 || V > kMaxVocab || ld < V || ld > kMaxLd) return QLORA_ERR_SHAPE;
   if (!dtype_ok(dt)) return QLORA_ERR_DTYPE;
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return QLORA_ERR_VALUE;
+  // (the kernels take exponents to base 2)
+  if (!(scale > 0.0f) || !std::isfinite(scale * 1.44269504f)) return QLORA_ERR_VALUE;
   return QLORA_OK;
 }
 

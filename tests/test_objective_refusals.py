@@ -1,5 +1,6 @@
 """Workspaces that are missing, short or misaligned, in the shapes of the
-objectives that need one (no GPU): refused before any pointer is touched."""
+objectives that need one, and scales past what fp32 holds (no GPU): refused
+before any pointer is touched."""
 
 import ctypes
 
@@ -73,3 +74,17 @@ def test_policy_workspace(L, T):
     assert call(P, n - 1) == 5 and call(P, 0) == 5
     assert call(None, n) == 1
     assert call(P + 4, n) == 3
+
+
+@pytest.mark.parametrize("s", [2.4e38, 3.4e38])
+def test_scales_past_fp32(L, s):
+    """s log2 e has to be a number in fp32, or every row would be NaN."""
+    pol = ctypes.byref(q.policy_struct(q.OBJ_CLIP))
+    big = 1 << 20
+    for scale, status in ((s, 7), (2.3e38, 1)):          # (1: on to the pointers, which are missing)
+        assert L.qlora_token_logp_fwd(None, 8, 1, 8, q.F32, P, scale, P, P, None, None, 0,
+                                      None) == status
+        assert L.qlora_token_logp_bwd(None, 8, 1, 8, q.F32, P, scale, P, None, P, None, P, 8,
+                                      None) == status
+        assert L.qlora_policy_logits(None, 8, 1, 8, q.F32, P, scale, None, None, None, None, pol,
+                                     P, None, P, 8, P, big, None) == status
