@@ -16,8 +16,8 @@ from oracle import objective as ob
 from quantized_rank_fine_amd import qlora as q
 
 from gpu_harness import out_to_f64, say, torch_dev
-from test_gpu_objective import (U, _dev, _fwd, _policy_logits, _tol_grad, _tol_rows, _token_tol,
-                                f32)
+from test_gpu_objective import (U, _dev, _fwd, _policy_logits, _special, _tol_grad, _tol_rows,
+                                _token_tol, f32)
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +140,46 @@ def test_policy_of_rows_with_finite_masks(V, s, dt, ent):
     out2, lp2, dx2, _ = _policy_logits(x.clone(), V, dt, y, s, pol, w, adv, old, ref, inplace=True)
     assert np.array_equal(out, out2) and np.array_equal(glp, lp2)
     assert np.array_equal(out_to_f64(dx2, dt).reshape(T, V), out_to_f64(dx, dt).reshape(T, V))
+
+
+@pytest.mark.parametrize("V", [13, 4100, 12001, 70001])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,ent", [("clip", 0.02), ("clip", 0.0), ("nll", 0.02)])
+def test_policy_of_special_rows(V, dt, kind, ent):
+    """Rows with words at -inf, all at bf16's lowest value, and one possible
+    word: scores, sums and gradient; beside them, in a call of their own, rows
+    of NaN and +inf, which are NaN themselves and leave the others alone."""
+    torch, dev = torch_dev()
+    say(f"[policy special] V={V} {dt} {kind} ent={ent}")
+    s, ent, kl, lo, hi = f32(1.5), f32(ent), f32(0.1), f32(0.2), f32(0.28)
+    xs, y = _special(V)
+    x = _dev(xs).to(torch.bfloat16 if dt == "bf16" else torch.float32)
+    good, bad = [0, 2, 3, 8], [5, 6, 7]
+    xv = out_to_f64(x, dt).reshape(xs.shape)[good]
+    T, yg = len(good), y[good]
+    lp, m, z, h = ob.token_logp(xv, yg, s)
+    w, adv = np.full(T, 0.25, np.float32), np.array([1.0, -0.5, 0.25, 2.0], np.float32)
+    old, ref = (lp + 0.05).astype(np.float32), (lp - 0.1).astype(np.float32)
+    ro, rg, rgh = ob.policy_loss(kind, lp, h, w, adv, old, ref, lo, hi, 0.0, kl, ent)
+    rd = ob.logits_grad(xv, yg, rg, rgh, s)
+    pol = q.policy_struct(q.OBJ_CLIP if kind == "clip" else q.OBJ_NLL, lo, hi, 0.0, kl, ent)
+    out, glp, dx, _ = _policy_logits(x[good].contiguous(), V, dt, yg, s, pol, w, adv, old, ref)
+    tl, tz, th = _tol_rows(V, lp, z)
+    assert np.all(np.abs(glp - lp) <= tl)
+    tloss, tg, tk = _token_tol(dict(logp=lp, entropy=h, adv=adv, old=old, ref=ref), kl, ent, tl)
+    tol = _tol_grad(xv, yg, rd, rg, rgh, s, w * tg + 2 * U * np.abs(rg))
+    if dt == "bf16":
+        tol = tol + 2.0 ** -8 * (np.abs(rd) + tol)
+    got = out_to_f64(dx, dt).reshape(T, V)
+    assert np.all(np.abs(got - rd) <= tol)
+    absum = np.array([(w * (tloss + abs(ent) * th)).sum(), (w * tk).sum(), 0.0, (w * th).sum()])
+    terms = w.sum() * (4 + np.abs(ro).max() / w.sum()) + (w * (np.abs(lp) + h)).sum()
+    assert np.all(np.abs(out - ro) <= absum + 4 * U * terms)
+    # with the others in the same call
+    at = good + bad
+    more = lambda v: np.concatenate([v, np.full(3, 0.25, np.float32)])  # noqa: E731
+    out, glp2, dx, _ = _policy_logits(x[at].contiguous(), V, dt, y[at], s, pol, more(w), more(adv),
+                                      more(old), more(ref))
+    d = out_to_f64(dx, dt).reshape(len(at), V)
+    assert np.array_equal(glp2[:T], glp) and np.array_equal(d[:T], got)
+    assert np.isnan(glp2[T:]).all() and np.isnan(d[T:]).all() and np.isnan(out[[0, 3]]).all()
