@@ -15,13 +15,14 @@
 //
 // HBM-bound: the forward reads each scored row once, the gradient also writes
 // each row once.  Measured with a quarter of the rows not scored: the forward
-// with entropy of 4096 x 32000 bf16 38.3 us (5.1 TB/s), its gradient 73.8 us
-// (6.2 TB/s), the policy objective of 8192 x 32000 bf16 163 us (5.6 TB/s) and 7
-// us for the sums; a 1 GiB device copy moves 5.2 TB/s on the same card.
+// with entropy of 4096 x 32000 bf16 38.7 us (5.1 TB/s), its gradient 73.8 us
+// (6.2 TB/s), the policy objective of 8192 x 32000 bf16 162 to 170 us (5.4 to
+// 5.6 TB/s) and 6 us for the sums; a 1 GiB device copy moves 5.2 TB/s on the
+// same card.
 //
-// Rows of an odd V start at any element: a row is cut into up to 7 words before
-// its first 16-byte boundary, groups of 16 bytes, and up to 7 words after the
-// last whole group.
+// Rows of an odd V start at any element: a row is cut into the words before its
+// first 16-byte boundary, groups of 16 bytes, and the words after the last
+// whole group (up to 7 of either in bf16, 3 in fp32).
 #include "objective.h"
 
 namespace qlora {

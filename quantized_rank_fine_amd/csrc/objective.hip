@@ -2,11 +2,11 @@
 // each with its gradient by token.  Both only stream a few fp32 arrays, so
 // they are bound by HBM when long and by the launch when short.  Sums are
 // fp64 and in an order that the sizes alone fix.  Measured: the policy loss of
-// 2 M tokens with entropies 15.4 us (67 MB, 4.3 TB/s) and 3.8 us for the
-// partials, of 1000 tokens 3.8 us; the preference loss of 256 pairs of 4608
-// tokens 7.7 and 1.5 us, of two pairs of 147000 4.0 and 6.9 us (latency: an
-// answer's place, its tokens, the join, the tokens' masks again), of four pairs
-// of 337 6.1 us in one launch.
+// 2 M tokens with entropies 15.8 us (67 MB, 4.25 TB/s) and 3.9 us for the
+// partials, of 1000 tokens 4.1 us; the preference loss of 256 pairs of 4608
+// tokens 7.6 and 1.5 us, of two pairs of 147000 4.0 and 6.8 us (latency: an
+// answer's place, its tokens, both answers' partials, the tokens' masks again,
+// one load after the other), of four pairs of 337 5.9 us in one launch.
 #include "objective.h"
 
 namespace qlora {
@@ -16,7 +16,8 @@ namespace {
 
 // Up to kPolicyLone the tokens are one workgroup's and its sums are the result;
 // past that there is a second launch.  us a call, one launch and two: 5000
-// tokens 7.9 and 11.6, 8000 8.7 and 11.5, 12000 10.9 and 11.2.
+// tokens 7.9 and 11.6, 8000 8.7 and 11.5, 12000 10.9 and 11.2 (before the KL
+// estimate's series, which adds 0.4 to 8000 tokens in one launch).
 constexpr int kPolicyThreads = 256;
 constexpr int64_t kPolicyLone = 8192;
 
@@ -82,14 +83,14 @@ __global__ __launch_bounds__(threads) void policy_kernel(const float *logp, cons
   put_sums(s, out, partial);
 }
 
-// Column sums of v [n x 4].
+// Column sums of v [n x 4].  A lane's loads wait for one another, since each is
+// behind its own end of the loop: 8192 rows take eight round trips, 6.3 us.
 template <class F>
 __global__ __launch_bounds__(1024) void sum4_kernel(const F *v, int64_t n, float *out,
                                                     double *partial) {
   __shared__ double red[4 * 16];
   double s[4] = {};
   const int64_t step = int64_t(gridDim.x) * 1024;
-#pragma unroll 8
   for (int64_t i = int64_t(blockIdx.x) * 1024 + threadIdx.x; i < n; i += step) {
     F x[4];
     __builtin_memcpy(x, v + 4 * i, sizeof(x));
@@ -203,7 +204,8 @@ struct Quad {
   }
 };
 
-// Arrays of less than four tokens take the byte and the word one by one.
+// Arrays of less than four tokens take the byte and the word one by one.  The
+// test is a lane's, though all lanes agree: each load is behind a branch.
 __device__ __forceinline__ uint32_t load_mask(const PrefArgs &a, const Quad &q) {
   uint32_t m = 0x01010101u;
   if (a.mask && q.at >= 0) __builtin_memcpy(&m, a.mask + q.at, 4);
@@ -223,8 +225,9 @@ __device__ __forceinline__ f32x4_t load_quad(const float *v, const Quad &q) {
   return x;
 }
 
-// The quads of a slice, N of a lane at a time: straight-line loads (past the
-// slice's end the last quad again, nothing of it counted).
+// The quads of a slice, N of a lane at a time (past the slice's end the last
+// quad again, nothing of it counted), so that the loads of all N are on their
+// way before the first is used.
 __device__ __forceinline__ int32_t quad_at(const Span &s, int32_t t, int i) {
   return t + 256 * i < s.last ? t + 256 * i : s.last;
 }
@@ -294,6 +297,7 @@ __device__ __forceinline__ Partial unit_sum(const PrefArgs &a, int32_t u, int n)
 __device__ __forceinline__ Partial total(const PrefArgs &a, const Partial *partial, int32_t i,
                                          int n, int at, int lanes) {
   Partial r = {0.0, 0.0};
+  // (four loads at once while four are left to a lane, the rest one by one)
 #pragma unroll 4
   for (int j = at; j < n; j += lanes) {
     r.sum += partial[int64_t(i) * n + j].sum;
@@ -410,7 +414,7 @@ __global__ __launch_bounds__(1024) void pref_mean_kernel(const double *losses, i
                                                          float *loss) {
   __shared__ double red[16];
   double s[1] = {};
-#pragma unroll 4
+#pragma unroll 4   // reached from 4096 pairs on
   for (int64_t k = threadIdx.x; k < P; k += 1024) s[0] += losses[k];
   block_sums<1, 1024>(s, red);
   if (threadIdx.x == 0) loss[0] = float(s[0] / double(P));
