@@ -426,7 +426,8 @@ size_t qlora_loftq_workspace_bytes(int64_t in, int64_t out, int32_t k);
  *     gradient row is 0.
  *   - A logit of -inf is a word that cannot occur (p = 0, gradient 0); a
  *     row of nothing else has logp = -inf, H = 0 and a zero gradient row.  A
- *     NaN or +inf makes its own row's results NaN.
+ *     large finite value masks a word as well where its row keeps others (a p
+ *     below 2^-126 is 0).  A NaN or +inf makes its own row's results NaN.
  *   - Arithmetic is fp32, the sums that give a loss fp64 across workgroups;
  *     results are rounded to the output's type once.
  */

@@ -277,9 +277,10 @@ __device__ __forceinline__ RowResult row_result(const Stat &a, float off, float 
 }
 
 // The sums of a row whose maximum is far: L = c (x - m) in two steps, the row
-// read again word by word (for rows that are cut, by one wavefront), several
-// times slower than the sums above.  Every word of such a row but -inf is a
-// mask of a large finite value, or its logits pass 10^9.
+// read again word by word.  Every word of such a row but -inf is a mask of a
+// large finite value, or its logits pass 10^9: no row that a model gives, so the
+// time is left as it is (scoring 4096 x 32000 bf16 118 us, not 41; rows that are
+// cut, by one wavefront, 64 x 200000 fp32 785 us, not 12).
 template <bool BF16, int threads>
 __device__ __forceinline__ Stat careful_row(const char *row, int32_t V, float m, float c,
                                             Stat *red) {
