@@ -2,8 +2,8 @@
 // each with its gradient by token.  Both only stream a few fp32 arrays, so
 // they are bound by HBM when long and by the launch when short.  Sums are
 // fp64 and in an order that the sizes alone fix.  Measured: the policy loss of
-// 2 M tokens with entropies 15.8 us (67 MB, 4.25 TB/s) and 3.9 us for the
-// partials, of 1000 tokens 4.1 us; the preference loss of 256 pairs of 4608
+// 2 M tokens with entropies 15.2 us (67 MB, 4.4 TB/s) and 3.9 us for the
+// partials, of 1000 tokens 3.9 us; the preference loss of 256 pairs of 4608
 // tokens 7.6 and 1.5 us, of two pairs of 147000 4.0 and 6.8 us (latency: an
 // answer's place, its tokens, both answers' partials, the tokens' masks again,
 // one load after the other), of four pairs of 337 5.9 us in one launch.
@@ -16,8 +16,7 @@ namespace {
 
 // Up to kPolicyLone the tokens are one workgroup's and its sums are the result;
 // past that there is a second launch.  us a call, one launch and two: 5000
-// tokens 7.9 and 11.6, 8000 8.7 and 11.5, 12000 10.9 and 11.2 (before the KL
-// estimate's series, which adds 0.4 to 8000 tokens in one launch).
+// tokens 7.9 and 11.6, 8000 8.7 and 11.5, 12000 10.9 and 11.2.
 constexpr int kPolicyThreads = 256;
 constexpr int64_t kPolicyLone = 8192;
 
@@ -66,15 +65,15 @@ __global__ __launch_bounds__(threads) void policy_kernel(const float *logp, cons
     f32x4_t g, gh;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bool on = j < n && w[j] != 0.0f;
+      const float v = j < n ? w[j] : 0.0f;   // 0: what the token holds is not used
       const PolicyToken t = policy_token(p, lp[j], h[j], adv[j], k.old ? lp[j] - old[j] : 0.0f,
                                          k.ref, ref[j]);
-      g[j] = on ? w[j] * t.dlogp : 0.0f;
-      gh[j] = on ? -w[j] * p.ent : 0.0f;
-      s[0] += on ? w[j] * t.loss : 0.0f;
-      s[1] += on ? w[j] * t.k : 0.0f;
-      s[2] += on ? w[j] * t.bound : 0.0f;
-      s[3] += on ? w[j] * h[j] : 0.0f;
+      g[j] = scaled(v, t.dlogp);
+      gh[j] = scaled(v, -p.ent);
+      s[0] += scaled(v, t.loss);
+      s[1] += scaled(v, t.k);
+      s[2] += scaled(v, t.bound);
+      s[3] += scaled(v, h[j]);
     }
     give4(dlogp, i, n, g);
     if (dentropy) give4(dentropy, i, n, gh);
