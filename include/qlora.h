@@ -424,10 +424,11 @@ size_t qlora_loftq_workspace_bytes(int64_t in, int64_t out, int32_t k);
  *   - A token whose label lies outside [0, V) (-100, say) is not scored: its
  *     logits are not read, its logp, stats and entropy are 0 and its
  *     gradient row is 0.
- *   - A logit of -inf is a word that cannot occur (p = 0, gradient 0); a
- *     row of nothing else has logp = -inf, H = 0 and a zero gradient row.  A
- *     large finite value masks a word as well where its row keeps others (a p
- *     below 2^-126 is 0).  A NaN or +inf makes its own row's results NaN.
+ *   - A logit of -inf is a word that cannot occur (p = 0, gradient 0, or s g
+ *     where it is the label); a row of nothing else has logp = -inf, H = 0 and
+ *     a zero gradient row.  A large finite value masks a word as well where its
+ *     row keeps others (a p below 2^-126 is 0).  A NaN or +inf makes its own
+ *     row's results NaN.
  *   - Arithmetic is fp32, the sums that give a loss fp64 across workgroups;
  *     results are rounded to the output's type once.
  */

@@ -34,4 +34,5 @@ def test_extreme_scales(s, V):
     hot = np.zeros(V)
     hot[4] = 1.0
     p = np.where(x[0] == 2.0, 0.5, 0.0) if n == 2 else np.full(V, 1.0 / V)
-    assert np.all(np.abs(got[0] - 0.25 * s * (p - hot)) <= s * (V / 64 + 64) * U) and not got[1].any()
+    assert np.all(np.abs(got[0] - 0.25 * s * (p - hot)) <= s * (V / 64 + 64) * U)
+    assert not got[1].any()

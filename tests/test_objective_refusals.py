@@ -81,7 +81,7 @@ def test_scales_past_fp32(L, s):
     """s log2 e has to be a number in fp32, or every row would be NaN."""
     pol = ctypes.byref(q.policy_struct(q.OBJ_CLIP))
     big = 1 << 20
-    for scale, status in ((s, 7), (2.3e38, 1)):          # (1: on to the pointers, which are missing)
+    for scale, status in ((s, 7), (2.3e38, 1)):          # (1: on to the missing pointers)
         assert L.qlora_token_logp_fwd(None, 8, 1, 8, q.F32, P, scale, P, P, None, None, 0,
                                       None) == status
         assert L.qlora_token_logp_bwd(None, 8, 1, 8, q.F32, P, scale, P, None, P, None, P, 8,
