@@ -379,6 +379,60 @@ qlora_status qlora_adam_step(float *theta, const float *grad, float *m, float *v
                              float weight_decay, uint16_t *theta_bf16, hipStream_t stream);
 
 /*
+ * qlora_muon_step: one orthogonalised step of n adapter matrices, in place
+ * (momentum, then Newton-Schulz products in place of the update's singular
+ * values; Jordan et al., "Muon: an optimizer for hidden layers in neural
+ * networks").  For each matrix, of rows x cols, row-major, fp32:
+ *   m <- momentum m + g;  u = g + momentum m (nesterov) or m;  m NULL: u = g;
+ *   X = u / (|u| + eps), |u| the Frobenius norm (u = 0 gives X = 0);
+ *   `steps` times, with X's shorter side as columns (rows of a wide X),
+ *     X <- a X + b X (X^T X) + c X (X^T X)^2,  (a, b, c) = coef;
+ *   theta <- theta - lr (scale X + weight_decay theta);  theta_bf16 as in
+ *   qlora_adam_step;  update receives X.  theta, theta_bf16 and update may each
+ *   be NULL (theta_bf16 needs theta); without m and theta the call just
+ *   orthogonalises grad.
+ * m, u and theta are fp32 as written (each operation rounded), everything
+ * between u and X is fp64, X is rounded to fp32 once.  A call's matrices may
+ * differ in shape and must not overlap one another; the shorter side is at
+ * most QLORA_MAX_RANK, the longer at most 2^24, and pointers need their
+ * element's alignment only (16 bytes, and an inner size that is a multiple of
+ * 4, are faster).  A matrix's bits may depend on the other shapes of its call.
+ * 0 <= n <= QLORA_MUON_MAX_MATS; mats is a host array, read before the call
+ * returns.  momentum >= 0, eps >= 0 and weight_decay >= 0, all values finite,
+ * 1 <= steps <= 16 and a^(2 steps) <= 1e9 (QLORA_ERR_VALUE; a = 3.4445 allows
+ * 8 steps): X's own error is near 1e-16 k a^(2 steps) at most, k the shorter
+ * side, which past that would show in fp32.
+ * ws: qlora_muon_workspace_bytes(n, mats) bytes, which depends on the shapes
+ * alone (0 if they are invalid).
+ */
+#define QLORA_MUON_MAX_MATS 4096
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  const float *grad;
+  float *m;
+  float *theta;
+  uint16_t *theta_bf16;
+  float *update;
+  float scale;
+} qlora_muon_mat;
+
+typedef struct {
+  float lr;
+  float momentum;
+  float weight_decay;
+  int32_t nesterov;
+  int32_t steps;
+  double eps;
+  double coef[3];
+} qlora_muon_hparams;
+
+qlora_status qlora_muon_step(int32_t n, const qlora_muon_mat *mats,
+                             const qlora_muon_hparams *hparams, void *ws, size_t ws_bytes,
+                             hipStream_t stream);
+size_t qlora_muon_workspace_bytes(int32_t n, const qlora_muon_mat *mats);
+
+/*
  * qlora_loftq_init: adapters started from the quantization residual instead
  * of B = 0 ("What QLoRA adds", the paragraph on running it: LoftQ-style
  * methods start A and B from an SVD of W0 - Q(W0)).
@@ -619,7 +673,8 @@ typedef enum {
   QLORA_KERNEL_PREF = 9,        /* preference loss                        */
   QLORA_KERNEL_POLICY = 10,     /* policy loss (tokens, logits)           */
   QLORA_KERNEL_DROPOUT = 11,    /* dropout from the counter               */
-  QLORA_KERNEL_COUNT = 12
+  QLORA_KERNEL_MUON = 12,       /* orthogonalised update                  */
+  QLORA_KERNEL_COUNT = 13
 } qlora_kernel_kind;
 
 int qlora_timing_enable(int kind_mask);

@@ -25,7 +25,8 @@ What it computes (plain, slow, obviously correct):
   the same with the alpha/r factor and dropout on X.A (mask given);
   the merged dense weight deq(Wq) + A.B; adapters initialised from the
   best rank-r approximation of the quantization residual W0 - deq(Q(W0)).
-* ``optim``   -- one Adam (AdamW) step of an adapter matrix, in float64.
+* ``optim``   -- one Adam (AdamW) step and one orthogonalised step of an adapter
+  matrix, in float64.
 * ``objective`` -- token log-probabilities and entropy of logits with their
   gradient, the preference losses, the clipped policy objective, and the
   Philox4x32-10 mask of the dropout, from their published formulas (pinned by
@@ -65,7 +66,7 @@ from .linear import (
     residual,
     loftq_init,
 )
-from .optim import adam_step
+from .optim import adam_step, muon_step, orthogonalize
 
 __all__ = [
     "nf4_levels",
@@ -93,6 +94,8 @@ __all__ = [
     "residual",
     "loftq_init",
     "adam_step",
+    "muon_step",
+    "orthogonalize",
     "backward_via_dense_dw",
     "forward_lora",
     "backward_lora",

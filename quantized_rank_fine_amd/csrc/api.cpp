@@ -421,6 +421,17 @@ qlora_status adam_target(const qlora_adam_state *s, const qlora_adam_hparams *h,
   return QLORA_OK;
 }
 
+qlora_status check_muon(int32_t n, const qlora_muon_mat *mats) {
+  if (n < 0 || n > QLORA_MUON_MAX_MATS) return QLORA_ERR_SHAPE;
+  if (n > 0 && !mats) return QLORA_ERR_NULL;
+  constexpr int64_t most = int64_t(1) << 24;
+  for (int32_t i = 0; i < n; ++i)
+    if (mats[i].rows < 1 || mats[i].cols < 1 || mats[i].rows > most || mats[i].cols > most ||
+        std::min(mats[i].rows, mats[i].cols) > QLORA_MAX_RANK)
+      return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -685,6 +696,42 @@ qlora_status qlora_adam_step(float *theta, const float *grad, float *m, float *v
                          theta_bf16, stream));
 }
 
+size_t qlora_muon_workspace_bytes(int32_t n, const qlora_muon_mat *mats) {
+  if (check_muon(n, mats) != QLORA_OK || n == 0) return 0;
+  return muon_workspace_bytes(mats, n);
+}
+
+qlora_status qlora_muon_step(int32_t n, const qlora_muon_mat *mats,
+                             const qlora_muon_hparams *hparams, void *ws, size_t ws_bytes,
+                             hipStream_t stream) {
+  qlora_status st = check_muon(n, mats);
+  if (st != QLORA_OK) return st;
+  if (!hparams) return QLORA_ERR_NULL;
+  const qlora_muon_hparams &h = *hparams;
+  const bool ok = std::isfinite(h.lr) && std::isfinite(h.momentum) && h.momentum >= 0.0f &&
+                  std::isfinite(h.weight_decay) && h.weight_decay >= 0.0f &&
+                  std::isfinite(h.eps) && h.eps >= 0.0 && std::isfinite(h.coef[0]) &&
+                  std::isfinite(h.coef[1]) && std::isfinite(h.coef[2]) && h.steps >= 1 &&
+                  h.steps <= 16 && std::pow(std::fabs(h.coef[0]), 2.0 * h.steps) <= 1e9;
+  if (!ok) return QLORA_ERR_VALUE;
+  for (int32_t i = 0; i < n; ++i) {
+    const qlora_muon_mat &q = mats[i];
+    if (!std::isfinite(q.scale)) return QLORA_ERR_VALUE;
+    if (!q.grad || (q.theta_bf16 && !q.theta)) return QLORA_ERR_NULL;
+    for (const void *p : {static_cast<const void *>(q.grad), static_cast<const void *>(q.m),
+                          static_cast<const void *>(q.theta), static_cast<const void *>(q.update)})
+      if (!aligned_to(p, 4)) return QLORA_ERR_ALIGN;
+    if (!aligned_to(q.theta_bf16, 2)) return QLORA_ERR_ALIGN;
+  }
+  if (n == 0) return QLORA_OK;
+  if (!ws) return QLORA_ERR_NULL;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (ws_bytes < muon_workspace_bytes(mats, n)) return QLORA_ERR_WORKSPACE;
+  const MuonParams p{h.momentum, h.lr, h.weight_decay, h.nesterov != 0, h.steps,
+                     h.eps, h.coef[0], h.coef[1], h.coef[2]};
+  return dev(timed(QLORA_KERNEL_MUON, stream, [&] { return launch_muon(mats, n, p, ws, stream); }));
+}
+
 size_t qlora_token_logp_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt) {
   if (check_logits(V, T, V, dt, 1.0f) != QLORA_OK) return 0;
   return part_bytes(T, forward_segments(T, V, dt == QLORA_BF16));
@@ -896,7 +943,7 @@ void qlora_timing_reset(void) {
 const char *qlora_kernel_name(int kind) {
   static const char *names[QLORA_KERNEL_COUNT] = {
       "quantize", "xa_rowdot", "fwd_gemm", "dy_pass", "dx_gemm", "da_pass", "reduce", "fwd_smallm",
-      "token_logp", "pref_loss", "policy_loss", "dropout"};
+      "token_logp", "pref_loss", "policy_loss", "dropout", "muon"};
   if (kind < 0 || kind >= QLORA_KERNEL_COUNT) return "unknown";
   return names[kind];
 }

@@ -6,6 +6,8 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include "qlora.h"
+
 namespace qlora {
 
 // Multiplier of a rank-r intermediate (XA in the forward, G = dY B^T in the
@@ -364,5 +366,15 @@ hipError_t launch_dropout(const DropoutArgs &a, bool bf16, hipStream_t s);
 // once per device).
 constexpr size_t kNoAllocScratchBytes = size_t(32) << 20;
 hipError_t noalloc_scratch(void **ptr);
+
+// The orthogonalised update of n adapter matrices (qlora_muon_step).
+struct MuonParams {
+  float mu, lr, wd;
+  int32_t nesterov, steps;
+  double eps, a, b, c;
+};
+size_t muon_workspace_bytes(const qlora_muon_mat *mats, int32_t n);
+hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &p, void *work,
+                       hipStream_t s);
 
 }  // namespace qlora

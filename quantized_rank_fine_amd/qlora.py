@@ -23,7 +23,7 @@ STATUS = {0: "ok", 1: "null pointer", 2: "invalid shape", 3: "pointer not 16-byt
           4: "invalid dtype", 5: "workspace too small", 6: "HIP runtime error",
           7: "invalid value"}
 KERNELS = ("quantize", "xa_rowdot", "fwd_gemm", "dy_pass", "dx_gemm", "da_pass", "reduce",
-           "fwd_smallm", "token_logp", "pref_loss", "policy_loss", "dropout")
+           "fwd_smallm", "token_logp", "pref_loss", "policy_loss", "dropout", "muon")
 PREF_SIGMOID, PREF_SQUARED, PREF_HINGE = 0, 1, 2                     # qlora_pref_kind
 OBJ_NLL, OBJ_CLIP = 0, 1                                             # qlora_objective
 
@@ -66,6 +66,20 @@ class qlora_policy(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("clip_lo", ctypes.c_float),
                 ("clip_hi", ctypes.c_float), ("clip_dual", ctypes.c_float),
                 ("kl_coef", ctypes.c_float), ("ent_coef", ctypes.c_float)]
+
+
+class qlora_muon_mat(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("grad", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("theta", ctypes.c_void_p),
+                ("theta_bf16", ctypes.c_void_p), ("update", ctypes.c_void_p),
+                ("scale", ctypes.c_float)]
+
+
+class qlora_muon_hparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("nesterov", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("eps", ctypes.c_double),
+                ("coef", ctypes.c_double * 3)]
 
 
 _lib = None
@@ -124,8 +138,12 @@ def lib():
     L.qlora_policy_logits.argtypes = [vp, i64, i64, i64, ci, vp, f32, vp, vp, vp, vp, ppol, vp,
                                       vp, vp, i64, vp, sz, vp]
     L.qlora_dropout.argtypes = [vp, i64, vp, i64, i64, i64, ci, f32, u64, u64, vp, i64, vp]
+    pmat = ctypes.POINTER(qlora_muon_mat)
+    L.qlora_muon_step.argtypes = [i32, pmat, ctypes.POINTER(qlora_muon_hparams), vp, sz, vp]
+    L.qlora_muon_workspace_bytes.argtypes = [i32, pmat]
+    L.qlora_muon_workspace_bytes.restype = sz
     for f in (L.qlora_token_logp_fwd, L.qlora_token_logp_bwd, L.qlora_pref_loss,
-              L.qlora_policy_loss, L.qlora_policy_logits, L.qlora_dropout):
+              L.qlora_policy_loss, L.qlora_policy_logits, L.qlora_dropout, L.qlora_muon_step):
         f.restype = ctypes.c_int
     L.qlora_token_logp_workspace_bytes.argtypes = [i64, i64, ci]
     L.qlora_policy_logits_workspace_bytes.argtypes = [i64, i64, ci]
@@ -262,6 +280,35 @@ def qlora_adam_step(theta, grad, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-
                                  float(lr), float(beta1), float(beta2), float(eps),
                                  float(weight_decay), _ptr(theta_bf16), _stream(stream)),
            "qlora_adam_step")
+
+
+MUON_MAX_MATS = 4096                  # QLORA_MUON_MAX_MATS
+MUON_COEF = (3.4445, -4.7750, 2.0315)
+
+
+def muon_mat(rows, cols, grad, m=None, theta=None, theta_bf16=None, update=None, scale=1.0):
+    """qlora_muon_mat: one matrix of qlora_muon_step (tensors or raw pointers)."""
+    return qlora_muon_mat(int(rows), int(cols), _ptr(grad), _ptr(m), _ptr(theta),
+                          _ptr(theta_bf16), _ptr(update), float(scale))
+
+
+def muon_mats(mats):
+    """The host array of a call's matrices; may be kept as long as their buffers are."""
+    mats = list(mats)
+    return (qlora_muon_mat * len(mats))(*mats)
+
+
+def qlora_muon_workspace_bytes(mats):
+    return int(lib().qlora_muon_workspace_bytes(len(mats), mats))
+
+
+def qlora_muon_step(mats, lr, ws, ws_bytes, momentum=0.95, nesterov=True, weight_decay=0.0,
+                    eps=1e-7, steps=5, coef=MUON_COEF, stream=None):
+    """One orthogonalised step of the matrices of `mats` (from muon_mats)."""
+    hp = qlora_muon_hparams(float(lr), float(momentum), float(weight_decay), int(bool(nesterov)),
+                            int(steps), float(eps), (ctypes.c_double * 3)(*coef))
+    _check(lib().qlora_muon_step(len(mats), mats, ctypes.byref(hp), _ptr(ws), int(ws_bytes),
+                                 _stream(stream)), "qlora_muon_step")
 
 
 def qlora_loftq_workspace_bytes(n_in, n_out, k):
