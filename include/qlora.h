@@ -280,6 +280,59 @@ qlora_status qlora_linear_bwd_lora(const qlora_nf4 *wq, const void *X, const voi
                                    hipStream_t stream);
 
 /*
+ * qlora_linear_fwd_ep: the forward with an elementwise end,
+ *   z = X.deq(Wq) + U.B + bias,   y = residual + act(z) o mul
+ * (U as above).  bias [out], mul and residual [M, out] in the act dtype, each
+ * optional (NULL); Z [M, out] act dtype (output), or NULL: z, which the
+ * backward reads.  With gate and up projections, silu and mul = the up
+ * projection's output it is the gated product of a feed-forward block; with a
+ * residual alone, the projection back into the residual stream.  Computed in
+ * fp32 from the accumulators on; Y and Z are rounded once each.  Y may be mul
+ * or residual itself.
+ *   NONE z, RELU max(z, 0), SILU z sigma(z), GELU z Phi(z),
+ *   GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
+ * Shapes, dtypes, workspace and errors as in qlora_linear_fwd_lora; an unknown
+ * activation is QLORA_ERR_VALUE.
+ */
+typedef enum {
+  QLORA_EP_NONE = 0,
+  QLORA_EP_RELU = 1,
+  QLORA_EP_GELU = 2,
+  QLORA_EP_GELU_TANH = 3,
+  QLORA_EP_SILU = 4
+} qlora_ep_act;
+
+typedef struct {
+  int32_t act; /* qlora_ep_act */
+  const void *bias;
+  const void *mul;
+  const void *residual;
+  void *Z;
+} qlora_epilogue;
+
+qlora_status qlora_linear_fwd_ep(const qlora_nf4 *wq, const void *X, int64_t M, qlora_dtype act,
+                                 const void *A, const void *B, int32_t r, qlora_dtype adt,
+                                 const qlora_lora *lora, const qlora_epilogue *ep, void *Y,
+                                 float *XA, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * qlora_ep_bwd: the gradient of that end from dY [M, out],
+ *   dZ = dY o mul o act'(Z)  (act dtype; the dY of qlora_linear_bwd),
+ *   dmul = dY o act(Z)       (act dtype),
+ *   dbias = column sums of dZ before its rounding (fp32, [out])
+ * (the residual's gradient is dY itself), each output optional (NULL).  Z is
+ * the forward's; it may be NULL where neither act' nor dmul needs it (NONE).
+ * mul NULL: 1; dmul needs mul.  RELU has act'(0) = 0.  dZ may be dY or Z, and
+ * dmul mul.  out as in the linears, M <= 2^24; M = 0 writes zeros to dbias.
+ * ws: qlora_ep_bwd_workspace_bytes(M, out, act) bytes where dbias is wanted
+ * (may be 0, ws then NULL).
+ */
+qlora_status qlora_ep_bwd(const void *Z, const void *mul, const void *dY, int64_t M, int64_t out,
+                          qlora_dtype act, int32_t ep_act, void *dZ, void *dmul, float *dbias,
+                          void *ws, size_t ws_bytes, hipStream_t stream);
+size_t qlora_ep_bwd_workspace_bytes(int64_t M, int64_t out, qlora_dtype act);
+
+/*
  * The backward with one Adam (AdamW) step of A and B fused into its final
  * reduction launch (the adapter update of "The code, line by line": the
  * optimizer holds only A and B), the same arithmetic as qlora_adam_step:
@@ -674,7 +727,8 @@ typedef enum {
   QLORA_KERNEL_POLICY = 10,     /* policy loss (tokens, logits)           */
   QLORA_KERNEL_DROPOUT = 11,    /* dropout from the counter               */
   QLORA_KERNEL_MUON = 12,       /* orthogonalised update                  */
-  QLORA_KERNEL_COUNT = 13
+  QLORA_KERNEL_EP_BWD = 13,     /* gradient of the elementwise end        */
+  QLORA_KERNEL_COUNT = 14
 } qlora_kernel_kind;
 
 int qlora_timing_enable(int kind_mask);

@@ -202,6 +202,67 @@ bool lora_mul(const qlora_lora *lora, RankMul &mul) {
   return std::isfinite(mul.c);
 }
 
+// The forward, with the elementwise end `ep`.
+qlora_status linear_fwd(const qlora_nf4 *wq, const void *X, int64_t M, qlora_dtype act,
+                        const void *A, const void *B, int32_t r, qlora_dtype adt,
+                        const RankMul &mul, const Epilogue &ep, void *Y, float *XA, void *ws,
+                        size_t ws_bytes, hipStream_t stream) {
+  qlora_status st = check_nf4(wq);
+  if (st != QLORA_OK) return st;
+  if (!tokens_ok(M) || r < 0 || r > QLORA_MAX_RANK) return QLORA_ERR_SHAPE;
+  if (!dtype_ok(act) || !dtype_ok(adt)) return QLORA_ERR_DTYPE;
+  if (M == 0) return QLORA_OK;
+  if (!X || !Y || !ws) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (r > 0) {
+    if (!A || !B) return QLORA_ERR_NULL;
+    if (!aligned16(A) || !aligned16(B) || (XA && !aligned16(XA))) return QLORA_ERR_ALIGN;
+  }
+  const bool xb = act == QLORA_BF16, ab = adt == QLORA_BF16;
+  const int64_t in = wq->in, out = wq->out;
+  const FwdPlan p = plan_fwd(M, in, out, r, xb);
+  if (ws_bytes < p.total) return QLORA_ERR_WORKSPACE;
+  hipError_t e = hipSuccess;
+#define QLORA_RUN(KIND, CALL)                              \
+  do {                                                     \
+    e = timed(KIND, stream, [&] { return CALL; });         \
+    if (e != hipSuccess) return QLORA_ERR_DEVICE;          \
+  } while (0)
+  if (p.small) {
+    float *P = at<float>(ws, p.off_p);
+    float *PXA = r > 0 ? at<float>(ws, p.off_pxa) : nullptr;
+    QLORA_RUN(QLORA_KERNEL_FWD_SMALLM,
+              launch_fwd_small_partial(wq->codes, wq->qscale, wq->gscale, in, out, X, xb, M, A,
+                                       ab, r, p.kc, P, PXA, wq->codebook, g16(wq), stream));
+    QLORA_RUN(QLORA_KERNEL_REDUCE, launch_fwd_small_reduce(P, PXA, p.ks, M, out, r, B, ab, XA,
+                                                           Y, xb, stream, mul, ep));
+    return QLORA_OK;
+  }
+  const uint16_t *X16 = static_cast<const uint16_t *>(X);
+  if (!xb) {
+    uint16_t *x16 = at<uint16_t>(ws, p.off_x16);
+    QLORA_RUN(QLORA_KERNEL_REDUCE, launch_convert_to_bf16(X, false, M * in, x16, stream));
+    X16 = x16;
+  }
+  // one launch: X . A (complete, or split-K partials) and the GEMM's block scales
+  float *cs = at<float>(ws, p.off_cs);
+  float *part = p.ks > 0 ? at<float>(ws, p.off_part) : nullptr;
+  uint16_t *XA16 = r > 0 ? at<uint16_t>(ws, p.off_xa16) : nullptr;
+  QLORA_RUN(QLORA_KERNEL_XA, launch_fwd_prep(X, xb, A, ab, M, in, r, part, XA, XA16, p.rp,
+                                             wq->qscale, wq->gscale, out,
+                                             g16(wq) ? nullptr : cs, stream, mul));
+  if (p.ks > 0) {
+    QLORA_RUN(QLORA_KERNEL_REDUCE, launch_reduce2(part, p.ks, M, r, XA, false, XA16, p.rp,
+                                                  nullptr, 0, 0, nullptr, false, nullptr, 0,
+                                                  stream, mul));
+  }
+  QLORA_RUN(QLORA_KERNEL_FWD_GEMM,
+            launch_fwd_gemm(wq->codes, g16(wq) ? wq->gscale : cs, in, out, X16, M, XA16,
+                            int32_t(p.rp), B, ab, r, Y, xb, wq->codebook, g16(wq), stream, ep));
+  return QLORA_OK;
+#undef QLORA_RUN
+}
+
 // The backward, with optional Adam steps of A and B fused into the final
 // reductions (ta/tb.theta != nullptr; dA/dB may then be null).  Every read of
 // A and B comes before those reductions, so the updated adapters may alias
@@ -421,6 +482,8 @@ qlora_status adam_target(const qlora_adam_state *s, const qlora_adam_hparams *h,
   return QLORA_OK;
 }
 
+bool ep_act_ok(int32_t act) { return act >= QLORA_EP_NONE && act <= QLORA_EP_SILU; }
+
 qlora_status check_muon(int32_t n, const qlora_muon_mat *mats) {
   if (n < 0 || n > QLORA_MUON_MAX_MATS) return QLORA_ERR_SHAPE;
   if (n > 0 && !mats) return QLORA_ERR_NULL;
@@ -495,60 +558,58 @@ qlora_status qlora_linear_fwd_lora(const qlora_nf4 *wq, const void *X, int64_t M
                                    void *ws, size_t ws_bytes, hipStream_t stream) {
   RankMul mul;
   if (!lora_mul(lora, mul)) return QLORA_ERR_VALUE;
-  qlora_status st = check_nf4(wq);
-  if (st != QLORA_OK) return st;
-  if (!tokens_ok(M) || r < 0 || r > QLORA_MAX_RANK) return QLORA_ERR_SHAPE;
-  if (!dtype_ok(act) || !dtype_ok(adt)) return QLORA_ERR_DTYPE;
-  if (M == 0) return QLORA_OK;
-  if (!X || !Y || !ws) return QLORA_ERR_NULL;
-  if (!aligned16(X) || !aligned16(Y) || !aligned16(ws)) return QLORA_ERR_ALIGN;
-  if (r > 0) {
-    if (!A || !B) return QLORA_ERR_NULL;
-    if (!aligned16(A) || !aligned16(B) || (XA && !aligned16(XA))) return QLORA_ERR_ALIGN;
-  }
-  const bool xb = act == QLORA_BF16, ab = adt == QLORA_BF16;
-  const int64_t in = wq->in, out = wq->out;
-  const FwdPlan p = plan_fwd(M, in, out, r, xb);
-  if (ws_bytes < p.total) return QLORA_ERR_WORKSPACE;
-  hipError_t e = hipSuccess;
-#define QLORA_RUN(KIND, CALL)                              \
-  do {                                                     \
-    e = timed(KIND, stream, [&] { return CALL; });         \
-    if (e != hipSuccess) return QLORA_ERR_DEVICE;          \
-  } while (0)
-  if (p.small) {
-    float *P = at<float>(ws, p.off_p);
-    float *PXA = r > 0 ? at<float>(ws, p.off_pxa) : nullptr;
-    QLORA_RUN(QLORA_KERNEL_FWD_SMALLM,
-              launch_fwd_small_partial(wq->codes, wq->qscale, wq->gscale, in, out, X, xb, M, A,
-                                       ab, r, p.kc, P, PXA, wq->codebook, g16(wq), stream));
-    QLORA_RUN(QLORA_KERNEL_REDUCE, launch_fwd_small_reduce(P, PXA, p.ks, M, out, r, B, ab, XA,
-                                                           Y, xb, stream, mul));
-    return QLORA_OK;
-  }
-  const uint16_t *X16 = static_cast<const uint16_t *>(X);
-  if (!xb) {
-    uint16_t *x16 = at<uint16_t>(ws, p.off_x16);
-    QLORA_RUN(QLORA_KERNEL_REDUCE, launch_convert_to_bf16(X, false, M * in, x16, stream));
-    X16 = x16;
-  }
-  // one launch: X . A (complete, or split-K partials) and the GEMM's block scales
-  float *cs = at<float>(ws, p.off_cs);
-  float *part = p.ks > 0 ? at<float>(ws, p.off_part) : nullptr;
-  uint16_t *XA16 = r > 0 ? at<uint16_t>(ws, p.off_xa16) : nullptr;
-  QLORA_RUN(QLORA_KERNEL_XA, launch_fwd_prep(X, xb, A, ab, M, in, r, part, XA, XA16, p.rp,
-                                             wq->qscale, wq->gscale, out,
-                                             g16(wq) ? nullptr : cs, stream, mul));
-  if (p.ks > 0) {
-    QLORA_RUN(QLORA_KERNEL_REDUCE, launch_reduce2(part, p.ks, M, r, XA, false, XA16, p.rp,
-                                                  nullptr, 0, 0, nullptr, false, nullptr, 0,
-                                                  stream, mul));
-  }
-  QLORA_RUN(QLORA_KERNEL_FWD_GEMM,
-            launch_fwd_gemm(wq->codes, g16(wq) ? wq->gscale : cs, in, out, X16, M, XA16,
-                            int32_t(p.rp), B, ab, r, Y, xb, wq->codebook, g16(wq), stream));
-  return QLORA_OK;
-#undef QLORA_RUN
+  return linear_fwd(wq, X, M, act, A, B, r, adt, mul, Epilogue(), Y, XA, ws, ws_bytes, stream);
+}
+
+qlora_status qlora_linear_fwd_ep(const qlora_nf4 *wq, const void *X, int64_t M, qlora_dtype act,
+                                 const void *A, const void *B, int32_t r, qlora_dtype adt,
+                                 const qlora_lora *lora, const qlora_epilogue *ep, void *Y,
+                                 float *XA, void *ws, size_t ws_bytes, hipStream_t stream) {
+  RankMul mul;
+  if (!lora_mul(lora, mul)) return QLORA_ERR_VALUE;
+  if (!ep) return QLORA_ERR_NULL;
+  if (!ep_act_ok(ep->act)) return QLORA_ERR_VALUE;
+  for (const void *p : {ep->bias, ep->mul, ep->residual, static_cast<const void *>(ep->Z)})
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  Epilogue e;
+  e.act = ep->act;
+  e.bias = ep->bias;
+  e.mul = ep->mul;
+  e.res = ep->residual;
+  e.z = ep->Z;
+  return linear_fwd(wq, X, M, act, A, B, r, adt, mul, e, Y, XA, ws, ws_bytes, stream);
+}
+
+size_t qlora_ep_bwd_workspace_bytes(int64_t M, int64_t out, qlora_dtype act) {
+  if (!tokens_ok(M) || M == 0 || !shape_ok(64, out) || !dtype_ok(act)) return 0;
+  const int64_t slabs = ep_bwd_slabs(M);
+  return slabs > 1 ? size_t(slabs) * out * sizeof(double) : 0;
+}
+
+qlora_status qlora_ep_bwd(const void *Z, const void *mul, const void *dY, int64_t M, int64_t out,
+                          qlora_dtype act, int32_t ep_act, void *dZ, void *dmul, float *dbias,
+                          void *ws, size_t ws_bytes, hipStream_t stream) {
+  if (!tokens_ok(M) || !shape_ok(64, out)) return QLORA_ERR_SHAPE;
+  if (!dtype_ok(act)) return QLORA_ERR_DTYPE;
+  if (!ep_act_ok(ep_act)) return QLORA_ERR_VALUE;
+  if (!aligned16(dbias)) return QLORA_ERR_ALIGN;
+  if (M == 0)
+    return dbias ? dev(timed(QLORA_KERNEL_EP_BWD, stream,
+                             [&] { return launch_fill_zero(dbias, out, stream); }))
+                 : QLORA_OK;
+  // Z is read for act' and for dmul
+  if (!dY || (dmul && !mul) || (!Z && (ep_act != QLORA_EP_NONE || dmul))) return QLORA_ERR_NULL;
+  for (const void *p : {Z, mul, dY, static_cast<const void *>(dZ), static_cast<const void *>(dmul)})
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  const size_t need = dbias ? qlora_ep_bwd_workspace_bytes(M, out, act) : 0;
+  if (need && !ws) return QLORA_ERR_NULL;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  if (!dZ && !dmul && !dbias) return QLORA_OK;
+  const EpBwdArgs a{ep_act != QLORA_EP_NONE || dmul ? Z : nullptr, mul, dY, dZ, dmul, dbias,
+                    static_cast<double *>(ws), M, out, 0, ep_act};
+  return dev(timed(QLORA_KERNEL_EP_BWD, stream,
+                   [&] { return launch_ep_bwd(a, act == QLORA_BF16, stream); }));
 }
 
 qlora_status qlora_linear_fwd_noalloc(const qlora_nf4 *wq, const void *X, int64_t M,
@@ -943,7 +1004,7 @@ void qlora_timing_reset(void) {
 const char *qlora_kernel_name(int kind) {
   static const char *names[QLORA_KERNEL_COUNT] = {
       "quantize", "xa_rowdot", "fwd_gemm", "dy_pass", "dx_gemm", "da_pass", "reduce", "fwd_smallm",
-      "token_logp", "pref_loss", "policy_loss", "dropout", "muon"};
+      "token_logp", "pref_loss", "policy_loss", "dropout", "muon", "ep_bwd"};
   if (kind < 0 || kind >= QLORA_KERNEL_COUNT) return "unknown";
   return names[kind];
 }

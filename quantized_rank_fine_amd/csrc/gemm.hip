@@ -45,6 +45,7 @@
 #include <type_traits>
 
 #include "device.h"
+#include "epilogue.h"
 
 namespace qlora {
 namespace {
@@ -868,13 +869,138 @@ __device__ __forceinline__ void epilogue(f32x16_t (&acc)[2][8], char *smem, cons
   round(std::integral_constant<int, 1>{});
 }
 
+// The epilogue with bias, activation, factor, residual and a saved z.  As
+// above up to the joined sums, which are staged in fp32 so that the output is
+// rounded once; the elementwise part runs where whole row segments leave, with
+// the segments of mul and res requested before the exchange (one wavefront to
+// a SIMD has the registers, and nothing else hides their latency).
+template <bool kOutBf16>
+__device__ __forceinline__ void epilogue_ep(f32x16_t (&acc)[2][8], char *smem, const RankOps &ro,
+                                            const uint16_t *__restrict__ P16, int ldp,
+                                            const AdapterRef q, int64_t M, int64_t N, int64_t m0,
+                                            int64_t n0, void *Y, const Epilogue &ep) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ch = wave & 1, kh = wave >> 1;
+  const int l32 = lane & 31, h2 = lane >> 5;
+  const int64_t nw = n0 + 64 * ch;
+
+  if (kh == 0 && q.r > 0) {
+    rank_mfmas(acc, ro, q, 0, M, N, m0, nw);
+    for (int r0 = 16; r0 < q.r; r0 += 16) {
+      RankOps o;
+      load_rank_ops(o, P16, ldp, q, r0, M, N, m0, nw);
+      rank_mfmas(acc, o, q, r0, M, N, m0, nw);
+    }
+  }
+
+  constexpr int W = kWide<kOutBf16>, kOE = kOutBf16 ? 2 : 4;
+  constexpr int kOPitch = 272;                                // 64 fp32 and 16 bytes
+  static_assert(65536 + 2 * 128 * kOPitch <= Geo<false>::kLdsBytes, "epilogue LDS");
+  char *stg = smem + 65536 + ch * 128 * kOPitch;              // 128 rows x 64 columns per ch
+  char *wr = smem + (ch * 2 + kh) * 16384 + lane * 16;        // this wavefront's region
+  const char *rd = smem + (ch * 2 + (1 - kh)) * 16384 + lane * 16;   // the partner's
+  const bool ncol = nw < N;                                   // N % 64 == 0
+  // wavefront kh stores staged rows 64 kh .. 64 kh + 63 of a round's 128: a
+  // lane has the same W columns of every row it touches
+  constexpr int kSegs = 64 / W;                               // lanes to a row
+  constexpr int kIts = kSegs;                                 // rows of a lane in a round
+  constexpr int kAhead = kOutBf16 ? kIts : kIts / 2;          // of them, requested together
+  const int col = W * (lane % kSegs), row0 = 64 * kh + lane / kSegs;
+  float bias[W];
+#pragma unroll
+  for (int e = 0; e < W; ++e) bias[e] = 0.0f;
+  if (ep.bias && ncol)
+    widen<kOutBf16>(*reinterpret_cast<const u32x4_t *>(static_cast<const char *>(ep.bias) +
+                                                       (nw + col) * kOE), bias);
+  auto round = [&](auto H) {
+    constexpr int h = decltype(H)::value;
+    u32x4_t mu[kAhead], re[kAhead];
+    auto request = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t m = m0 + 128 * h + row0 + (64 / kSegs) * (i0 + i);
+        const int64_t at = ncol && m < M ? (m * N + nw + col) * kOE : 0;   // (0: not used)
+        if (ep.mul) mu[i] = *reinterpret_cast<const u32x4_t *>(static_cast<const char *>(ep.mul) + at);
+        if (ep.res) re[i] = *reinterpret_cast<const u32x4_t *>(static_cast<const char *>(ep.res) + at);
+      }
+    };
+    request(0);
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const f32x16_t v = acc[1][4 * h + f];
+      char *w = wr + f * 4096;
+      *reinterpret_cast<f32x4_t *>(w) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+      *reinterpret_cast<f32x4_t *>(w + 1024) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+      *reinterpret_cast<f32x4_t *>(w + 2048) = __builtin_shufflevector(v, v, 8, 9, 10, 11);
+      *reinterpret_cast<f32x4_t *>(w + 3072) = __builtin_shufflevector(v, v, 12, 13, 14, 15);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const f32x4_t x = *reinterpret_cast<const f32x4_t *>(rd + f * 4096 + c * 1024);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<float *>(stg + (32 * f + 8 * c + 4 * h2 + e) * kOPitch +
+                                     (32 * kh + l32) * 4) = acc[0][4 * h + f][4 * c + e] + x[e];
+      }
+    }
+    __syncthreads();
+    with_act(ep.act, [&](auto A) {
+      constexpr int act = decltype(A)::value;
+#pragma unroll
+      for (int i0 = 0; i0 < kIts; i0 += kAhead) {
+        if (i0 > 0) request(i0);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int row = row0 + (64 / kSegs) * (i0 + i);
+          const int64_t m = m0 + 128 * h + row;
+          if (!ncol || m >= M) continue;
+          float z[W], y[W], g[W];
+#pragma unroll
+          for (int e = 0; e < W; e += 4) {
+            const f32x4_t v = *reinterpret_cast<const f32x4_t *>(stg + row * kOPitch + (col + e) * 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[e + k] = v[k] + bias[e + k];
+          }
+          const int64_t at = (m * N + nw + col) * kOE;
+          if (ep.z)
+            __builtin_nontemporal_store(narrow<kOutBf16>(z), reinterpret_cast<u32x4_t *>(
+                                                                 static_cast<char *>(ep.z) + at));
+#pragma unroll
+          for (int e = 0; e < W; ++e) y[e] = activated<act>(z[e]);
+          if (ep.mul) {
+            widen<kOutBf16>(mu[i], g);
+#pragma unroll
+            for (int e = 0; e < W; ++e) y[e] *= g[e];
+          }
+          if (ep.res) {
+            widen<kOutBf16>(re[i], g);
+#pragma unroll
+            for (int e = 0; e < W; ++e) y[e] += g[e];
+          }
+          __builtin_nontemporal_store(narrow<kOutBf16>(y), reinterpret_cast<u32x4_t *>(
+                                                               static_cast<char *>(Y) + at));
+        }
+      }
+    });
+  };
+  // (the barriers as in epilogue())
+  __syncthreads();
+  round(std::integral_constant<int, 0>{});
+  round(std::integral_constant<int, 1>{});
+}
+
 // ================================================================ forward
-template <bool kOutBf16, bool kG16>
+// kEp: with the elementwise end of `ep`.
+template <bool kOutBf16, bool kG16, bool kEp>
 __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(
     const uint8_t *__restrict__ codes, const float *__restrict__ cs, int64_t K, int64_t N,
     const uint16_t *__restrict__ X16, int64_t M, const uint16_t *__restrict__ XA16,
-    int ldp, AdapterRef bq, void *__restrict__ Y, ExpandConsts tb,
-    int nt_count) {
+    int ldp, AdapterRef bq, void *Y, ExpandConsts tb,
+    int nt_count, Epilogue ep) {
   extern __shared__ __align__(16) char smem[];
   int mt, nt;
   tile_of(nt_count, mt, nt);
@@ -891,7 +1017,10 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(
       for (int r = 0; r < 16; ++r) acc[b][i][r] = 0.f;
   gemm_mainloop<true, kG16>(X16, M, K, N, codes, cs, m0, n0, tb, smem, acc, DbFold{});
   // rank-r term: y += XA16 . B (B read as rows n of B^T)
-  epilogue<kOutBf16>(acc, smem, ro, XA16, ldp, bq, M, N, m0, n0, Y);
+  if constexpr (kEp)
+    epilogue_ep<kOutBf16>(acc, smem, ro, XA16, ldp, bq, M, N, m0, n0, Y, ep);
+  else
+    epilogue<kOutBf16>(acc, smem, ro, XA16, ldp, bq, M, N, m0, n0, Y);
 }
 
 // ================================================================ dX
@@ -930,28 +1059,34 @@ bool set_lds(const void *fn, int bytes) {
 hipError_t launch_fwd_gemm(const uint8_t *codes, const float *cs, int64_t K, int64_t N,
                            const uint16_t *X16, int64_t M, const uint16_t *XA16, int32_t ldp,
                            const void *B, bool b_bf16, int32_t r, void *Y, bool y_bf16,
-                           int codebook, bool g16, hipStream_t s) {
+                           int codebook, bool g16, hipStream_t s, const Epilogue &ep) {
   if (M == 0) return hipSuccess;
   const AdapterRef bq{B, b_bf16, 1, N, int(r)};
   const int mtc = int((M + BM - 1) / BM), ntc = int((N + BN - 1) / BN);
   dim3 grid(unsigned(mtc * ntc));
   if (!tables(codebook).symmetric) return hipErrorInvalidValue;
   const ExpandConsts tb = tables(codebook).expand;
-#define QLORA_FWD(OB, G)                                                                        \
-  do {                                                                                          \
-    constexpr int lds = Geo<G>::kLdsBytes;                                                      \
-    static bool ok = set_lds(reinterpret_cast<const void *>(&fwd_gemm_kernel<OB, G>), lds);     \
-    if (!ok) return hipErrorInvalidValue;                                                       \
-    hipLaunchKernelGGL((fwd_gemm_kernel<OB, G>), grid, dim3(kThreads), lds, s, codes, cs, K, N, \
-                       X16, M, XA16, int(ldp), bq, Y, tb, ntc);                                 \
+#define QLORA_FWD(OB, G, EP)                                                                     \
+  do {                                                                                           \
+    constexpr int lds = Geo<G>::kLdsBytes;                                                       \
+    static bool ok = set_lds(reinterpret_cast<const void *>(&fwd_gemm_kernel<OB, G, EP>), lds);  \
+    if (!ok) return hipErrorInvalidValue;                                                        \
+    hipLaunchKernelGGL((fwd_gemm_kernel<OB, G, EP>), grid, dim3(kThreads), lds, s, codes, cs, K, \
+                       N, X16, M, XA16, int(ldp), bq, Y, tb, ntc, ep);                           \
+  } while (0)
+#define QLORA_FWD_EP(OB, G)               \
+  do {                                    \
+    if (ep.plain()) QLORA_FWD(OB, G, false); \
+    else QLORA_FWD(OB, G, true);          \
   } while (0)
   if (g16) {
-    if (y_bf16) QLORA_FWD(true, true);
-    else QLORA_FWD(false, true);
+    if (y_bf16) QLORA_FWD_EP(true, true);
+    else QLORA_FWD_EP(false, true);
   } else {
-    if (y_bf16) QLORA_FWD(true, false);
-    else QLORA_FWD(false, false);
+    if (y_bf16) QLORA_FWD_EP(true, false);
+    else QLORA_FWD_EP(false, false);
   }
+#undef QLORA_FWD_EP
 #undef QLORA_FWD
   return hipGetLastError();
 }

@@ -164,6 +164,30 @@ hipError_t launch_reduce2(const float *part_a, int64_t ks_a, int64_t rows_a, int
                           const AdamTarget &adam_a = AdamTarget(),
                           const AdamTarget &adam_b = AdamTarget());
 
+// The elementwise end of a forward: y = res + act(z) mul with z = the linear +
+// bias.  bias [out], mul, res and the saved z [M x out] in the activation dtype,
+// each optional.
+constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4;
+struct Epilogue {
+  int act = kActNone;
+  const void *bias = nullptr, *mul = nullptr, *res = nullptr;
+  void *z = nullptr;
+  bool plain() const { return act == kActNone && !bias && !mul && !res && !z; }
+};
+
+// The gradient of such an end (outputs optional).  partial: ep_bwd_slabs(M) * out
+// doubles where dbias is wanted and that is more than one slab.
+struct EpBwdArgs {
+  const void *Z, *mul, *dY;
+  void *dZ, *dmul;
+  float *dbias;
+  double *partial;
+  int64_t M, out, slab;
+  int act;
+};
+int64_t ep_bwd_slabs(int64_t M);
+hipError_t launch_ep_bwd(EpBwdArgs a, bool bf16, hipStream_t s);
+
 // y = X16 . deq(Wq) + XA16 . B (K = in, N = out).  X16 [M x K] bf16; XA16
 // [M x ldp] bf16 with zero padding columns r..ldp-1; B [r x N] (f32 or bf16)
 // as given by the caller; cs from the prep pass (rows = K), or with g16 the
@@ -172,7 +196,7 @@ hipError_t launch_fwd_gemm(const uint8_t *codes, const float *cs, int64_t K,
                            int64_t N, const uint16_t *X16, int64_t M,
                            const uint16_t *XA16, int32_t ldp, const void *B,
                            bool b_bf16, int32_t r, void *Y, bool y_bf16, int codebook,
-                           bool g16, hipStream_t s);
+                           bool g16, hipStream_t s, const Epilogue &ep = Epilogue());
 
 // dX = dY16 . deq(Wq)^T + G16 . A^T.  dY16 [M x out] bf16; G16 [M x ldp] bf16
 // zero-padded; A [in x r] (f32 or bf16) as given; cs as in the forward.
@@ -204,7 +228,7 @@ hipError_t launch_fwd_small_partial(const uint8_t *codes, const int8_t *qscale,
 hipError_t launch_fwd_small_reduce(const float *P, const float *PXA, int64_t KS, int64_t M,
                                    int64_t N, int64_t r, const void *B, bool b_bf16, float *XA,
                                    void *Y, bool y_bf16, hipStream_t s,
-                          RankMul mul = RankMul());
+                                   RankMul mul = RankMul(), const Epilogue &ep = Epilogue());
 
 // Up to kSmallMaxGroup independent few-token linears (same M, r and dtypes)
 // in the same two launches: each workgroup of the partial pass (and of the

@@ -27,6 +27,7 @@
 // double quantization) takes the same route with one scale per (k row,
 // 16-column MFMA tile q): the activation operand is scaled once per q.
 #include "device.h"
+#include "epilogue.h"
 
 namespace qlora {
 namespace {
@@ -408,8 +409,11 @@ struct SmallReduceArgs {
   RankMul mul;
 };
 
-template <bool kY16, bool kB16>
-__device__ __forceinline__ void fwd_small_reduce_block(const SmallReduceArgs &ra, int bx) {
+// kEp: with the elementwise end `ep`, whose operands are requested with the
+// partials.
+template <bool kY16, bool kB16, bool kEp>
+__device__ __forceinline__ void fwd_small_reduce_block(const SmallReduceArgs &ra, int bx,
+                                                       const Epilogue &ep) {
   const float *__restrict__ P = ra.P;
   const float *__restrict__ PXA = ra.PXA;
   const int64_t KS = ra.KS, M = ra.M, N = ra.N, r = ra.r;
@@ -446,6 +450,18 @@ __device__ __forceinline__ void fwd_small_reduce_block(const SmallReduceArgs &ra
                                           rP, uint32_t(((u * M + m) * N + n) * 4), 0, 0));
 #pragma unroll
   for (int q = 0; q < 16; ++q) bv[q] = load_b(q);
+  float bias = 0.0f, mu = 1.0f, re = 0.0f;
+  if constexpr (kEp) {
+    auto load_y = [](const void *p, int64_t i) {
+      return kY16 ? __uint_as_float(uint32_t(static_cast<const uint16_t *>(p)[i]) << 16)
+                  : static_cast<const float *>(p)[i];
+    };
+    if (ok) {
+      if (ep.bias) bias = load_y(ep.bias, n);
+      if (ep.mul) mu = load_y(ep.mul, int64_t(m) * N + n);
+      if (ep.res) re = load_y(ep.res, int64_t(m) * N + n);
+    }
+  }
   // ---- XA = sum over chunks of PXA
   for (int e = t; e < ER; e += kThreads) {
     float xv[32];
@@ -485,16 +501,27 @@ __device__ __forceinline__ void fwd_small_reduce_block(const SmallReduceArgs &ra
     for (int q = 0; q < 16; ++q)
       if (j0 + q < r) ua += xa[m][j0 + q] * bv[q];
   }
-  const float y = sum + ua;
-  if (kY16)
-    static_cast<uint16_t *>(Y)[int64_t(m) * N + n] = __builtin_bit_cast(uint16_t, (__bf16)y);
-  else
-    static_cast<float *>(Y)[int64_t(m) * N + n] = y;
+  float y = sum + ua;
+  auto store = [&](void *p, float v) {
+    if (kY16)
+      static_cast<uint16_t *>(p)[int64_t(m) * N + n] = __builtin_bit_cast(uint16_t, (__bf16)v);
+    else
+      static_cast<float *>(p)[int64_t(m) * N + n] = v;
+  };
+  if constexpr (kEp) {
+    const float z = y + bias;
+    if (ep.z) store(ep.z, z);
+    with_act(ep.act, [&](auto A) { y = activated<decltype(A)::value>(z); });
+    if (ep.mul) y *= mu;
+    if (ep.res) y += re;
+  }
+  store(Y, y);
 }
 
-template <bool kY16, bool kB16>
-__global__ __launch_bounds__(kThreads) void fwd_small_reduce_kernel(SmallReduceArgs ra) {
-  fwd_small_reduce_block<kY16, kB16>(ra, int(blockIdx.x));
+template <bool kY16, bool kB16, bool kEp>
+__global__ __launch_bounds__(kThreads) void fwd_small_reduce_kernel(SmallReduceArgs ra,
+                                                                    Epilogue ep) {
+  fwd_small_reduce_block<kY16, kB16, kEp>(ra, int(blockIdx.x), ep);
 }
 
 struct SmallReduceGroup {
@@ -510,7 +537,7 @@ __global__ __launch_bounds__(kThreads) void fwd_small_reduce_group_kernel(SmallR
 #pragma unroll
   for (int j = 1; j < kSmallMaxGroup; ++j)
     if (j < g.n && bid >= g.base[j]) l = j;
-  fwd_small_reduce_block<kY16, kB16>(g.a[l], bid - g.base[l]);
+  fwd_small_reduce_block<kY16, kB16, false>(g.a[l], bid - g.base[l], Epilogue());
 }
 
 }  // namespace
@@ -568,18 +595,28 @@ hipError_t launch_fwd_small_partial(const uint8_t *codes, const int8_t *qscale,
 
 hipError_t launch_fwd_small_reduce(const float *P, const float *PXA, int64_t KS, int64_t M,
                                    int64_t N, int64_t r, const void *B, bool b_bf16, float *XA,
-                                   void *Y, bool y_bf16, hipStream_t s,
-                         RankMul mul) {
+                                   void *Y, bool y_bf16, hipStream_t s, RankMul mul,
+                                   const Epilogue &ep) {
   const int cols = reduce_cols(M);
   const dim3 grid = dim3(unsigned((N + cols - 1) / cols));
   const SmallReduceArgs ra{P, PXA, KS, M, N, r, cols, B, XA, Y, mul};
+#define QLORA_REDUCE(YB, BB)                                                                      \
+  do {                                                                                            \
+    if (ep.plain())                                                                               \
+      hipLaunchKernelGGL((fwd_small_reduce_kernel<YB, BB, false>), grid, dim3(kThreads), 0, s, ra, \
+                         ep);                                                                     \
+    else                                                                                          \
+      hipLaunchKernelGGL((fwd_small_reduce_kernel<YB, BB, true>), grid, dim3(kThreads), 0, s, ra,  \
+                         ep);                                                                     \
+  } while (0)
   if (y_bf16) {
-    if (b_bf16) hipLaunchKernelGGL((fwd_small_reduce_kernel<true, true>), grid, dim3(kThreads), 0, s, ra);
-    else hipLaunchKernelGGL((fwd_small_reduce_kernel<true, false>), grid, dim3(kThreads), 0, s, ra);
+    if (b_bf16) QLORA_REDUCE(true, true);
+    else QLORA_REDUCE(true, false);
   } else {
-    if (b_bf16) hipLaunchKernelGGL((fwd_small_reduce_kernel<false, true>), grid, dim3(kThreads), 0, s, ra);
-    else hipLaunchKernelGGL((fwd_small_reduce_kernel<false, false>), grid, dim3(kThreads), 0, s, ra);
+    if (b_bf16) QLORA_REDUCE(false, true);
+    else QLORA_REDUCE(false, false);
   }
+#undef QLORA_REDUCE
   return hipGetLastError();
 }
 

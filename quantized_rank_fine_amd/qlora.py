@@ -23,8 +23,10 @@ STATUS = {0: "ok", 1: "null pointer", 2: "invalid shape", 3: "pointer not 16-byt
           4: "invalid dtype", 5: "workspace too small", 6: "HIP runtime error",
           7: "invalid value"}
 KERNELS = ("quantize", "xa_rowdot", "fwd_gemm", "dy_pass", "dx_gemm", "da_pass", "reduce",
-           "fwd_smallm", "token_logp", "pref_loss", "policy_loss", "dropout", "muon")
+           "fwd_smallm", "token_logp", "pref_loss", "policy_loss", "dropout", "muon",
+           "ep_bwd")
 PREF_SIGMOID, PREF_SQUARED, PREF_HINGE = 0, 1, 2                     # qlora_pref_kind
+EP_NONE, EP_RELU, EP_GELU, EP_GELU_TANH, EP_SILU = 0, 1, 2, 3, 4      # qlora_ep_act
 OBJ_NLL, OBJ_CLIP = 0, 1                                             # qlora_objective
 
 
@@ -44,6 +46,11 @@ class qlora_nf4(ctypes.Structure):
 class qlora_lora(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("dropout_p", ctypes.c_float),
                 ("keep", ctypes.c_void_p)]
+
+
+class qlora_epilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("Z", ctypes.c_void_p)]
 
 
 class qlora_adam_state(ctypes.Structure):
@@ -109,6 +116,11 @@ def lib():
                                         plora, vp, vp, vp, sz, vp]
     L.qlora_linear_bwd_lora.argtypes = [pnf4, vp, vp, i64, ctypes.c_int, vp, vp, i32,
                                         ctypes.c_int, plora, vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_linear_fwd_ep.argtypes = [pnf4, vp, i64, ctypes.c_int, vp, vp, i32, ctypes.c_int,
+                                      plora, ctypes.POINTER(qlora_epilogue), vp, vp, vp, sz, vp]
+    L.qlora_ep_bwd.argtypes = [vp, vp, vp, i64, i64, ctypes.c_int, i32, vp, vp, vp, vp, sz, vp]
+    L.qlora_ep_bwd_workspace_bytes.argtypes = [i64, i64, ctypes.c_int]
+    L.qlora_ep_bwd_workspace_bytes.restype = sz
     pst, php = ctypes.POINTER(qlora_adam_state), ctypes.POINTER(qlora_adam_hparams)
     L.qlora_linear_bwd_adam.argtypes = [pnf4, vp, vp, i64, ctypes.c_int, vp, vp, i32,
                                         ctypes.c_int, plora, vp, vp, pst, pst, php, vp, vp, vp,
@@ -143,7 +155,8 @@ def lib():
     L.qlora_muon_workspace_bytes.argtypes = [i32, pmat]
     L.qlora_muon_workspace_bytes.restype = sz
     for f in (L.qlora_token_logp_fwd, L.qlora_token_logp_bwd, L.qlora_pref_loss,
-              L.qlora_policy_loss, L.qlora_policy_logits, L.qlora_dropout, L.qlora_muon_step):
+              L.qlora_policy_loss, L.qlora_policy_logits, L.qlora_dropout, L.qlora_muon_step,
+              L.qlora_linear_fwd_ep, L.qlora_ep_bwd):
         f.restype = ctypes.c_int
     L.qlora_token_logp_workspace_bytes.argtypes = [i64, i64, ci]
     L.qlora_policy_logits_workspace_bytes.argtypes = [i64, i64, ci]
@@ -381,6 +394,36 @@ def qlora_linear_bwd_lora(wq, X, dY, M, act, A, B, r, adt, scale, dropout_p, kee
                                        _ptr(XA), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws),
                                        int(ws_bytes), _stream(stream)),
            "qlora_linear_bwd_lora")
+
+
+def epilogue_struct(act=EP_NONE, bias=None, mul=None, residual=None, Z=None):
+    """qlora_epilogue: the elementwise end of qlora_linear_fwd_ep (device tensors
+    or None; Z receives the value before the activation)."""
+    return qlora_epilogue(int(act), _ptr(bias), _ptr(mul), _ptr(residual), _ptr(Z))
+
+
+def qlora_linear_fwd_ep(wq, X, M, act, A, B, r, adt, scale, dropout_p, keep, ep, Y, XA, ws,
+                        ws_bytes, stream=None):
+    """qlora_linear_fwd_lora with the elementwise end `ep` (from epilogue_struct):
+    Y = residual + act(Z) mul, Z = the linear + bias."""
+    s = wq.struct() if isinstance(wq, NF4Weight) else wq
+    o = _lora(scale, dropout_p, keep)
+    _check(lib().qlora_linear_fwd_ep(ctypes.byref(s), _ptr(X), int(M), int(act), _ptr(A),
+                                     _ptr(B), int(r), int(adt), ctypes.byref(o),
+                                     ctypes.byref(ep), _ptr(Y), _ptr(XA), _ptr(ws),
+                                     int(ws_bytes), _stream(stream)), "qlora_linear_fwd_ep")
+
+
+def qlora_ep_bwd_workspace_bytes(M, n_out, act=BF16):
+    return int(lib().qlora_ep_bwd_workspace_bytes(int(M), int(n_out), int(act)))
+
+
+def qlora_ep_bwd(Z, mul, dY, M, n_out, act, ep_act, dZ, dmul, dbias, ws, ws_bytes, stream=None):
+    """The gradient of the elementwise end: dZ (qlora_linear_bwd's dY), dmul and
+    dbias, each of which may be None."""
+    _check(lib().qlora_ep_bwd(_ptr(Z), _ptr(mul), _ptr(dY), int(M), int(n_out), int(act),
+                              int(ep_act), _ptr(dZ), _ptr(dmul), _ptr(dbias), _ptr(ws),
+                              int(ws_bytes), _stream(stream)), "qlora_ep_bwd")
 
 
 def qlora_linear_bwd_adam(wq, X, dY, M, act, A, B, r, adt, XA, dX, state_A, state_B, step, lr,
