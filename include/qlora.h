@@ -569,6 +569,54 @@ qlora_status qlora_token_logp_bwd(const void *logits, int64_t ld, int64_t T, int
                                   hipStream_t stream);
 
 /*
+ * qlora_token_top: the k most likely words of each row, with log p of the label
+ * and the entropy, in one pass over the logits.
+ *   ids [T, k] int32 (output), top [T, k] fp32 (output): words and their log p
+ *   in descending order of the logits, of equal ones the lower index first (0
+ *   and -0 are equal; words at -inf have log p = -inf).
+ *   labels as above, or NULL: every row is scored and logp must be NULL.
+ *   logp [T], entropy [T] fp32 (outputs), each optional (NULL).
+ * A row that is not scored has ids = -1 and zeros.  The ids of a row with a NaN
+ * leave the NaN words out, and are -1 where too few are left.
+ * 1 <= k <= QLORA_MAX_TOP, k <= V.  ws: qlora_token_top_workspace_bytes(T, V,
+ * dt, k) bytes (may be 0, ws then NULL).  T = 0 is a no-op.
+ */
+#define QLORA_MAX_TOP 64
+qlora_status qlora_token_top(const void *logits, int64_t ld, int64_t T, int64_t V,
+                             qlora_dtype dt, const int64_t *labels, float scale, int32_t k,
+                             int32_t *ids, float *top, float *logp, float *entropy, void *ws,
+                             size_t ws_bytes, hipStream_t stream);
+size_t qlora_token_top_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt, int32_t k);
+
+/*
+ * qlora_distill_logits: the divergence of a row's distribution from a teacher's
+ * alternatives (as qlora_token_top stores them) and the logits' gradient, in
+ * one pass.  With t_j = teacher[t, j] for the alternatives whose word ids[t, j]
+ * lies in [0, V) (the others do not count, -1 say; a word may occur more than
+ * once, each for itself),
+ *   q_j = exp(t_j) / sum_i exp(t_i) if `normalize`, else exp(t_j);  C = sum_j q_j,
+ *   kl = sum_j q_j (ln q_j - log p_(ids_j))  (0 where q_j = 0),
+ *   loss [1] = sum weight kl,
+ *   dlogits_v = weight s (C p_v - sum_(ids_j = v) q_j).
+ *   weight [T]: a token's share of the loss (as in qlora_policy_loss; 0: the
+ *     token is skipped, whatever its other inputs hold; NULL: all 1).
+ *   ids [T, k] int32, teacher [T, k] fp32; t_j = -inf is q_j = 0.
+ *   kl [T] fp32 (output; 0 for a skipped token); dlogits as in
+ *   qlora_token_logp_bwd, also in place; 0 in the rows that are skipped or
+ *   have no q_j > 0.
+ * A word with q_j > 0 that the row cannot give (-inf) makes its kl infinite;
+ * its gradient is that of the formula.
+ * 1 <= k <= QLORA_MAX_TOP.  ws: qlora_distill_workspace_bytes(T, V, dt, k) bytes
+ * (may be 0, ws then NULL).  T = 0 gives loss = 0.
+ */
+qlora_status qlora_distill_logits(const void *logits, int64_t ld, int64_t T, int64_t V,
+                                  qlora_dtype dt, float scale, const float *weight, int32_t k,
+                                  const int32_t *ids, const float *teacher, int32_t normalize,
+                                  float *loss, float *kl, void *dlogits, int64_t ldd, void *ws,
+                                  size_t ws_bytes, hipStream_t stream);
+size_t qlora_distill_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt, int32_t k);
+
+/*
  * qlora_pref_loss: loss of P pairs of answers (chosen, rejected) and its
  * gradient, from the log-probabilities of their tokens.
  *   logp, ref [T]: under the model and the frozen reference (NULL: none).
@@ -728,7 +776,9 @@ typedef enum {
   QLORA_KERNEL_DROPOUT = 11,    /* dropout from the counter               */
   QLORA_KERNEL_MUON = 12,       /* orthogonalised update                  */
   QLORA_KERNEL_EP_BWD = 13,     /* gradient of the elementwise end        */
-  QLORA_KERNEL_COUNT = 14
+  QLORA_KERNEL_TOP = 14,        /* top alternatives                       */
+  QLORA_KERNEL_DISTILL = 15,    /* loss against a teacher's alternatives  */
+  QLORA_KERNEL_COUNT = 16
 } qlora_kernel_kind;
 
 int qlora_timing_enable(int kind_mask);

@@ -157,3 +157,44 @@ def dropout_keep(rows, cols, p, seed, counter, only=None):
             n = min(8, cols - 8 * j)
             keep[i, 8 * j:8 * j + n] = np.array(half[:n]) >= p16
     return keep, p16
+
+
+def token_top(x, k, scale=1.0):
+    """The k largest logits of each row, ties to the lower index: (ids, log p).
+    A NaN is no word."""
+    x = np.asarray(x, np.float64)
+    order = np.argsort(np.where(np.isnan(x), np.inf, -x), axis=1, kind="stable")[:, :k]
+    m = x.max(1, keepdims=True)
+    m = np.where(np.isfinite(m), m, 0.0)
+    with np.errstate(divide="ignore"):
+        lp = scale * (x - m) - np.log(np.exp(scale * (x - m)).sum(1, keepdims=True))
+    lp = np.where(x == -np.inf, -np.inf, lp)
+    return order, np.take_along_axis(lp, order, 1)
+
+
+def distill(x, ids, teacher, weight, scale=1.0, normalize=True):
+    """(loss, kl [T], dx [T, V]) of rows x against the teacher's alternatives."""
+    x = np.asarray(x, np.float64)
+    T, V = x.shape
+    kl, dx = np.zeros(T), np.zeros((T, V))
+    for t in range(T):
+        if weight[t] == 0:
+            continue
+        on = (ids[t] >= 0) & (ids[t] < V) & (teacher[t] != -np.inf)
+        if not on.any():
+            continue
+        word, lq = ids[t][on], teacher[t][on].astype(np.float64)
+        if normalize:
+            lq = lq - (lq.max() + np.log(np.exp(lq - lq.max()).sum()))
+        q = np.exp(lq)
+        m = x[t].max()
+        if m == -np.inf:
+            kl[t] = np.inf
+            continue
+        u = scale * (x[t] - m)
+        lp = u - np.log(np.exp(u).sum())
+        kl[t] = np.where(q > 0, q * (lq - lp[word]), 0.0).sum()
+        dx[t] = q.sum() * np.exp(lp)
+        np.subtract.at(dx[t], word, q)
+        dx[t] *= scale * weight[t]
+    return (weight * kl)[weight != 0].sum(), kl, dx

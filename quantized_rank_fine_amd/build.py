@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libqlora.so")
 SOURCES = ["api.cpp", "tables.cpp", "quantize.hip", "skinny.hip", "gemm.hip", "smallm.hip",
            "merge.hip", "optim.hip", "loftq.hip", "loftq.cpp", "noalloc.hip", "logits.hip",
            "objective.hip", "dropout.hip", "muon.hip",
-           "epilogue.hip"]
+           "epilogue.hip", "alternatives.hip"]
 
 ARCH = "gfx950"
 COMMON = [

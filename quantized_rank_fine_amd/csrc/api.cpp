@@ -443,6 +443,35 @@ TermsPlan plan_terms(int64_t T, int64_t V) {
   return p;
 }
 
+// Workspace of the alternatives' calls: segments' sums, what else a cut row
+// leaves (its best words; its (m, z)), the partial sums of a loss.
+struct SegmentPlan {
+  size_t off_part = 0, off_other = 0, off_sum = 0, total = 0;
+};
+
+SegmentPlan plan_top(int64_t T, int64_t V, qlora_dtype dt, int32_t k) {
+  SegmentPlan p;
+  Layout L;
+  if (const int64_t n = forward_segments(T, V, dt == QLORA_BF16)) {
+    p.off_part = L.take(part_bytes(T, n));
+    p.off_other = L.take(size_t(T * n) * k * sizeof(uint64_t));
+  }
+  p.total = L.o;
+  return p;
+}
+
+SegmentPlan plan_distill(int64_t T, int64_t V) {
+  SegmentPlan p;
+  Layout L;
+  if (const int64_t n = T > 0 ? distill_segments(V) : 0) {
+    p.off_part = L.take(part_bytes(T, n));
+    p.off_other = L.take(size_t(T) * 2 * sizeof(float));
+  }
+  if (weighted_sum_blocks(T) > 1) p.off_sum = L.take(size_t(weighted_sum_blocks(T)) * sizeof(double));
+  p.total = L.o;
+  return p;
+}
+
 qlora_status policy_params(const qlora_policy *q, PolicyParams &p) {
   if (!q) return QLORA_ERR_NULL;
   const bool ok = (q->kind == QLORA_OBJ_NLL || q->kind == QLORA_OBJ_CLIP) &&
@@ -839,6 +868,70 @@ qlora_status qlora_token_logp_bwd(const void *logits, int64_t ld, int64_t T, int
   }));
 }
 
+size_t qlora_token_top_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt, int32_t k) {
+  if (check_logits(V, T, V, dt, 1.0f) != QLORA_OK || k < 1 || k > kMaxTop || k > V) return 0;
+  return plan_top(T, V, dt, k).total;
+}
+
+qlora_status qlora_token_top(const void *logits, int64_t ld, int64_t T, int64_t V,
+                             qlora_dtype dt, const int64_t *labels, float scale, int32_t k,
+                             int32_t *ids, float *top, float *logp, float *entropy, void *ws,
+                             size_t ws_bytes, hipStream_t stream) {
+  qlora_status st = check_logits(ld, T, V, dt, scale);
+  if (st != QLORA_OK) return st;
+  if (k < 1 || k > kMaxTop || k > V) return QLORA_ERR_SHAPE;
+  if (T == 0) return QLORA_OK;
+  if (!logits || !ids || !top || (logp && !labels)) return QLORA_ERR_NULL;
+  if (!aligned_el(logits, dt) || !aligned_to(labels, 8) || !aligned_to(ids, 4) ||
+      !aligned_to(top, 4) || !aligned_to(logp, 4) || !aligned_to(entropy, 4))
+    return QLORA_ERR_ALIGN;
+  const SegmentPlan p = plan_top(T, V, dt, k);
+  if (p.total && !ws) return QLORA_ERR_NULL;
+  if (!aligned_to(ws, 8)) return QLORA_ERR_ALIGN;
+  if (ws_bytes < p.total) return QLORA_ERR_WORKSPACE;
+  const LogitRows a{logits, ld, T, V, dt == QLORA_BF16, labels, scale};
+  return dev(timed(QLORA_KERNEL_TOP, stream, [&] {
+    return launch_top(a, TopRows{k, ids, top, logp, entropy}, at<float>(ws, p.off_part),
+                      at<uint64_t>(ws, p.off_other), stream);
+  }));
+}
+
+size_t qlora_distill_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt, int32_t k) {
+  if (check_logits(V, T, V, dt, 1.0f) != QLORA_OK || k < 1 || k > kMaxTop) return 0;
+  return plan_distill(T, V).total;
+}
+
+qlora_status qlora_distill_logits(const void *logits, int64_t ld, int64_t T, int64_t V,
+                                  qlora_dtype dt, float scale, const float *weight, int32_t k,
+                                  const int32_t *ids, const float *teacher, int32_t normalize,
+                                  float *loss, float *kl, void *dlogits, int64_t ldd, void *ws,
+                                  size_t ws_bytes, hipStream_t stream) {
+  qlora_status st = check_logits(ld, T, V, dt, scale);
+  if (st != QLORA_OK) return st;
+  if (ldd < V || ldd > kMaxLd || k < 1 || k > kMaxTop) return QLORA_ERR_SHAPE;
+  if (!loss || (T > 0 && (!logits || !ids || !teacher || !kl || !dlogits))) return QLORA_ERR_NULL;
+  if (!aligned_el(logits, dt) || !aligned_el(dlogits, dt) || !aligned_to(weight, 4) ||
+      !aligned_to(ids, 4) || !aligned_to(teacher, 4) || !aligned_to(loss, 4) ||
+      !aligned_to(kl, 4))
+    return QLORA_ERR_ALIGN;
+  const SegmentPlan p = plan_distill(T, V);
+  if (p.total && !ws) return QLORA_ERR_NULL;
+  if (!aligned_to(ws, 8)) return QLORA_ERR_ALIGN;
+  if (ws_bytes < p.total) return QLORA_ERR_WORKSPACE;
+  if (T > 0) {
+    const LogitRows a{logits, ld, T, V, dt == QLORA_BF16, nullptr, scale};
+    const DistillRows d{weight, k, ids, teacher, normalize != 0};
+    const hipError_t e = timed(QLORA_KERNEL_DISTILL, stream, [&] {
+      return launch_distill(a, d, kl, dlogits, ldd, at<float>(ws, p.off_part),
+                            at<float>(ws, p.off_other), stream);
+    });
+    if (e != hipSuccess) return QLORA_ERR_DEVICE;
+  }
+  return dev(timed(QLORA_KERNEL_DISTILL, stream, [&] {
+    return launch_weighted_sum(kl, weight, T, loss, at<double>(ws, p.off_sum), stream);
+  }));
+}
+
 size_t qlora_pref_workspace_bytes(int64_t P, int64_t T) {
   if (P < 1 || P > kMaxPairs || T < 0 || T > kMaxVec) return 0;
   return size_t(pref_partials(P, T)) * sizeof(double);
@@ -1004,7 +1097,8 @@ void qlora_timing_reset(void) {
 const char *qlora_kernel_name(int kind) {
   static const char *names[QLORA_KERNEL_COUNT] = {
       "quantize", "xa_rowdot", "fwd_gemm", "dy_pass", "dx_gemm", "da_pass", "reduce", "fwd_smallm",
-      "token_logp", "pref_loss", "policy_loss", "dropout", "muon", "ep_bwd"};
+      "token_logp", "pref_loss", "policy_loss", "dropout", "muon", "ep_bwd", "token_top",
+      "distill"};
   if (kind < 0 || kind >= QLORA_KERNEL_COUNT) return "unknown";
   return names[kind];
 }

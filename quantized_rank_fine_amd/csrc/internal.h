@@ -349,6 +349,37 @@ struct PolicySplit {
 hipError_t launch_policy_logits(const LogitRows &a, const PolicyTokens &t,
                                 const PolicyParams &p, float *terms, float *logp, void *dx,
                                 int64_t ldd, const PolicySplit &o, hipStream_t s);
+// The k best words of each row (labels may be null: every row is scored), and
+// the label's log p and the entropy where wanted.  Scratch of rows that are cut
+// (forward_segments of them): part as above, best k 64-bit keys a segment.
+constexpr int kMaxTop = QLORA_MAX_TOP;
+struct TopRows {
+  int k;
+  int32_t *ids;
+  float *top, *logp, *entropy;
+};
+hipError_t launch_top(const LogitRows &a, const TopRows &o, float *part, uint64_t *best,
+                      hipStream_t s);
+
+// The loss against k alternatives a row and the logits' gradient (a.labels is
+// not used).  Scratch of rows that are cut (distill_segments of them): part,
+// and (m, z) by row.
+struct DistillRows {
+  const float *weight;
+  int k;
+  const int32_t *ids;
+  const float *logt;
+  int normalize;
+};
+int64_t distill_segments(int64_t V);
+hipError_t launch_distill(const LogitRows &a, const DistillRows &d, float *kl, void *dx,
+                          int64_t ldd, float *part, float *stats, hipStream_t s);
+// out[0] = sum weight kl over the tokens with weight, fp64.  partial:
+// weighted_sum_blocks(T) doubles, unused (may be null) when that is 1.
+int64_t weighted_sum_blocks(int64_t T);
+hipError_t launch_weighted_sum(const float *kl, const float *weight, int64_t T, float *out,
+                               double *partial, hipStream_t s);
+
 // out[4] = the columns' sums of terms [n x 4], fp64, in an order that n fixes.
 // partial: terms_blocks(n) * 4 doubles, unused (may be null) when that is 1.
 int64_t terms_blocks(int64_t n);

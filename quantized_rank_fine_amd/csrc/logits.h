@@ -366,13 +366,14 @@ __device__ __forceinline__ void zero_row(char *out, int32_t V) {
 
 constexpr int kPartThreads = 256, kPartNG = 4;
 
-template <bool BF16, bool ENT>
+// LABELS: rows that are not scored are left out, else only those without weight.
+template <bool BF16, bool ENT, bool LABELS = true>
 __global__ __launch_bounds__(kPartThreads) void part_kernel(LogitRows a, const float *weight,
                                                             Stat *part) {
   __shared__ Stat red[kPartThreads / 64];
   const int64_t t = row_index();
   if (t >= a.T) return;
-  const int64_t y = a.labels[t];
+  const int64_t y = LABELS ? a.labels[t] : 0;
   if (y < 0 || y >= a.V || (weight && weight[t] == 0.0f)) return;   // nor will it be joined
   const char *row = row_at<BF16>(a.x, t * a.ld);
   const float c = a.scale * kLog2e;

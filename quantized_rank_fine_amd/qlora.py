@@ -17,6 +17,7 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 
 F32, BF16 = 0, 1
 LAB_GROUP = 16                        # QLORA_LAB_GROUP: 16-entry scale groups
+MAX_TOP = 64                          # QLORA_MAX_TOP
 NOALLOC_SCRATCH_BYTES = 32 << 20      # QLORA_NOALLOC_SCRATCH_BYTES
 CB_NF4, CB_UNIFORM4, CB_INT4, CB_INT3, CB_TERNARY = 0, 1, 2, 3, 4   # qlora_codebook
 STATUS = {0: "ok", 1: "null pointer", 2: "invalid shape", 3: "pointer not 16-byte aligned",
@@ -24,7 +25,7 @@ STATUS = {0: "ok", 1: "null pointer", 2: "invalid shape", 3: "pointer not 16-byt
           7: "invalid value"}
 KERNELS = ("quantize", "xa_rowdot", "fwd_gemm", "dy_pass", "dx_gemm", "da_pass", "reduce",
            "fwd_smallm", "token_logp", "pref_loss", "policy_loss", "dropout", "muon",
-           "ep_bwd")
+           "ep_bwd", "token_top", "distill")
 PREF_SIGMOID, PREF_SQUARED, PREF_HINGE = 0, 1, 2                     # qlora_pref_kind
 EP_NONE, EP_RELU, EP_GELU, EP_GELU_TANH, EP_SILU = 0, 1, 2, 3, 4      # qlora_ep_act
 OBJ_NLL, OBJ_CLIP = 0, 1                                             # qlora_objective
@@ -154,9 +155,15 @@ def lib():
     L.qlora_muon_step.argtypes = [i32, pmat, ctypes.POINTER(qlora_muon_hparams), vp, sz, vp]
     L.qlora_muon_workspace_bytes.argtypes = [i32, pmat]
     L.qlora_muon_workspace_bytes.restype = sz
+    L.qlora_token_top.argtypes = [vp, i64, i64, i64, ci, vp, f32, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_distill_logits.argtypes = [vp, i64, i64, i64, ci, f32, vp, i32, vp, vp, i32, vp, vp,
+                                       vp, i64, vp, sz, vp]
+    for f in (L.qlora_token_top_workspace_bytes, L.qlora_distill_workspace_bytes):
+        f.argtypes = [i64, i64, ci, i32]
+        f.restype = sz
     for f in (L.qlora_token_logp_fwd, L.qlora_token_logp_bwd, L.qlora_pref_loss,
               L.qlora_policy_loss, L.qlora_policy_logits, L.qlora_dropout, L.qlora_muon_step,
-              L.qlora_linear_fwd_ep, L.qlora_ep_bwd):
+              L.qlora_linear_fwd_ep, L.qlora_ep_bwd, L.qlora_token_top, L.qlora_distill_logits):
         f.restype = ctypes.c_int
     L.qlora_token_logp_workspace_bytes.argtypes = [i64, i64, ci]
     L.qlora_policy_logits_workspace_bytes.argtypes = [i64, i64, ci]
@@ -501,6 +508,36 @@ def qlora_token_logp_bwd(logits, ld, T, V, dt, labels, scale, stats, entropy, g,
                                       _ptr(labels), float(scale), _ptr(stats), _ptr(entropy),
                                       _ptr(g), _ptr(g_entropy), _ptr(dlogits), int(ldd),
                                       _stream(stream)), "qlora_token_logp_bwd")
+
+
+def qlora_token_top_workspace_bytes(T, V, dt, k):
+    return int(lib().qlora_token_top_workspace_bytes(int(T), int(V), int(dt), int(k)))
+
+
+def qlora_token_top(logits, ld, T, V, dt, labels, scale, k, ids, top, logp, entropy, ws, ws_bytes,
+                    stream=None):
+    """The k most likely words of each row (ids int32, top their log p), the
+    labels' log p and the entropy; labels, logp and entropy may be None."""
+    _check(lib().qlora_token_top(_ptr(logits), int(ld), int(T), int(V), int(dt), _ptr(labels),
+                                 float(scale), int(k), _ptr(ids), _ptr(top), _ptr(logp),
+                                 _ptr(entropy), _ptr(ws), int(ws_bytes), _stream(stream)),
+           "qlora_token_top")
+
+
+def qlora_distill_workspace_bytes(T, V, dt, k):
+    return int(lib().qlora_distill_workspace_bytes(int(T), int(V), int(dt), int(k)))
+
+
+def qlora_distill_logits(logits, ld, T, V, dt, scale, weight, k, ids, teacher, normalize, loss, kl,
+                         dlogits, ldd, ws, ws_bytes, stream=None):
+    """Divergence from a teacher's k alternatives a row (ids int32, teacher their
+    log p, as qlora_token_top gives them) and the logits' gradient (dlogits may
+    be logits); weight may be None."""
+    _check(lib().qlora_distill_logits(_ptr(logits), int(ld), int(T), int(V), int(dt),
+                                      float(scale), _ptr(weight), int(k), _ptr(ids),
+                                      _ptr(teacher), int(bool(normalize)), _ptr(loss), _ptr(kl),
+                                      _ptr(dlogits), int(ldd), _ptr(ws), int(ws_bytes),
+                                      _stream(stream)), "qlora_distill_logits")
 
 
 def qlora_pref_workspace_bytes(P, T):
