@@ -58,9 +58,22 @@ __device__ __forceinline__ uint32_t kth_key(uint32_t a, uint32_t b, int k) {
 }
 
 struct TopList {
-  uint64_t e[kList];
+  alignas(16) uint64_t e[kList];
   int n;
 };
+
+// How many of the list's n entries are above e.
+__device__ __forceinline__ int place_of(const TopList &list, int n, uint64_t e) {
+  int r = 0;
+  for (int j = 0; j < n; j += 8) {            // (kList is a multiple of 8)
+    uint64_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = list.e[j + i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r += j + i < n && v[i] > e;
+  }
+  return r;
+}
 
 // Number of this workgroup's words that f counts, in every lane.
 template <int threads, class F>
@@ -77,20 +90,12 @@ __device__ __forceinline__ int counted(F &&f, int *sum) {
   return n;
 }
 
-// Adds a held chunk's best k words (words [from, end) of the groups, and the
-// ones with the first) to the list behind its first `have` entries; end - from
-// is at most the words that are held.  Returns the new length (every lane).
+// The largest word of each held group, and of the lane.
 template <bool BF16, int threads, int NG>
-__device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF16> &cut,
-                                        int32_t from, int32_t end, int k, int have, TopList &list,
-                                        uint32_t *keys, int *sum) {
+__device__ __forceinline__ float group_maxima(const Held<BF16, threads, NG> &h,
+                                              float (&gm)[8 * NG / kGroup<BF16>]) {
   constexpr int W = kGroup<BF16>, G = 8 * NG / W;
-  constexpr int share = threads > 128 ? threads / 128 : 1;   // lanes to a key
-  h.keep();
-  float gm[G], top = -INFINITY;
-  const int32_t one = from == 0 ? cut.one(int32_t(threadIdx.x)) : cut.V;
-  const bool has_one = one < cut.V;
-  if (has_one) top = fmaxf(top, h.one);
+  float top = h.one;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     float e[W];
@@ -100,6 +105,22 @@ __device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF
     for (int i = 1; i < W; ++i) gm[g] = fmaxf(gm[g], e[i]);
     top = fmaxf(top, gm[g]);
   }
+  return fmaxf(top, -INFINITY);              // (no word but NaN)
+}
+
+// Adds a held chunk's best k words (words [from, end) of the groups, and the
+// ones with the first) to the list behind its first `have` entries; end - from
+// is at most the words that are held, gm and top are theirs (group_maxima).
+// Returns the new length (every lane).
+template <bool BF16, int threads, int NG>
+__device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF16> &cut,
+                                        int32_t from, int32_t end,
+                                        const float (&gm)[8 * NG / kGroup<BF16>], float top, int k,
+                                        int have, TopList &list, uint32_t *keys, int *sum) {
+  constexpr int W = kGroup<BF16>, G = 8 * NG / W;
+  constexpr int share = threads > 128 ? threads / 128 : 1;   // lanes to a key
+  const int32_t one = from == 0 ? cut.one(int32_t(threadIdx.x)) : cut.V;
+  const bool has_one = one < cut.V;
 #pragma unroll
   for (int d = 1; d < share; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
   if (threadIdx.x == 0) list.n = have;
@@ -127,17 +148,22 @@ __device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF
       if (at < kList) list.e[at] = entry_of(x, uint32_t(v));
     }
   };
-  // f(value, word) of every held word
+  // f(value, word) of the held words of groups that reach the bound.  The
+  // registers are laundered, or what is worked out of them would be kept from
+  // one use for the next (four times the registers).
   auto words = [&](auto &&f) {
+    h.keep();
+    int32_t at = from + h.first(0);
+    asm volatile("" : "+v"(at));
     if (has_one) f(h.one, one);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int32_t at = from + h.first(g);
+    for (int g = 0; g < G; ++g, at += threads * W) {
       if (at >= end || !(gm[g] >= least)) continue;
       float e[W];
       unpack<BF16>(h.q[g], e);
 #pragma unroll
       for (int i = 0; i < W; ++i) f(e[i], cut.head + at + i);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   words(offer);
@@ -148,6 +174,7 @@ __device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF
   __syncthreads();
   if (threadIdx.x == 0) list.n = have;
   uint64_t kth = 0;
+#pragma unroll 1
   for (int bit = 63; bit >= 0; --bit) {
     const uint64_t c = kth | uint64_t(1) << bit;
     const int m = counted<threads>(
@@ -179,9 +206,7 @@ __device__ __forceinline__ void order(TopList &list, int n, int k) {
     place[q] = k;
     if (i >= n) continue;
     own[q] = list.e[i];
-    int r = 0;
-    for (int j = 0; j < n; ++j) r += list.e[j] > own[q];
-    place[q] = r;
+    place[q] = place_of(list, n, own[q]);
   }
   __syncthreads();
 #pragma unroll
@@ -190,23 +215,29 @@ __device__ __forceinline__ void order(TopList &list, int n, int k) {
   __syncthreads();
 }
 
-// A row's alternatives from its list's best n.
+// Alternative j of row t.
+__device__ __forceinline__ void write_entry(const TopRows &o, int64_t t, int j, bool some,
+                                            uint64_t e, const RowResult &r, float scale) {
+  o.ids[t * o.k + j] = some ? int32_t(word_of(e)) : -1;
+  const float x = value_of(uint32_t(e >> 32));
+  // a row of nothing but -inf has m = -inf
+  o.top[t * o.k + j] =
+      r.z != r.z ? r.z : !(x > -INFINITY) ? -INFINITY : scale * (x - r.m) - r.z;
+}
+
+__device__ __forceinline__ void write_row(const TopRows &o, int64_t t, const RowResult &r) {
+  if (o.logp) o.logp[t] = r.logp;
+  if (o.entropy) o.entropy[t] = r.ent;
+}
+
+// A row's alternatives from its list's best n, which are in order (fewer than
+// k: a row of NaN).
 template <int threads>
 __device__ __forceinline__ void write_top(const TopRows &o, int64_t t, const TopList &list, int n,
                                           const RowResult &r, float scale) {
-  for (int j = threadIdx.x; j < o.k; j += threads) {
-    const bool some = j < n;                               // (fewer: a row of NaN)
-    const uint64_t e = some ? list.e[j] : 0;
-    o.ids[t * o.k + j] = some ? int32_t(word_of(e)) : -1;
-    const float x = value_of(uint32_t(e >> 32));
-    // a row of nothing but -inf has m = -inf
-    o.top[t * o.k + j] = r.z != r.z ? r.z : !(x > -INFINITY) ? -INFINITY
-                                            : scale * (x - r.m) - r.z;
-  }
-  if (threadIdx.x == 0) {
-    if (o.logp) o.logp[t] = r.logp;
-    if (o.entropy) o.entropy[t] = r.ent;
-  }
+  for (int j = threadIdx.x; j < o.k; j += threads)
+    write_entry(o, t, j, j < n, j < n ? list.e[j] : 0, r, scale);
+  if (threadIdx.x == 0) write_row(o, t, r);
 }
 
 template <int threads>
@@ -228,7 +259,8 @@ __device__ __forceinline__ bool row_label(const LogitRows &a, int64_t t, int32_t
   return v >= 0 && v < a.V;
 }
 
-template <bool BF16, bool ENT, int threads, int NG>
+// ONE: the row is held whole (a loop over chunks costs its invariants' registers).
+template <bool BF16, bool ENT, bool ONE, int threads, int NG>
 __global__ __launch_bounds__(threads) void top_kernel(LogitRows a, TopRows o) {
   __shared__ Stat red[threads / 64];
   __shared__ TopList list;
@@ -244,20 +276,48 @@ __global__ __launch_bounds__(threads) void top_kernel(LogitRows a, TopRows o) {
   const Cut<BF16> k(row, V);
   Held<BF16, threads, NG> h;
   Stat s = {-INFINITY, 0.0f, 0.0f};
-  const float xy = load1<BF16>(row, uint32_t(y));
   int n = 0;
-  int32_t from = 0, end = first_chunk<Held<BF16, threads, NG>::words>(k.whole);
+  int32_t from = 0, end = ONE ? k.whole : first_chunk<Held<BF16, threads, NG>::words>(k.whole);
+  h.load(row, k, from, end);
+  const float xy = load1<BF16>(row, uint32_t(y));
   for (;;) {
-    h.load(row, k, from, end);
-    add_chunk<ENT>(s, h, c);
-    n = add_best(h, k, from, end, o.k, n, list, keys, sum);
+    float gm[8 * NG / kGroup<BF16>];
+    const float top = group_maxima(h, gm);
+    add_sums<ENT>(s, h, c, fmaxf(s.m, top));
+    if (ONE) {
+      // (the barriers of add_best come before the sums are read)
+      s = joined(s, c);
+      if (threads > 64 && threadIdx.x % 64 == 0) red[threadIdx.x / 64] = s;
+    }
+    n = add_best(h, k, from, end, gm, top, o.k, n, list, keys, sum);
+    if (ONE) break;
     order<threads>(list, n, o.k);
     n = n < o.k ? n : o.k;
     if (end >= k.whole) break;
     from = end;
     end += h.words;
+    h.load(row, k, from, end);
   }
-  s = joined_block<threads>(s, c, red);
+  if (ONE) {
+    // A short list, as it nearly always is, is one wavefront's: an entry a lane.
+    const int lane = threadIdx.x % 64;
+    const bool lone = n <= 64;
+    if (lone && threadIdx.x >= 64) return;
+    if (threads > 64)
+      s = joined(lane < threads / 64 ? red[lane] : Stat{-INFINITY, 0.0f, 0.0f}, c);
+    if (lone) {
+      const RowResult r = finished<BF16, 64>(s, row, V, xy, a.scale, nullptr);
+      const uint64_t e = lane < n ? list.e[lane] : 0;
+      const int j = lane < n ? place_of(list, n, e) : lane;
+      if (j < o.k) write_entry(o, t, j, lane < n, e, r, a.scale);
+      if (lane == 0) write_row(o, t, r);
+      return;
+    }
+    order<threads>(list, n, o.k);
+    n = n < o.k ? n : o.k;
+  } else {
+    s = joined_block<threads>(s, c, red);
+  }
   const RowResult r = finished<BF16, threads>(s, row, V, xy, a.scale, red);
   write_top<threads>(o, t, list, n, r, a.scale);
 }
@@ -284,8 +344,10 @@ __global__ __launch_bounds__(kPartThreads) void top_part_kernel(LogitRows a, int
   int n = 0;
   if (from == 0 || from < cut.whole) {
     h.load(row, cut, from, end);
-    add_chunk<ENT>(s, h, c);
-    n = add_best(h, cut, from, end, k, 0, list, keys, sum);
+    float gm[8 * kPartNG / kGroup<BF16>];
+    const float top = group_maxima(h, gm);
+    add_sums<ENT>(s, h, c, top);
+    n = add_best(h, cut, from, end, gm, top, k, 0, list, keys, sum);
     order<kPartThreads>(list, n, k);
   }
   const int64_t at = t * gridDim.x + blockIdx.x;
@@ -326,7 +388,7 @@ __global__ __launch_bounds__(kJoinThreads) void top_join_kernel(LogitRows a, Top
   write_top<kJoinThreads>(o, t, list, n, r, a.scale);
 }
 
-// Lanes and groups as in logp_fwd.
+// Lanes and groups as in logp_fwd, whose bits the log p and the entropy so have.
 template <bool BF16, bool ENT>
 void top(const LogitRows &a, const TopRows &o, float *part, uint64_t *best, hipStream_t s) {
   if (const int64_t n = forward_segments(a.T, a.V, BF16)) {
@@ -337,13 +399,15 @@ void top(const LogitRows &a, const TopRows &o, float *part, uint64_t *best, hipS
                        best, int(n));
     return;
   }
-#define ROWS(threads, NG)                                                                   \
-  hipLaunchKernelGGL((top_kernel<BF16, ENT, threads, NG>), row_grid(a.T), dim3(threads), 0, s, \
-                     a, o)
-  if (a.V <= 4096) ROWS(64, 4);
-  else if (a.V <= 8192) ROWS(128, 8);
-  else if (a.V <= 16384) ROWS(256, 8);
-  else ROWS(512, 8);
+#define ROWS(ONE, threads, NG)                                                                  \
+  hipLaunchKernelGGL((top_kernel<BF16, ENT, ONE, threads, NG>), row_grid(a.T), dim3(threads), 0, \
+                     s, a, o)
+  if (a.V <= 2048) ROWS(true, 64, 4);
+  else if (a.V <= 4096) ROWS(false, 64, 4);
+  else if (a.V <= 8192) ROWS(true, 128, 8);
+  else if (a.V <= 16384) ROWS(true, 256, 8);
+  else if (a.V <= 32768) ROWS(true, 512, 8);
+  else ROWS(false, 512, 8);
 #undef ROWS
 }
 

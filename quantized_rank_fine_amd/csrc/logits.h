@@ -195,18 +195,10 @@ __device__ __forceinline__ Stat raised(const Stat &a, float top, float c) {
   return {top, f * a.t, f * __builtin_fmaf(d, a.t, a.w)};
 }
 
-// A lane's share of a chunk into its running sums.
+// A lane's share of a chunk into its running sums; top: the largest word of both.
 template <bool ENT, bool BF16, int threads, int NG>
-__device__ __forceinline__ void add_chunk(Stat &a, Held<BF16, threads, NG> &h, float c) {
+__device__ __forceinline__ void add_sums(Stat &a, Held<BF16, threads, NG> &h, float c, float top) {
   constexpr int W = kGroup<BF16>, G = 8 * NG / W;
-  float top = fmaxf(a.m, h.one);
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    float e[W];
-    unpack<BF16>(h.q[g], e);
-#pragma unroll
-    for (int i = 0; i < W; ++i) top = fmaxf(top, e[i]);
-  }
   a = raised(a, top, c);
   h.keep();
   const float M = reference(top, c);
@@ -218,6 +210,20 @@ __device__ __forceinline__ void add_chunk(Stat &a, Held<BF16, threads, NG> &h, f
 #pragma unroll
     for (int i = 0; i < W; ++i) add<ENT>(a, e[i], c, M);
   }
+}
+
+template <bool ENT, bool BF16, int threads, int NG>
+__device__ __forceinline__ void add_chunk(Stat &a, Held<BF16, threads, NG> &h, float c) {
+  constexpr int W = kGroup<BF16>, G = 8 * NG / W;
+  float top = fmaxf(a.m, h.one);
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    float e[W];
+    unpack<BF16>(h.q[g], e);
+#pragma unroll
+    for (int i = 0; i < W; ++i) top = fmaxf(top, e[i]);
+  }
+  add_sums<ENT>(a, h, c, top);
 }
 
 // The sums of 64 lanes as one, in every lane.
