@@ -261,7 +261,7 @@ __device__ __forceinline__ bool row_label(const LogitRows &a, int64_t t, int32_t
 
 // ONE: the row is held whole (a loop over chunks costs its invariants' registers).
 template <bool BF16, bool ENT, bool ONE, int threads, int NG>
-__global__ __launch_bounds__(threads) void top_kernel(LogitRows a, TopRows o) {
+__global__ __launch_bounds__(threads, ONE && BF16 ? 8 : 1) void top_kernel(LogitRows a, TopRows o) {
   __shared__ Stat red[threads / 64];
   __shared__ TopList list;
   __shared__ uint32_t keys[threads < 128 ? threads : 128];

@@ -19,21 +19,22 @@
 // Launches: Gram partials over slabs of the long side (and the momentum); their
 // sum; the k x k iterations, in one workgroup's LDS for k <= 64, else by
 // 16 x 16 tiles, one launch a product; the last product and the update.
+#include <type_traits>
+
 #include "device.h"
 #include "qlora.h"
 
 namespace qlora {
 namespace {
 
-// A matrix in the kernels: n long, k short; quads: 16-byte loads of grad and m.
-// span: long rows to a Gram workgroup, `splits` of them; apply: long rows to
-// an update workgroup; area: where its fp64 scratch begins.
+// A matrix in the kernels: n long, k short; quads: 16-byte accesses.  span: long rows to a Gram workgroup,
+// `splits` of them; area: where its fp64 scratch begins.
 struct MuonMat {
   const float *grad;
   float *m, *theta;
   uint16_t *theta16;
   float *update;
-  int64_t n, span, apply, area;
+  int64_t n, span, area;
   int32_t k, wide, quads, splits;
   float scale;
 };
@@ -46,141 +47,116 @@ __device__ __forceinline__ f64x4_t mfma64(double a, double b, f64x4_t d) {
   return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, d, 0, 0, 0);
 }
 
-// LDS row pitch (floats) of a slab [long][short] of kp short columns: 17 past a
-// multiple of 64 (49 for 32 columns), so that both a fragment (4 rows of 16, or
-// 16 rows of 4) and a column written by consecutive lanes spread over the banks.
-__host__ __device__ constexpr int slab_pitch(int kp) {
-  return kp == 32 ? 49 : (kp + 46) / 64 * 64 + 17;
-}
-
-// Long rows staged at a time: about 4096 values.
-__host__ __device__ constexpr int slab_rows(int kp) {
-  return kp <= 16 ? 256 : kp <= 32 ? 128 : kp <= 64 ? 64 : kp <= 128 ? 32 : 16;
-}
-
 constexpr int kPad = 16;
 __host__ __device__ inline int padded(int k) { return (k + kPad - 1) / kPad * kPad; }
 
 // One value's momentum and the update's direction.
-template <bool kStore>
+template <bool kStep>
 __device__ __forceinline__ float direction(const MuonParams &p, bool has_m, float g, float &m) {
   if (!has_m) return g;
-  if (kStore) m = p.mu * m + g;
+  if (kStep) m = p.mu * m + g;
   return p.nesterov ? g + p.mu * m : m;
 }
 
-// `rows` long rows from `at` of a matrix into us [rows][pitch] as u; kStore: the
-// momentum is advanced (else it is read as it is).  Rows past n become 0; the
-// columns past k are not touched.  A thread's loads go out before the first
-// value is used.
-template <bool kStore, int threads, int kMost>
-__device__ __forceinline__ void stage(const MuonMat &a, const MuonParams &p, int64_t at, int rows,
-                                      int pitch, float *us) {
-  const int t = threadIdx.x, k = a.k;
-  const int64_t left = a.n - at;
-  const int live = int(left < rows ? left : rows);
-  const bool has_m = a.m != nullptr;
-  const bool read_g = kStore || !has_m || p.nesterov;
-  const uint32_t inv = k > 1 ? 0xffffffffu / uint32_t(k) + 1u : 0u;   // e / k for e < 2^16
-  if (a.quads) {
-    constexpr int U = (kMost / 4 + threads - 1) / threads;
-    const int per = a.wide ? rows / 4 : k / 4;         // quads of a memory row
-    const uint32_t pinv = per > 1 ? 0xffffffffu / uint32_t(per) + 1u : 0u;
-    const int quads = a.wide ? k * per : rows * per;
-    f32x4_t g[U], m[U];
-    int64_t off[U];
-    int row[U], col[U];
+// Where a lane's values lie: a place that is the same for the wavefront, and the
+// lane's distance from it (a scalar and one 32-bit register an address).  The
+// common place itself always lies in the array.
+struct Place {
+  int64_t base;
+  uint32_t lane;
+};
+
+// The first `live` of N values at a place, the rest 0.  Q: live is 0 or N and
+// the values are aligned to them (one load).  No load is conditional: what is
+// not live reads the common place and is dropped.
+template <int N>
+struct Run {
+  float v[N];
+};
+template <bool Q, int N>
+__device__ __forceinline__ Run<N> load_run(const float *p, Place at, int live) {
+  Run<N> r;
+  p += at.base;
+  if (Q) {
+    __builtin_memcpy(&r, __builtin_assume_aligned(p + (live ? at.lane : 0u), 4 * N), 4 * N);
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int e = t + i * threads;
-      const int hi = per > 1 ? int(__umulhi(uint32_t(e), pinv)) : e, lo = e - hi * per;
-      row[i] = a.wide ? 4 * lo : hi;
-      col[i] = a.wide ? hi : 4 * lo;
-      off[i] = e < quads && row[i] < live
-                   ? (a.wide ? int64_t(col[i]) * a.n + at + row[i] : (at + row[i]) * k + col[i])
-                   : -1;
-      g[i] = m[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      if (off[i] >= 0) {
-        if (read_g) g[i] = *reinterpret_cast<const f32x4_t *>(a.grad + off[i]);
-        if (has_m) m[i] = *reinterpret_cast<const f32x4_t *>(a.m + off[i]);
-      }
-    }
+    for (int i = 0; i < N; ++i) r.v[i] = live ? r.v[i] : 0.0f;
+  } else {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (t + i * threads >= quads) break;
-      float u[4];
+    for (int i = 0; i < N; ++i) r.v[i] = p[i < live ? at.lane + i : 0u];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float mm = m[i][e];
-        u[e] = direction<kStore>(p, has_m, g[i][e], mm);
-        m[i][e] = mm;
-      }
-      if (kStore && has_m && off[i] >= 0) *reinterpret_cast<f32x4_t *>(a.m + off[i]) = m[i];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        us[(row[i] + (a.wide ? e : 0)) * pitch + col[i] + (a.wide ? 0 : e)] = u[e];
-    }
-    return;
+    for (int i = 0; i < N; ++i) r.v[i] = i < live ? r.v[i] : 0.0f;
   }
-  // any alignment: one value a lane at a time
-  const int all = rows * k;
-  const uint32_t rinv = 0xffffffffu / uint32_t(rows) + 1u;
-  for (int base = 0; base < all; base += 8 * threads) {
-    float g[8], m[8];
-    int64_t off[8];
-    int slot[8];
+  return r;
+}
+template <bool Q, int N>
+__device__ __forceinline__ void store_run(float *p, Place at, int live, const Run<N> &r) {
+  p += at.base;
+  if (Q) {
+    if (live) __builtin_memcpy(__builtin_assume_aligned(p + at.lane, 4 * N), &r, 4 * N);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = base + i * threads + t;
-      int r, c;
-      if (a.wide) {
-        c = int(__umulhi(uint32_t(e), rinv));
-        r = e - c * rows;
-      } else {
-        r = k > 1 ? int(__umulhi(uint32_t(e), inv)) : e;
-        c = e - r * k;
-      }
-      slot[i] = e < all ? r * pitch + c : -1;
-      off[i] = e < all && r < live ? (a.wide ? int64_t(c) * a.n + at + r : (at + r) * k + c) : -1;
-      g[i] = m[i] = 0.0f;
-      if (off[i] >= 0) {
-        if (read_g) g[i] = a.grad[off[i]];
-        if (has_m) m[i] = a.m[off[i]];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (slot[i] < 0) continue;
-      const float u = direction<kStore>(p, has_m, g[i], m[i]);
-      if (kStore && has_m && off[i] >= 0) a.m[off[i]] = m[i];
-      us[slot[i]] = u;
-    }
+    for (int i = 0; i < N; ++i)
+      if (i < live) p[at.lane + i] = r.v[i];
   }
 }
 
-// Slabs of kp short columns hold at most this many values (quads of them, for
-// k a multiple of 4, at most rows kp / 4).
-constexpr int kSlabMost = 4096;
+__device__ __forceinline__ int clamped(int64_t left, int most) {
+  return left < most ? (left < 0 ? 0 : int(left)) : most;
+}
 
-template <int threads>
-__device__ __forceinline__ void clear(float *us, int n) {
-  for (int i = threadIdx.x; i < n; i += threads) us[i] = 0.0f;
+// f(integral_constant<bool>), f(integral_constant<int>) for uniform values.
+template <class F>
+__device__ __forceinline__ void with_bool(bool v, F &&f) {
+  if (v) f(std::true_type{});
+  else f(std::false_type{});
+}
+template <class F>
+__device__ __forceinline__ void with_tiles(int t, F &&f) {
+  switch (t) {
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    case 3: f(std::integral_constant<int, 3>{}); break;
+    default: f(std::integral_constant<int, 4>{}); break;
+  }
 }
 
 // ------------------------------------------------------------ Gram partials
 //
-// One slab range of a matrix to a workgroup: u goes to LDS in fp32 (advancing
-// the momentum on the way) and is multiplied from there.  NB 64-column blocks:
-// NB = 1: four wavefronts share the rows and hold all tiles of the upper
-// triangle; else a wavefront to each pair of blocks (of the upper triangle),
-// all rows each.  Partial sums: [tile][register][lane], fp64.
-template <int NB>
-struct Pairs {
-  static constexpr int count = NB * (NB + 1) / 2;
-  static constexpr int threads = NB == 1 ? 256 : count * 64;
+// A wavefront sums u^T u of its long rows for one pair of 64-column blocks, from
+// registers: no LDS, no barrier until the end.  The 16 columns of a tile and
+// the four rows of a product may be any, so they are chosen for the loads:
+//   tall (a long row is k consecutive values): a block of w columns has T = 1, 2
+//     or 4 tiles; lane (g, c) loads T consecutive columns T c .. of row 4 s + g,
+//     one for each tile: tile t holds columns T c + t.
+//   wide (a short row is n consecutive values): lane (g, c) loads four
+//     consecutive long rows 4 g .. of column 16 t + c, one for each of four
+//     products.
+// The momentum is advanced on the way where one wavefront sees every value
+// (k <= 64), else by a pass of its own before.  The four wavefronts of a
+// workgroup share a slab's rows and leave the sum of theirs, [pair][tile][
+// register][lane] in fp64, tile = 4 ti + tj.
+struct Block {
+  int first, tiles, width;                     // columns first .. first + width - 1
 };
+__host__ __device__ __forceinline__ Block block_of(int k, int b, int wide) {
+  const int w = k - 64 * b < 64 ? k - 64 * b : 64;
+  const int t = (w + 15) / 16;
+  return {64 * b, wide ? t : t == 3 ? 4 : t, w};
+}
+// Short index of element c of tile t.
+__host__ __device__ __forceinline__ int column_of(const Block &b, int wide, int t, int c) {
+  return b.first + (wide ? 16 * t + c : b.tiles * c + t);
+}
 
-__device__ __forceinline__ int tile_index(int ti, int tj) { return tj * (tj + 1) / 2 + ti; }
+constexpr int kGramThreads = 256;
+constexpr int kGramRows = 64;                  // long rows that a workgroup takes at a time
+constexpr int kPairDoubles = 16 * 256;
+
+__host__ __device__ inline int pairs_of(int k) {
+  const int nb = (k + 63) / 64;
+  return nb * (nb + 1) / 2;
+}
 
 // Matrices to a launch whose arguments describe them.
 constexpr int kMuonChunk = 32;
@@ -190,100 +166,205 @@ struct MuonChunk {
   MuonMat mats[kMuonChunk];
 };
 
-template <int NB>
-__global__ __launch_bounds__(Pairs<NB>::threads) void gram_kernel(MuonChunk c, MuonParams p,
-                                                                  MuonMat *table, double *ws) {
-  constexpr int threads = Pairs<NB>::threads;
-  const MuonMat &a = c.mats[blockIdx.y];
-  // the later launches find the matrix in the table
-  if (blockIdx.x == 0 && threadIdx.x == 0) table[c.first + blockIdx.y] = a;
-  if (int(blockIdx.x) >= a.splits || (a.k + 63) / 64 != NB) return;
-  extern __shared__ __align__(16) float us[];
-  const int kp = padded(a.k), NT = kp / 16, pitch = slab_pitch(kp), rows = slab_rows(kp);
+// A wavefront's 16 long rows of one block of T tiles as the products' operands:
+// x[s][t] is tile t's of product s.
+template <bool WIDE, bool Q, bool kStep, int T>
+struct GramRows;
+
+// tall: rows r .. r + 15, four to a product
+template <bool Q, bool kStep, int T>
+struct GramRows<false, Q, kStep, T> {
+  Run<T> g[4], m[4];
+  Place at[4];
+  int live[4];
+  __device__ __forceinline__ void request(const MuonMat &a, const MuonParams &p, const Block &b,
+                                          int64_t r, int64_t end) {
+    const int lane = threadIdx.x & 63, grp = lane >> 4, c = lane & 15;
+    const int mine = clamped(b.width - T * c, T);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int64_t row = r + 4 * s;
+      live[s] = row + grp < end ? mine : 0;
+      at[s] = {(row < end ? row : 0) * a.k + b.first, uint32_t(grp * a.k + T * c)};
+      g[s] = kStep || !a.m || p.nesterov ? load_run<Q, T>(a.grad, at[s], live[s]) : Run<T>{};
+      m[s] = a.m ? load_run<Q, T>(a.m, at[s], live[s]) : Run<T>{};
+    }
+  }
+  __device__ __forceinline__ void finish(const MuonMat &a, const MuonParams &p, double (&x)[4][T]) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+        x[s][t] = double(direction<kStep>(p, a.m != nullptr, g[s].v[t], m[s].v[t]));
+      if (kStep && a.m) store_run<Q, T>(a.m, at[s], live[s], m[s]);
+    }
+  }
+};
+// wide: long rows r .. r + 15, rows 4 g + s in product s
+template <bool Q, bool kStep, int T>
+struct GramRows<true, Q, kStep, T> {
+  Run<4> g[T], m[T];
+  Place at[T];
+  int live[T];
+  __device__ __forceinline__ void request(const MuonMat &a, const MuonParams &p, const Block &b,
+                                          int64_t r, int64_t end) {
+    const int lane = threadIdx.x & 63, grp = lane >> 4, c = lane & 15;
+    const int mine = clamped(end - (r + 4 * grp), 4);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      live[t] = 16 * t + c < b.width ? mine : 0;
+      at[t] = {(b.first + 16 * t) * a.n + (r < end ? r : 0), uint32_t(c * a.n) + 4 * grp};
+      g[t] = kStep || !a.m || p.nesterov ? load_run<Q, 4>(a.grad, at[t], live[t]) : Run<4>{};
+      m[t] = a.m ? load_run<Q, 4>(a.m, at[t], live[t]) : Run<4>{};
+    }
+  }
+  __device__ __forceinline__ void finish(const MuonMat &a, const MuonParams &p, double (&x)[4][T]) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        x[s][t] = double(direction<kStep>(p, a.m != nullptr, g[t].v[s], m[t].v[s]));
+      if (kStep && a.m) store_run<Q, 4>(a.m, at[t], live[t], m[t]);
+    }
+  }
+};
+
+__device__ __forceinline__ void pair_of(int p, int &bi, int &bj) {
+  bj = 0;
+  while (p > bj) p -= ++bj;
+  bi = p;
+}
+
+// The rows of a slab that are this wavefront's, for blocks of TI and TJ tiles
+// (kSame: one block).  Everything that the products depend on is known here:
+// a branch between two products costs the wait for their results.
+template <bool kSame, bool WIDE, bool Q, bool kStep, int TI, int TJ>
+__device__ __forceinline__ void gram_rows(const MuonMat &a, const MuonParams &p, const Block &bi,
+                                          const Block &bj, int64_t from, int64_t end,
+                                          f64x4_t (&acc)[4][4]) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  GramRows<WIDE, Q, kStep, TI> x;
+  GramRows<WIDE, Q, kStep, TJ> y;
+  int64_t r = from + 16 * wave;
+  x.request(a, p, bi, r, end);
+  if (!kSame) y.request(a, p, bj, r, end);
+  for (; r < end; r += kGramRows) {
+    double u[4][TI], v[4][TJ];
+    x.finish(a, p, u);
+    if (!kSame) y.finish(a, p, v);
+    // the next rows are on their way while these are multiplied (past the end:
+    // nothing is live)
+    x.request(a, p, bi, r + kGramRows, end);
+    if (!kSame) y.request(a, p, bj, r + kGramRows, end);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int i = 0; i < (kSame ? j + 1 : TI); ++i)
+          if constexpr (kSame) acc[i][j] = mfma64(u[s][i], u[s][j], acc[i][j]);
+          else acc[i][j] = mfma64(u[s][i], v[s][j], acc[i][j]);
+  }
+}
+
+// ONE: k <= 64.  Q: matrices of 16-byte accesses, or the others (whose loads take
+// more registers).
+template <bool ONE, bool Q>
+__global__ __launch_bounds__(kGramThreads, 2) void gram_kernel(const MuonMat *table, MuonParams p,
+                                                            double *ws) {
+  __shared__ double sum[kPairDoubles];
+  const MuonMat a = table[blockIdx.z];
+  if ((a.k <= 64) != ONE || bool(a.quads) != Q || int(blockIdx.x) >= a.splits ||
+      int(blockIdx.y) >= pairs_of(a.k))
+    return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int fr = lane >> 4, fc = lane & 15;
-  int bi = 0, bj = 0;                       // this wavefront's pair of blocks
-  if (NB > 1)
-    for (int q = wave; q > bj; q -= ++bj) bi = q - bj - 1;
+  int bi = 0, bj = 0;
+  if (!ONE) pair_of(int(blockIdx.y), bi, bj);
   f64x4_t acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f64x4_t{0.0, 0.0, 0.0, 0.0};
-  clear<threads>(us, rows * pitch);
   const int64_t from = int64_t(blockIdx.x) * a.span;
   const int64_t end = from + a.span < a.n ? from + a.span : a.n;
-  for (int64_t at = from; at < end; at += rows) {
-    __syncthreads();
-    stage<true, threads, kSlabMost>(a, p, at, rows, pitch, us);
-    __syncthreads();
-    const int step = NB == 1 ? 16 : 4;
-    for (int r = NB == 1 ? 4 * wave : 0; r < rows; r += step) {
-      const float *row = us + (r + fr) * pitch + fc;
-      double x[4], y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = 64 * bi + 16 * i < kp ? double(row[64 * bi + 16 * i]) : 0.0;
-        if (NB > 1) y[i] = 64 * bj + 16 * i < kp ? double(row[64 * bj + 16 * i]) : 0.0;
+  const Block b = block_of(a.k, bi, a.wide), c = block_of(a.k, bj, a.wide);
+  with_bool(a.wide, [&](auto WIDE) {
+    with_tiles(c.tiles, [&](auto T) {
+      constexpr int TJ = decltype(T)::value;
+      constexpr bool w = decltype(WIDE)::value;
+      if constexpr (w || TJ != 3) {
+        if (ONE || bi == bj) gram_rows<true, w, Q, ONE, TJ, TJ>(a, p, b, c, from, end, acc);
+        // (all blocks but the last have four tiles)
+        else if constexpr (!ONE) gram_rows<false, w, Q, ONE, 4, TJ>(a, p, b, c, from, end, acc);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (4 * bj + j >= NT) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (4 * bi + i <= 4 * bj + j) acc[i][j] = mfma64(x[i], NB > 1 ? y[j] : x[j], acc[i][j]);
-      }
-    }
-  }
-  const int tiles = NT * (NT + 1) / 2;
-  double *out = ws + a.area + int64_t(blockIdx.x) * tiles * 256;
-  if (NB == 1) {
-    // the four wavefronts' sums in their order
-    double *sum = reinterpret_cast<double *>(us);
-    for (int w = 0; w < 4; ++w) {
-      __syncthreads();
-      if (wave == w) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i <= j; ++i)
-            if (j < NT) {
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                double *s = sum + (tile_index(i, j) * 4 + r) * 64 + lane;
-                *s = w == 0 ? acc[i][j][r] : *s + acc[i][j][r];
-              }
-            }
-      }
-    }
+    });
+  });
+  // the four wavefronts' sums in their order
+  for (int w = 0; w < 4; ++w) {
     __syncthreads();
-    for (int e = threadIdx.x; e < tiles * 256; e += threads) out[e] = sum[e];
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
+    if (wave != w) continue;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (4 * bj + j < NT && 4 * bi + i <= 4 * bj + j) {
-        double *o = out + tile_index(4 * bi + i, 4 * bj + j) * 256 + lane;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[64 * r] = acc[i][j][r];
+      for (int j = 0; j < 4; ++j) {
+        if (i >= b.tiles || j >= c.tiles || (bi == bj && i > j)) continue;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          double *s = sum + ((4 * i + j) * 4 + r) * 64 + lane;
+          *s = w == 0 ? acc[i][j][r] : *s + acc[i][j][r];
+        }
       }
+  }
+  __syncthreads();
+  double *out = ws + a.area + (int64_t(blockIdx.x) * pairs_of(a.k) + blockIdx.y) * kPairDoubles;
+  for (int e = threadIdx.x; e < kPairDoubles; e += kGramThreads) {
+    const int i = e >> 10, j = (e >> 8) & 3;
+    if (i < b.tiles && j < c.tiles && (bi != bj || i <= j)) out[e] = sum[e];
+  }
+}
+
+// The table of the call's matrices, which the other launches read.
+__global__ __launch_bounds__(64) void table_kernel(MuonChunk c, MuonMat *table) {
+  if (int(threadIdx.x) < c.count) table[c.first + threadIdx.x] = c.mats[threadIdx.x];
+}
+
+// The momentum of matrices of k > 64, whose values several wavefronts read.
+__global__ __launch_bounds__(256) void momentum_kernel(const MuonMat *table, MuonParams p) {
+  const MuonMat a = table[blockIdx.y];
+  if (a.k <= 64 || !a.m) return;
+  const int64_t all = a.n * a.k, step = int64_t(gridDim.x) * 1024;
+  for (int64_t first = int64_t(blockIdx.x) * 1024; first < all; first += step) {
+    const int live = clamped(all - first - 4 * int(threadIdx.x), 4);
+    with_bool(a.quads, [&](auto Q) {
+      constexpr bool q = decltype(Q)::value;
+      const Place at = {first, 4u * threadIdx.x};
+      const Run<4> g = load_run<q, 4>(a.grad, at, live);
+      Run<4> m = load_run<q, 4>(a.m, at, live);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) (void)direction<true>(p, true, g.v[i], m.v[i]);
+      store_run<q, 4>(a.m, at, live, m);
+    });
+  }
 }
 
 // Sum of a matrix's partials into the first, an element to a lane.
 __global__ __launch_bounds__(256) void gram_sum_kernel(const MuonMat *table, double *ws) {
-  const MuonMat a = table[blockIdx.y];
-  if (a.k <= 16) return;                   // one tile: small_kernel sums it
-  const int NT = padded(a.k) / 16, n = NT * (NT + 1) / 2 * 256;
-  const int e = int(blockIdx.x) * 256 + threadIdx.x;
-  if (e >= n) return;
-  double *x = ws + a.area + e;
+  const MuonMat a = table[blockIdx.z];
+  const int pairs = pairs_of(a.k);
+  if (a.k <= 16 || int(blockIdx.y) >= pairs) return;       // (one tile: small_kernel sums it)
+  int bi, bj;
+  pair_of(int(blockIdx.y), bi, bj);
+  const int i = int(blockIdx.x) >> 2, j = int(blockIdx.x) & 3;
+  if (i >= block_of(a.k, bi, a.wide).tiles || j >= block_of(a.k, bj, a.wide).tiles ||
+      (bi == bj && i > j))
+    return;
+  double *x = ws + a.area + int64_t(blockIdx.y) * kPairDoubles + int(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t n = int64_t(pairs) * kPairDoubles;
   double s = 0.0;
   for (int b = 0; b < a.splits; b += 8) {
     double v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = b + i < a.splits ? x[int64_t(b + i) * n] : 0.0;
+    for (int i = 0; i < 8; ++i) v[i] = b + i < a.splits ? x[(b + i) * n] : 0.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += v[i];
   }
@@ -346,22 +427,26 @@ __global__ __launch_bounds__(Small<NT>::threads) void small_kernel(const MuonMat
   double *G = sq, *P = sq + S::size, *Q = sq + 2 * S::size;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double *area = ws + a.area;
-  for (int e = threadIdx.x; e < S::tiles * 256; e += S::threads) {
+  // (a tall matrix of 33 .. 48 columns has four tiles of partials: columns 4 c + t)
+  const Block b = block_of(a.k, 0, a.wide);
+  for (int e = threadIdx.x; e < (NT == 1 ? 256 : kPairDoubles); e += S::threads) {
+    const int ti = e >> 10, tj = (e >> 8) & 3;
+    if (tj >= b.tiles || ti > tj) continue;
     double v = 0.0;
     if (NT == 1) {                         // one tile: its partials are summed here
-      for (int b = 0; b < a.splits; b += 8) {
+      for (int q = 0; q < a.splits; q += 8) {
         double w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = b + i < a.splits ? area[(b + i) * 256 + e] : 0.0;
+        for (int i = 0; i < 8; ++i) w[i] = q + i < a.splits ? area[int64_t(q + i) * kPairDoubles + e] : 0.0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v += w[i];
       }
     } else {
       v = area[e];
     }
-    int ti, tj;
-    tile_of_index(e / 256, ti, tj);
-    const int i = 16 * ti + ((e & 63) >> 4) + 4 * ((e >> 6) & 3), j = 16 * tj + (e & 15);
+    const int i = column_of(b, a.wide, ti, ((e & 63) >> 4) + 4 * ((e >> 6) & 3));
+    const int j = column_of(b, a.wide, tj, e & 15);
+    if (i >= S::kp || j >= S::kp) continue;
     G[i * S::pitch + j] = v;
     if (ti < tj) G[j * S::pitch + i] = v;
   }
@@ -453,22 +538,24 @@ __global__ __launch_bounds__(Small<NT>::threads) void small_kernel(const MuonMat
 // S, H, P, Q, Q'.  A workgroup owns one 16 x 16 tile of the upper triangle of a
 // product, its four wavefronts a quarter of the sum each; operands come from
 // L2 (both symmetric, so every fragment is four runs of 128 bytes).
-enum MuonStage { kUnpack, kSquare, kPolynomial, kAdvance };
+enum MuonStage { kSquare, kPolynomial, kAdvance };
 
 struct Slots {
-  double *G, *S, *H, *P, *Q[2];
+  double *G, *S, *H, *P, *Q0, *Q1;
   __device__ __forceinline__ Slots(double *area, int kp) {
     const int64_t n = int64_t(kp) * kp;
-    G = area + n;                 // past the summed partials
+    G = area + int64_t(pairs_of(kp)) * kPairDoubles;   // past the summed partials
     S = G + n;
     H = S + n;
     P = H + n;
-    Q[0] = P + n;
-    Q[1] = Q[0] + n;
+    Q0 = P + n;
+    Q1 = Q0 + n;
   }
+  __device__ __forceinline__ double *Q(int i) const { return i & 1 ? Q1 : Q0; }
 };
 
-// A quarter of the sum of tile (ti, tj) of A B.
+// A quarter of the sum of tile (ti, tj) of A B.  All operands are requested
+// before the first product (steps past the quarter's end read its last rows).
 __device__ __forceinline__ f64x4_t part_product(const double *A, const double *B, int kp, int ti,
                                                 int tj, int wave) {
   const int lane = threadIdx.x & 63;
@@ -476,8 +563,19 @@ __device__ __forceinline__ f64x4_t part_product(const double *A, const double *B
   const int64_t at = int64_t(4 * wave * steps + (lane >> 4)) * kp + (lane & 15);
   const double *x = A + at + 16 * ti, *y = B + at + 16 * tj;
   f64x4_t d = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 4
-  for (int q = 0; q < steps; ++q) d = mfma64(x[4 * q * kp], y[4 * q * kp], d);
+#pragma unroll
+  for (int h = 0; h < 16; h += 8) {
+    if (h >= steps) break;
+    double u[8], v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = h + i < steps ? h + i : steps - 1;
+      u[i] = x[4 * q * kp];
+      v[i] = y[4 * q * kp];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d = mfma64(h + i < steps ? u[i] : 0.0, v[i], d);
+  }
   return d;
 }
 
@@ -492,6 +590,25 @@ __device__ __forceinline__ double joined_part(f64x4_t d, int wave, double (*red)
 #pragma unroll
   for (int w = 0; w < 4; ++w) s += red[w][wave][lane];
   return s;
+}
+
+// The summed partials of a block pair into G, both ways round.
+__global__ __launch_bounds__(256) void unpack_kernel(const MuonMat *table, double *ws) {
+  const MuonMat a = table[blockIdx.z];
+  if (a.k <= 64 || int(blockIdx.y) >= pairs_of(a.k)) return;
+  const int kp = padded(a.k), ti = int(blockIdx.x) >> 2, tj = int(blockIdx.x) & 3;
+  int bi, bj;
+  pair_of(int(blockIdx.y), bi, bj);
+  const Block b = block_of(a.k, bi, a.wide), c = block_of(a.k, bj, a.wide);
+  if (ti >= b.tiles || tj >= c.tiles || (bi == bj && ti > tj)) return;
+  const int e = threadIdx.x;
+  const int i = column_of(b, a.wide, ti, ((e & 63) >> 4) + 4 * (e >> 6));
+  const int j = column_of(c, a.wide, tj, e & 15);
+  if (i >= kp || j >= kp) return;
+  const double v = ws[a.area + int64_t(blockIdx.y) * kPairDoubles + int(blockIdx.x) * 256 + e];
+  double *G = Slots(ws + a.area, kp).G;
+  G[int64_t(i) * kp + j] = v;
+  G[int64_t(j) * kp + i] = v;
 }
 
 __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonParams p, double *ws,
@@ -512,15 +629,11 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
     M[ij] = v;
     if (ti < tj) M[ji] = v;
   };
-  if (stage == kUnpack) {
-    put(m.G, ws[a.area + t * 256 + 64 * wave + lane]);
-    return;
-  }
   if (stage == kSquare) {
     put(m.S, joined_part(part_product(m.G, m.G, kp, ti, tj, wave), wave, red[0]));
     return;
   }
-  const double *q = m.Q[it & 1];
+  const double *q = m.Q(it);
   if (stage == kPolynomial) {
     // the first G is not yet scaled: its powers take the factor here
     double f = 1.0, inv = 1.0;
@@ -539,7 +652,7 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
     const double g = f * m.G[ij], s = f * f * m.S[ij];
     const double v = (i == j ? p.a : 0.0) + p.b * g + p.c * s;
     put(m.P, v);
-    if (it == 0) put(m.Q[1], inv * v);
+    if (it == 0) put(m.Q1, inv * v);
     if (!last)
       put(m.H, p.a * g + p.b * s +
                    p.c * (f * f * f *
@@ -550,74 +663,306 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
   if (it + 1 < p.steps)
     put(m.G, joined_part(part_product(m.H, m.P, kp, ti, tj, wave), wave, red[0]));
   if (it > 0)
-    put(m.Q[(it + 1) & 1], joined_part(part_product(q, m.P, kp, ti, tj, wave), wave, red[1]));
+    put(m.Q(it + 1), joined_part(part_product(q, m.P, kp, ti, tj, wave), wave, red[1]));
 }
 
 // ------------------------------------------------------------ the update
 //
-// O = u Q for `rows` long rows at a time: u staged in LDS as above, a wavefront
-// to 16 rows, four tiles of columns at a time.  Of a tall matrix the long side
-// is the rows of a tile, of a wide one its columns (the operands swapped: Q is
-// symmetric), so that 16 lanes always run along memory.  kLds: Q is in LDS too.
-constexpr int kApplyRows = 64;
+// O = u Q and theta's step.  The operands and results of a product are again
+// chosen for the memory: u comes straight into registers, four values of a lane
+// at a time, and a lane's results of all tiles are neighbours.
+//
+// A value's step from its X.
+__device__ __forceinline__ float stepped(const MuonParams &p, float scale, float th, float x) {
+  return th - p.lr * (scale * x + p.wd * th);
+}
 
-template <bool kLds>
-__global__ __launch_bounds__(256) void apply_kernel(const MuonMat *table, MuonParams p,
-                                                    const double *ws) {
-  const MuonMat a = table[blockIdx.y];
-  const int kp = padded(a.k), NT = kp / 16, pitch = slab_pitch(kp);
-  const int64_t from = int64_t(blockIdx.x) * a.apply;
-  if (from >= a.n || (a.k <= 64) != kLds) return;
-  extern __shared__ __align__(16) float us[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const double *Q = ws + a.area;
-  if (!kLds) Q = Slots(const_cast<double *>(Q), kp).Q[p.steps & 1];
-  clear<256>(us, kApplyRows * pitch);
-  double *ql = reinterpret_cast<double *>(us + (kApplyRows * pitch + 3) / 4 * 4);
-  if (kLds)
-    for (int e = threadIdx.x; e < kp * kp; e += 256) ql[e] = Q[e];
-  const double *qs = kLds ? ql : Q;
-  const int64_t end = from + a.apply < a.n ? from + a.apply : a.n;
-  for (int64_t at = from; at < end; at += kApplyRows) {
-    __syncthreads();
-    // (kSlabMost values at most are staged in one go)
-    for (int r = 0; r < kApplyRows; r += slab_rows(kp) < kApplyRows ? slab_rows(kp) : kApplyRows)
-      if (at + r < end)
-        stage<false, 256, kSlabMost>(a, p, at + r,
-                                     slab_rows(kp) < kApplyRows ? slab_rows(kp) : kApplyRows,
-                                     pitch, us + r * pitch);
-    __syncthreads();
-    const float *x = us + (16 * wave + (lane & 15)) * pitch + (lane >> 4);
-    for (int t0 = 0; t0 < NT; t0 += 4) {
-      f64x4_t d[4];
+template <bool Q, int N>
+__device__ __forceinline__ void update_run(const MuonMat &a, const MuonParams &p, Place at,
+                                           int live, const Run<N> &x, Run<N> th) {
+  if (a.update) store_run<Q, N>(a.update, at, live, x);
+  if (!a.theta) return;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) d[j] = f64x4_t{0.0, 0.0, 0.0, 0.0};
-      for (int q = 0; q < kp / 4; ++q) {
-        const double u = double(x[4 * q]);
-        const double *y = qs + (4 * q + (lane >> 4)) * kp + 16 * t0 + (lane & 15);
+  for (int i = 0; i < N; ++i) th.v[i] = stepped(p, a.scale, th.v[i], x.v[i]);
+  store_run<Q, N>(a.theta, at, live, th);
+  if (!a.theta16) return;
+  if constexpr (Q && N > 1) {
+    if (live) {
+      uint32_t h[N / 2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (t0 + j < NT) d[j] = a.wide ? mfma64(y[16 * j], u, d[j]) : mfma64(u, y[16 * j], d[j]);
-      }
+      for (int i = 0; i < N; i += 2) h[i / 2] = pack_bf16x2(th.v[i], th.v[i + 1]);
+      __builtin_memcpy(__builtin_assume_aligned(a.theta16 + at.base + at.lane, 2 * N), h, 2 * N);
+    }
+  } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < N; ++i)
+      if (i < live) (a.theta16 + at.base)[at.lane + i] = __builtin_bit_cast(uint16_t, (__bf16)th.v[i]);
+  }
+}
+
+// k <= 64: Q in LDS, a wavefront to 16 long rows (tall) or 32 (wide) at a time,
+// no barrier between them.
+//   tall: lane (g, c) loads columns 16 j + 4 g .. + 3 of row c, the operands of
+//     four products; tile t has columns NT c + t.
+//   wide: lane (g, c) loads long rows 2 c, 2 c + 1 of column 4 s + g, the operands
+//     of two tiles; a result's rows are short.
+constexpr int kApplyRows = 256;              // long rows to a workgroup
+
+template <int NT, bool Q>
+__device__ __forceinline__ void apply_tall(const MuonMat &a, const MuonParams &p, const double *Qs,
+                                           int pitch, int64_t r, int64_t end) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const bool has_m = a.m != nullptr, read_g = !has_m || p.nesterov;
+  Run<4> gr[NT], m[NT];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int over = (lane >> 4) + 4 * r, along = lane & 15;
-          const int64_t i = at + 16 * wave + (a.wide ? along : over);
-          const int c = 16 * (t0 + j) + (a.wide ? over : along);
-          if (i >= a.n || c >= a.k) continue;
-          const int64_t e = a.wide ? int64_t(c) * a.n + i : i * a.k + c;
-          const float o = float(d[j][r]);
-          if (a.update) a.update[e] = o;
-          if (a.theta) {
-            const float th = a.theta[e], v = th - p.lr * (a.scale * o + p.wd * th);
-            a.theta[e] = v;
-            if (a.theta16) a.theta16[e] = __builtin_bit_cast(uint16_t, (__bf16)v);
-          }
-        }
+  for (int j = 0; j < NT; ++j) {
+    const int live = r + c < end ? clamped(a.k - 16 * j - 4 * g, 4) : 0;
+    const Place at = {r * a.k + (16 * j < a.k ? 16 * j : 0), uint32_t(c * a.k + 4 * g)};
+    gr[j] = read_g ? load_run<Q, 4>(a.grad, at, live) : Run<4>{};
+    m[j] = has_m ? load_run<Q, 4>(a.m, at, live) : Run<4>{};
+  }
+  Run<NT> th[4];
+  const int mine = clamped(a.k - NT * c, NT);
+  auto place = [&](int i) {
+    return Place{(r + 4 * i < end ? r + 4 * i : 0) * a.k, uint32_t(g * a.k + NT * c)};
+  };
+  auto live_of = [&](int i) { return r + 4 * i + g < end ? mine : 0; };
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    th[i] = a.theta ? load_run<Q, NT>(a.theta, place(i), live_of(i)) : Run<NT>{};
+  f64x4_t d[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) d[t] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const double u = double(direction<false>(p, has_m, gr[j].v[e], m[j].v[e]));
+      const double *y = Qs + (16 * j + 4 * g + e) * pitch + NT * c;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) d[t] = mfma64(u, y[t], d[t]);
+    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    Run<NT> x;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) x.v[t] = float(d[t][i]);
+    update_run<Q, NT>(a, p, place(i), live_of(i), x, th[i]);
+  }
+}
+
+template <int NT, bool Q>
+__device__ __forceinline__ void apply_wide(const MuonMat &a, const MuonParams &p, const double *Qs,
+                                           int pitch, int64_t r, int64_t end) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const bool has_m = a.m != nullptr, read_g = !has_m || p.nesterov;
+  const int along = clamped(end - r - 2 * c, 2);
+  f64x4_t d[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) d[t][0] = d[t][1] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+  // column (row of memory) 4 s + g
+  auto place = [&](int s) {
+    return Place{(4 * s < a.k ? 4 * s : 0) * a.n + r, uint32_t(g * a.n) + 2 * c};
+  };
+  auto live_of = [&](int s) { return 4 * s + g < a.k ? along : 0; };
+  Run<2> gr[4 * NT], m[4 * NT];
+#pragma unroll
+  for (int s = 0; s < 4 * NT; ++s) {
+    const Place at = place(s);
+    const int live = live_of(s);
+    gr[s] = read_g ? load_run<Q, 2>(a.grad, at, live) : Run<2>{};
+    m[s] = has_m ? load_run<Q, 2>(a.m, at, live) : Run<2>{};
+  }
+#pragma unroll
+  for (int s = 0; s < 4 * NT; ++s) {
+    const double *y = Qs + (4 * s + g) * pitch + c;
+    double u[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) u[e] = double(direction<false>(p, has_m, gr[s].v[e], m[s].v[e]));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const double w = y[16 * t];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) d[t][e] = mfma64(w, u[e], d[t][e]);
     }
   }
+  Run<2> th[4 * NT];
+#pragma unroll
+  for (int i = 0; i < 4 * NT; ++i)
+    th[i] = a.theta ? load_run<Q, 2>(a.theta, place(i), live_of(i)) : Run<2>{};
+#pragma unroll
+  for (int i = 0; i < 4 * NT; ++i) {
+    const Run<2> x = {{float(d[i / 4][0][i % 4]), float(d[i / 4][1][i % 4])}};
+    update_run<Q, 2>(a, p, place(i), live_of(i), x, th[i]);
+  }
+}
+
+template <int NT, bool ALIGNED>
+__global__ __launch_bounds__(256, 2) void apply_kernel(const MuonMat *table, MuonParams p,
+                                                    const double *ws) {
+  constexpr int K = 16 * NT, pitch = K + 2;
+  __shared__ __align__(16) double Q[K * pitch];
+  const MuonMat a = table[blockIdx.y];
+  const int kp = padded(a.k);
+  const int64_t from = int64_t(blockIdx.x) * kApplyRows;
+  if (from >= a.n || kp > K || (NT > 1 && kp <= K / 2) || bool(a.quads) != ALIGNED) return;
+  const int64_t end = from + kApplyRows < a.n ? from + kApplyRows : a.n;
+  const double *q = ws + a.area;
+  for (int e = threadIdx.x; e < K * K; e += 256) {
+    const int i = e / K, j = e % K;
+    Q[i * pitch + j] = i < kp && j < kp ? q[i * kp + j] : 0.0;
+  }
+  __syncthreads();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (a.wide) {
+    for (int64_t r = from + 32 * wave; r < end; r += 128)
+      apply_wide<NT, ALIGNED>(a, p, Q, pitch, r, end);
+  } else {
+    for (int64_t r = from + 16 * wave; r < end; r += 64)
+      apply_tall<NT, ALIGNED>(a, p, Q, pitch, r, end);
+  }
+}
+
+// k > 64: 64 long rows of u in LDS (fp32) for a workgroup, each of whose NB
+// wavefronts forms a block of 64 columns of O; Q comes from L2, each value once
+// a workgroup, requested a product ahead.
+constexpr int kLargeRows = 64;
+
+// LDS row pitch (floats): 17 past a multiple of 64, so that a fragment (16 rows
+// of 4) and a column written by consecutive lanes spread over the banks.
+__host__ __device__ constexpr int large_pitch(int kp) { return (kp + 46) / 64 * 64 + 17; }
+
+// The products and the update of T tiles of columns (q: the first one's Q).
+template <bool WIDE, int T>
+__device__ __forceinline__ void large_block(const MuonMat &a, const MuonParams &p, const float *us,
+                                            int pitch, const double *q, int kp, int64_t from,
+                                            int first) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  f64x4_t d[4][T];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int t = 0; t < T; ++t) d[i][t] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+  // two products of operands in hand, two on their way (kp / 4 is a multiple of
+  // four; past the end the last ones again)
+  double y[4][T];
+  float x[4][4];
+  const float *xs = us + c * pitch + g;
+  const double *ys = q + int64_t(g) * kp + c;
+  const int last = kp / 4 - 2;
+  auto request = [&](int at, int s) {
+    const int e = s < last ? s : last;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int t = 0; t < T; ++t) y[at + h][t] = ys[int64_t(4 * (e + h)) * kp + 16 * t];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[at + h][i] = xs[16 * i * pitch + 4 * (e + h)];
+    }
+  };
+  auto multiply = [&](int at) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const double u = double(x[at + h][i]);
+          d[i][t] = WIDE ? mfma64(y[at + h][t], u, d[i][t]) : mfma64(u, y[at + h][t], d[i][t]);
+        }
+  };
+  request(0, 0);
+  for (int s = 0; s < kp / 4; s += 4) {
+    request(2, s + 2);
+    multiply(0);
+    request(0, s + 4);
+    multiply(2);
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    Run<1> th[4][4];
+    // long row row0 + (wide: c, tall: g), column col0 + (wide: g, tall: c)
+    auto row0 = [&](int i, int r) { return from + 16 * i + (WIDE ? 0 : 4 * r); };
+    auto col0 = [&](int r) { return first + 16 * t + (WIDE ? 4 * r : 0); };
+    auto live_of = [&](int i, int r) {
+      return row0(i, r) + (WIDE ? c : g) < a.n && col0(r) + (WIDE ? g : c) < a.k;
+    };
+    auto place = [&](int i, int r) {
+      const int64_t row = row0(i, r) < a.n ? row0(i, r) : 0;
+      const int col = col0(r) < a.k ? col0(r) : 0;
+      return WIDE ? Place{col * a.n + row, uint32_t(g * a.n) + c}
+                  : Place{row * a.k + col, uint32_t(g * a.k + c)};
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        th[i][r] = a.theta ? load_run<true, 1>(a.theta, place(i, r), live_of(i, r)) : Run<1>{};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        update_run<true, 1>(a, p, place(i, r), live_of(i, r), Run<1>{{float(d[i][t][r])}}, th[i][r]);
+  }
+}
+
+// u of 64 long rows into LDS, four values of a lane at a time along memory.
+template <bool WIDE, bool Q, int threads>
+__device__ __forceinline__ void stage_rows(const MuonMat &a, const MuonParams &p, int64_t from,
+                                           int kp, int pitch, float *us) {
+  const bool has_m = a.m != nullptr, read_g = !has_m || p.nesterov;
+  const int per = WIDE ? kLargeRows / 4 : (a.k + 3) / 4;         // runs of a memory row
+  const int items = WIDE ? a.k * per : kLargeRows * per;
+  const uint32_t inv = 0xffffffffu / uint32_t(per) + 1u;         // e / per for e < 2^16
+  for (int e0 = threadIdx.x; e0 < items; e0 += 4 * threads) {
+    Run<4> gr[4], m[4];
+    int slot[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + i * threads, hi = int(__umulhi(uint32_t(e), inv)), lo = 4 * (e - hi * per);
+      const int64_t row = from + (WIDE ? lo : hi);
+      const int live = e < items && row < a.n ? clamped(WIDE ? a.n - row : a.k - lo, 4) : 0;
+      // (255 n + 63 and 64 k fit 32 bits)
+      const Place at = WIDE ? Place{from, uint32_t(hi) * uint32_t(a.n) + lo}
+                            : Place{from * a.k, uint32_t(hi * a.k + lo)};
+      gr[i] = read_g ? load_run<Q, 4>(a.grad, at, live) : Run<4>{};
+      m[i] = has_m ? load_run<Q, 4>(a.m, at, live) : Run<4>{};
+      slot[i] = e >= items ? -1 : WIDE ? lo * pitch + hi : hi * pitch + lo;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (slot[i] < 0) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        us[slot[i] + e * (WIDE ? pitch : 1)] = direction<false>(p, has_m, gr[i].v[e], m[i].v[e]);
+    }
+  }
+  // the columns past k (a tall row's last run has filled some)
+  const int filled = WIDE ? a.k : 4 * per, pad = kp - filled;
+  for (int e = threadIdx.x; e < kLargeRows * pad; e += threads)
+    us[e / pad * pitch + filled + e % pad] = 0.0f;
+}
+
+template <int NB>
+__global__ __launch_bounds__(64 * NB) void apply_large_kernel(const MuonMat *table, MuonParams p,
+                                                              double *ws) {
+  extern __shared__ __align__(16) float us[];
+  const MuonMat a = table[blockIdx.y];
+  const int64_t from = int64_t(blockIdx.x) * kLargeRows;
+  if (from >= a.n || (a.k + 63) / 64 != NB) return;
+  const int kp = padded(a.k), pitch = large_pitch(kp);
+  const int first = 64 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const double *q = Slots(ws + a.area, kp).Q(p.steps) + first;
+  with_bool(a.wide, [&](auto W) {
+    constexpr bool wide = decltype(W)::value;
+    with_bool(a.quads, [&](auto A) {
+      stage_rows<wide, decltype(A)::value, 64 * NB>(a, p, from, kp, pitch, us);
+    });
+    __syncthreads();
+    with_tiles((kp - first) / 16, [&](auto T) {
+      large_block<wide, decltype(T)::value>(a, p, us, pitch, q, kp, from, first);
+    });
+  });
 }
 
 template <class F>
@@ -625,19 +970,6 @@ bool raise_lds(F *f, int bytes) {
   return hipFuncSetAttribute(reinterpret_cast<const void *>(f),
                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess;
 }
-
-// LDS of a Gram workgroup of NB blocks: the largest slab (NB = 1: of 32
-// columns; its tiles' sums, 10 x 2 KiB, take less).
-template <int NB>
-constexpr int gram_lds() {
-  return NB == 1 ? 128 * slab_pitch(32) * 4 : slab_rows(64 * NB) * slab_pitch(64 * NB) * 4;
-}
-static_assert(gram_lds<1>() >= 10 * 2048 && gram_lds<1>() >= 256 * slab_pitch(16) * 4 &&
-                  gram_lds<1>() >= 64 * slab_pitch(64) * 4,
-              "Gram LDS");
-
-constexpr int kApplyLds = kApplyRows * slab_pitch(64) * 4 + 64 * 64 * 8;
-constexpr int kApplyLdsLarge = kApplyRows * slab_pitch(256) * 4;
 
 // A matrix of a call: span0 as muon_span gives it for the call, o the doubles
 // of the workspace that the matrices before it take.
@@ -652,18 +984,18 @@ MuonMat planned(const qlora_muon_mat &q, int64_t span0, int64_t &o) {
   a.wide = q.rows < q.cols;
   a.n = a.wide ? q.cols : q.rows;
   a.k = int32_t(a.wide ? q.rows : q.cols);
-  auto ok16 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-  a.quads = ok16(a.grad) && ok16(a.m) && (a.wide ? a.n : int64_t(a.k)) % 4 == 0;
-  const int kp = padded(a.k), rows = slab_rows(kp);
+  auto ok = [](const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+  a.quads = (a.wide ? a.n : int64_t(a.k)) % 4 == 0 && ok(a.grad, 16) && ok(a.m, 16) &&
+            ok(a.theta, 16) && ok(a.theta16, 8) && ok(a.update, 16);
+  const int kp = padded(a.k);
   // a slab's k x k partial sums stay a small part of what it reads
   const int64_t span = span0 < kp / 2 ? kp / 2 : span0;
-  a.span = (span + rows - 1) / rows * rows;
+  a.span = (span + kGramRows - 1) / kGramRows * kGramRows;
   a.splits = int32_t((a.n + a.span - 1) / a.span);
-  a.apply = a.k <= 64 && a.span > kApplyRows ? a.span / kApplyRows * kApplyRows : kApplyRows;
   a.area = o;
-  const int64_t sq = int64_t(kp) * kp, tiles = int64_t(kp / 16) * (kp / 16 + 1) / 2 * 256;
-  const int64_t squares = (a.k <= 64 ? 1 : 7) * sq, partials = a.splits * tiles;
-  o += squares > partials ? squares : partials;
+  const int64_t first = int64_t(pairs_of(a.k)) * kPairDoubles, sq = int64_t(kp) * kp;
+  const int64_t squares = a.k <= 64 ? sq : first + 6 * sq;
+  o += squares > a.splits * first ? squares : a.splits * first;
   return a;
 }
 
@@ -691,38 +1023,48 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
   MuonMat *table = static_cast<MuonMat *>(work);
   double *ws = reinterpret_cast<double *>(static_cast<char *>(work) + table_bytes(n));
   const int64_t span = muon_span(mats, n);
-  int64_t o = 0, blocks = 0, blocks_large = 0;
+  // largest grids, by whether matrices have 16-byte accesses
+  int64_t o = 0, blocks[2][5] = {}, blocks_large[5] = {}, splits[2] = {}, splits_large[2] = {};
+  int64_t values = 0;
   int most_k = 0;
   bool small[5] = {};
+  auto raise = [](int64_t &to, int64_t v) { to = v > to ? v : to; };
   for (int32_t i = 0; i < n; i += kMuonChunk) {
     MuonChunk c;
     c.count = n - i < kMuonChunk ? n - i : kMuonChunk;
     c.first = i;
-    bool any[5] = {};
-    int32_t most = 0;
     for (int j = 0; j < c.count; ++j) {
       const MuonMat a = c.mats[j] = planned(mats[i + j], span, o);
-      any[(a.k + 63) / 64] = true;
-      most = a.splits > most ? a.splits : most;
       most_k = a.k > most_k ? a.k : most_k;
-      int64_t &b = a.k <= 64 ? blocks : blocks_large;
-      const int64_t need = (a.n + a.apply - 1) / a.apply;
-      b = need > b ? need : b;
-      if (a.k <= 64) small[(a.k + 15) / 16] = true;
+      const int kp = padded(a.k);
+      if (a.k <= 64) {
+        small[kp / 16] = true;
+        raise(splits[a.quads], a.splits);
+        raise(blocks[a.quads][kp <= 16 ? 1 : kp <= 32 ? 2 : 4], (a.n + kApplyRows - 1) / kApplyRows);
+      } else {
+        raise(splits_large[a.quads], a.splits);
+        raise(blocks_large[(a.k + 63) / 64], (a.n + kLargeRows - 1) / kLargeRows);
+        if (a.m) raise(values, a.n * a.k);
+      }
     }
-#define QLORA_GRAM(NB)                                                                         \
-  if (any[NB])                                                                                 \
-    hipLaunchKernelGGL((gram_kernel<NB>), dim3(unsigned(most), unsigned(c.count)),             \
-                       dim3(Pairs<NB>::threads), gram_lds<NB>(), s, c, p, table, ws)
-    QLORA_GRAM(1);
-    QLORA_GRAM(2);
-    QLORA_GRAM(3);
-    QLORA_GRAM(4);
-#undef QLORA_GRAM
+    hipLaunchKernelGGL(table_kernel, dim3(1), dim3(64), 0, s, c, table);
   }
-  const int NT = (most_k + 15) / 16;
-  const dim3 tiles(unsigned(NT * (NT + 1) / 2), unsigned(n));
-  if (most_k > 16) hipLaunchKernelGGL(gram_sum_kernel, tiles, dim3(256), 0, s, table, ws);
+  if (values) {
+    const int64_t b = (values + 1023) / 1024;
+    hipLaunchKernelGGL(momentum_kernel, dim3(unsigned(b < 1024 ? b : 1024), unsigned(n)), dim3(256), 0,
+                       s, table, p);
+  }
+#define QLORA_GRAM(ONE, Q, X, Y)                                                       \
+  if (X)                                                                               \
+    hipLaunchKernelGGL((gram_kernel<ONE, Q>), dim3(unsigned(X), unsigned(Y), unsigned(n)), \
+                       dim3(kGramThreads), 0, s, table, p, ws)
+  QLORA_GRAM(true, true, splits[1], 1);
+  QLORA_GRAM(true, false, splits[0], 1);
+  QLORA_GRAM(false, true, splits_large[1], pairs_of(most_k));
+  QLORA_GRAM(false, false, splits_large[0], pairs_of(most_k));
+#undef QLORA_GRAM
+  const dim3 pairs(16, unsigned(pairs_of(most_k)), unsigned(n));
+  if (most_k > 16) hipLaunchKernelGGL(gram_sum_kernel, pairs, dim3(256), 0, s, table, ws);
 #define QLORA_SMALL(NT)                                                                 \
   if (small[NT]) {                                                                      \
     static const bool ok = raise_lds(&small_kernel<NT>, Small<NT>::bytes);              \
@@ -736,25 +1078,41 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
   QLORA_SMALL(4)
 #undef QLORA_SMALL
   if (most_k > 64) {
+    const int NT = (most_k + 15) / 16;
+    const dim3 tiles(unsigned(NT * (NT + 1) / 2), unsigned(n));
     auto go = [&](int stage, int it) {
       hipLaunchKernelGGL(stage_kernel, tiles, dim3(256), 0, s, table, p, ws, stage, it);
     };
-    go(kUnpack, 0);
+    hipLaunchKernelGGL(unpack_kernel, pairs, dim3(256), 0, s, table, ws);
     for (int it = 0; it < p.steps; ++it) {
       go(kSquare, it);
       go(kPolynomial, it);
       if (p.steps > 1) go(kAdvance, it);
     }
   }
-  if (blocks)
-    hipLaunchKernelGGL((apply_kernel<true>), dim3(unsigned(blocks), unsigned(n)), dim3(256),
-                       kApplyLds, s, table, p, ws);
-  if (blocks_large) {
-    static const bool ok = raise_lds(&apply_kernel<false>, kApplyLdsLarge);
-    if (!ok) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((apply_kernel<false>), dim3(unsigned(blocks_large), unsigned(n)),
-                       dim3(256), kApplyLdsLarge, s, table, p, ws);
+#define QLORA_APPLY(NT, Q)                                                                     \
+  if (blocks[Q][NT])                                                                           \
+    hipLaunchKernelGGL((apply_kernel<NT, Q>), dim3(unsigned(blocks[Q][NT]), unsigned(n)),      \
+                       dim3(256), 0, s, table, p, ws)
+  QLORA_APPLY(1, true);
+  QLORA_APPLY(1, false);
+  QLORA_APPLY(2, true);
+  QLORA_APPLY(2, false);
+  QLORA_APPLY(4, true);
+  QLORA_APPLY(4, false);
+#undef QLORA_APPLY
+#define QLORA_APPLY(NB)                                                                    \
+  if (blocks_large[NB]) {                                                                  \
+    constexpr int lds = kLargeRows * large_pitch(64 * NB) * 4;                             \
+    static const bool ok = raise_lds(&apply_large_kernel<NB>, lds);                        \
+    if (!ok) return hipErrorInvalidValue;                                                  \
+    hipLaunchKernelGGL((apply_large_kernel<NB>), dim3(unsigned(blocks_large[NB]), unsigned(n)), \
+                       dim3(64 * NB), lds, s, table, p, ws);                               \
   }
+  QLORA_APPLY(2)
+  QLORA_APPLY(3)
+  QLORA_APPLY(4)
+#undef QLORA_APPLY
   return hipGetLastError();
 }
 
