@@ -21,16 +21,17 @@
 // 16 x 16 tiles, one launch a product; the last product and the update.
 #include <type_traits>
 
-#include "device.h"
+#include "objective.h"
 #include "qlora.h"
 
 namespace qlora {
 namespace {
 
 // A matrix in the kernels: n long, k short; quads: 16-byte accesses.  span: long rows to a Gram workgroup,
-// `splits` of them; area: where its fp64 scratch begins.
+// `splits` of them; area: where its fp64 scratch begins.  u: the direction, of
+// k > 64 (grad, m or an array of its own).
 struct MuonMat {
-  const float *grad;
+  const float *grad, *u;
   float *m, *theta;
   uint16_t *theta16;
   float *update;
@@ -50,7 +51,7 @@ __device__ __forceinline__ f64x4_t mfma64(double a, double b, f64x4_t d) {
 constexpr int kPad = 16;
 __host__ __device__ inline int padded(int k) { return (k + kPad - 1) / kPad * kPad; }
 
-// One value's momentum and the update's direction.
+// One value's momentum (kStep: advanced here) and the update's direction.
 template <bool kStep>
 __device__ __forceinline__ float direction(const MuonParams &p, bool has_m, float g, float &m) {
   if (!has_m) return g;
@@ -133,7 +134,7 @@ __device__ __forceinline__ void with_tiles(int t, F &&f) {
 //     consecutive long rows 4 g .. of column 16 t + c, one for each of four
 //     products.
 // The momentum is advanced on the way where one wavefront sees every value
-// (k <= 64), else by a pass of its own before.  The four wavefronts of a
+// (k <= 64), else by a pass of its own before, which also leaves u.  The four wavefronts of a
 // workgroup share a slab's rows and leave the sum of theirs, [pair][tile][
 // register][lane] in fp64, tile = 4 ti + tj.
 struct Block {
@@ -186,8 +187,8 @@ struct GramRows<false, Q, kStep, T> {
       const int64_t row = r + 4 * s;
       live[s] = row + grp < end ? mine : 0;
       at[s] = {(row < end ? row : 0) * a.k + b.first, uint32_t(grp * a.k + T * c)};
-      g[s] = kStep || !a.m || p.nesterov ? load_run<Q, T>(a.grad, at[s], live[s]) : Run<T>{};
-      m[s] = a.m ? load_run<Q, T>(a.m, at[s], live[s]) : Run<T>{};
+      g[s] = load_run<Q, T>(kStep ? a.grad : a.u, at[s], live[s]);
+      if (kStep) m[s] = a.m ? load_run<Q, T>(a.m, at[s], live[s]) : Run<T>{};
     }
   }
   __device__ __forceinline__ void finish(const MuonMat &a, const MuonParams &p, double (&x)[4][T]) {
@@ -195,7 +196,7 @@ struct GramRows<false, Q, kStep, T> {
     for (int s = 0; s < 4; ++s) {
 #pragma unroll
       for (int t = 0; t < T; ++t)
-        x[s][t] = double(direction<kStep>(p, a.m != nullptr, g[s].v[t], m[s].v[t]));
+        x[s][t] = double(kStep ? direction<true>(p, a.m != nullptr, g[s].v[t], m[s].v[t]) : g[s].v[t]);
       if (kStep && a.m) store_run<Q, T>(a.m, at[s], live[s], m[s]);
     }
   }
@@ -214,8 +215,8 @@ struct GramRows<true, Q, kStep, T> {
     for (int t = 0; t < T; ++t) {
       live[t] = 16 * t + c < b.width ? mine : 0;
       at[t] = {(b.first + 16 * t) * a.n + (r < end ? r : 0), uint32_t(c * a.n) + 4 * grp};
-      g[t] = kStep || !a.m || p.nesterov ? load_run<Q, 4>(a.grad, at[t], live[t]) : Run<4>{};
-      m[t] = a.m ? load_run<Q, 4>(a.m, at[t], live[t]) : Run<4>{};
+      g[t] = load_run<Q, 4>(kStep ? a.grad : a.u, at[t], live[t]);
+      if (kStep) m[t] = a.m ? load_run<Q, 4>(a.m, at[t], live[t]) : Run<4>{};
     }
   }
   __device__ __forceinline__ void finish(const MuonMat &a, const MuonParams &p, double (&x)[4][T]) {
@@ -223,7 +224,7 @@ struct GramRows<true, Q, kStep, T> {
     for (int t = 0; t < T; ++t) {
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        x[s][t] = double(direction<kStep>(p, a.m != nullptr, g[t].v[s], m[t].v[s]));
+        x[s][t] = double(kStep ? direction<true>(p, a.m != nullptr, g[t].v[s], m[t].v[s]) : g[t].v[s]);
       if (kStep && a.m) store_run<Q, 4>(a.m, at[t], live[t], m[t]);
     }
   }
@@ -328,7 +329,8 @@ __global__ __launch_bounds__(64) void table_kernel(MuonChunk c, MuonMat *table) 
   if (int(threadIdx.x) < c.count) table[c.first + threadIdx.x] = c.mats[threadIdx.x];
 }
 
-// The momentum of matrices of k > 64, whose values several wavefronts read.
+// The momentum of matrices of k > 64, whose values several wavefronts read, and
+// (Nesterov) their direction.
 __global__ __launch_bounds__(256) void momentum_kernel(const MuonMat *table, MuonParams p) {
   const MuonMat a = table[blockIdx.y];
   if (a.k <= 64 || !a.m) return;
@@ -340,18 +342,36 @@ __global__ __launch_bounds__(256) void momentum_kernel(const MuonMat *table, Muo
       const Place at = {first, 4u * threadIdx.x};
       const Run<4> g = load_run<q, 4>(a.grad, at, live);
       Run<4> m = load_run<q, 4>(a.m, at, live);
+      Run<4> u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) (void)direction<true>(p, true, g.v[i], m.v[i]);
+      for (int i = 0; i < 4; ++i) u.v[i] = direction<true>(p, true, g.v[i], m.v[i]);
       store_run<q, 4>(a.m, at, live, m);
+      if (p.nesterov) store_run<q, 4>(const_cast<float *>(a.u), at, live, u);
     });
   }
 }
+
+// The k x k matrices of k > 64 (kp x kp, row-major), behind the partials in the
+// matrix's area: G, S, H, P and Q in two places.
+struct Slots {
+  double *G, *S, *H, *P, *Q0, *Q1;
+  __device__ __forceinline__ Slots(double *area, int splits, int kp) {
+    const int64_t n = int64_t(kp) * kp;
+    G = area + int64_t(splits) * pairs_of(kp) * kPairDoubles;
+    S = G + n;
+    H = S + n;
+    P = H + n;
+    Q0 = P + n;
+    Q1 = Q0 + n;
+  }
+  __device__ __forceinline__ double *Q(int i) const { return i & 1 ? Q1 : Q0; }
+};
 
 // Sum of a matrix's partials into the first, an element to a lane.
 __global__ __launch_bounds__(256) void gram_sum_kernel(const MuonMat *table, double *ws) {
   const MuonMat a = table[blockIdx.z];
   const int pairs = pairs_of(a.k);
-  if (a.k <= 16 || int(blockIdx.y) >= pairs) return;       // (one tile: small_kernel sums it)
+  if (a.k <= 16 || int(blockIdx.y) >= pairs) return;       // (one tile: tiny_kernel sums it)
   int bi, bj;
   pair_of(int(blockIdx.y), bi, bj);
   const int i = int(blockIdx.x) >> 2, j = int(blockIdx.x) & 3;
@@ -368,42 +388,106 @@ __global__ __launch_bounds__(256) void gram_sum_kernel(const MuonMat *table, dou
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += v[i];
   }
-  *x = s;
+  if (a.k <= 64) {
+    *x = s;
+    return;
+  }
+  // k > 64: into G, both ways round
+  const int kp = padded(a.k), e = threadIdx.x;
+  const int row = column_of(block_of(a.k, bi, a.wide), a.wide, i, ((e & 63) >> 4) + 4 * (e >> 6));
+  const int col = column_of(block_of(a.k, bj, a.wide), a.wide, j, e & 15);
+  if (row >= kp || col >= kp) return;
+  double *G = Slots(ws + a.area, a.splits, kp).G;
+  G[int64_t(row) * kp + col] = s;
+  G[int64_t(col) * kp + row] = s;
 }
 
 // ---------------------------------------------- k x k iterations, k <= 64
 //
-// One workgroup, three fp64 matrices in LDS: G, S (then P), Q; row pitch 16
-// past a multiple of 32 doubles, so that the rows of a fragment fall on
-// different halves of the banks.  A product's tiles of the upper triangle are
-// dealt over the wavefronts, kept in registers until every read is done, and
-// stored with their mirror images.
+// Register r of a product's result is row l / 16 + 4 r, column l % 16 of its
+// tile: for the product's step r that is also the layout of a B operand, and of
+// an A operand whose matrix is symmetric, as all are here.  So a tile of a
+// result feeds the next products as it is.
+//
+// k <= 16: one tile, one wavefront, no LDS after the partials are summed: 17
+// products of four steps, each waiting for the last.
+__device__ __forceinline__ f64x4_t tile_product(const f64x4_t &a, const f64x4_t &b) {
+  f64x4_t d = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) d = mfma64(a[s], b[s], d);
+  return d;
+}
+
+// 1 / (|u| + eps) from |u|^2; a zero update stays zero.
+__device__ __forceinline__ double inverse_norm(double trace, double eps) {
+  const double d = sqrt(trace) + eps;
+  return d > 0.0 ? 1.0 / d : 0.0;
+}
+
+__global__ __launch_bounds__(256) void tiny_kernel(const MuonMat *table, MuonParams p, double *ws) {
+  __shared__ double part[4][64];
+  const MuonMat a = table[blockIdx.x];
+  if (a.k > 16) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  double *area = ws + a.area;
+  double v = 0.0;                                      // register `wave` of this lane
+  for (int q = 0; q < a.splits; q += 16) {
+    double w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      w[i] = area[int64_t(q + i < a.splits ? q + i : q) * kPairDoubles + threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += q + i < a.splits ? w[i] : 0.0;
+  }
+  part[wave][lane] = v;
+  __syncthreads();
+  if (wave) return;
+  f64x4_t G, Q, I;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    G[r] = part[r][lane];
+    I[r] = (lane >> 4) + 4 * r == (lane & 15) ? 1.0 : 0.0;
+  }
+  const double inv =
+      inverse_norm(wave_sum(G[0] * I[0] + G[1] * I[1] + G[2] * I[2] + G[3] * I[3]), p.eps);
+  G *= inv * inv;
+  Q = I * inv;
+  for (int it = 0; it < p.steps; ++it) {
+    const f64x4_t S = tile_product(G, G);
+    const f64x4_t P = p.a * I + p.b * G + p.c * S;
+    if (it + 1 < p.steps) {
+      const f64x4_t H = p.a * G + p.b * S + p.c * tile_product(G, S);
+      G = tile_product(H, P);
+    }
+    Q = tile_product(Q, P);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) area[((lane >> 4) + 4 * r) * 16 + (lane & 15)] = Q[r];
+}
+
+// 16 < k <= 64: one workgroup, three matrices in LDS: G, S (then P), Q, as tiles
+// of registers ([tile][register][lane], tile = NT ti + tj), so that every operand
+// is one contiguous read.  A product's tiles of the upper triangle are dealt
+// over the wavefronts, kept in registers until every read is done, and stored
+// with their mirror images.
 template <int NT>
 struct Small {
-  static constexpr int kp = 16 * NT, pitch = (kp + 15) / 32 * 32 + 16, tiles = NT * (NT + 1) / 2;
-  static constexpr int threads = NT == 1 ? 64 : NT == 2 ? 256 : 512, waves = threads / 64;
-  static constexpr int size = kp * pitch;
+  static constexpr int kp = 16 * NT, tiles = NT * (NT + 1) / 2, size = kp * kp;
+  static constexpr int threads = NT == 2 ? 256 : 512, waves = threads / 64;
   static constexpr int bytes = 3 * size * 8;
 };
 
 template <int NT>
 __device__ __forceinline__ f64x4_t lds_product(const double *A, const double *B, int ti, int tj) {
-  constexpr int pitch = Small<NT>::pitch;
   const int lane = threadIdx.x & 63;
-  const double *x = A + (lane >> 4) * pitch + (lane & 15) + 16 * ti;   // A symmetric: A[k][i]
-  const double *y = B + (lane >> 4) * pitch + (lane & 15) + 16 * tj;
+  const double *x = A + ti * 256 + lane, *y = B + tj * 256 + lane;
   f64x4_t d = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-  for (int q = 0; q < 4 * NT; ++q) d = mfma64(x[4 * q * pitch], y[4 * q * pitch], d);
-  return d;
-}
-
-// Tile (ti, tj) of a symmetric matrix, element by element: f(row, column, register).
-template <class F>
-__device__ __forceinline__ void each(int ti, int tj, F &&f) {
-  const int lane = threadIdx.x & 63;
+  for (int k = 0; k < NT; ++k)
 #pragma unroll
-  for (int r = 0; r < 4; ++r) f(16 * ti + (lane >> 4) + 4 * r, 16 * tj + (lane & 15), r);
+    for (int s = 0; s < 4; ++s)
+      d = mfma64(x[k * NT * 256 + 64 * s], y[k * NT * 256 + 64 * s], d);
+  return d;
 }
 
 __device__ __forceinline__ void tile_of_index(int t, int &ti, int &tj) {
@@ -412,9 +496,22 @@ __device__ __forceinline__ void tile_of_index(int t, int &ti, int &tj) {
   ti = t;
 }
 
-__device__ __forceinline__ double inverse_norm(double trace, double eps) {
-  const double d = sqrt(trace) + eps;
-  return d > 0.0 ? 1.0 / d : 0.0;          // a zero update stays zero
+template <int NT>
+__device__ __forceinline__ void put_tile(double *M, int ti, int tj, const f64x4_t &d) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) M[(NT * ti + tj) * 256 + 64 * r + lane] = d[r];
+  if (ti == tj) return;
+  // element (lane / 16 + 4 r, lane % 16) is (lane % 16, lane / 16 + 4 r) there
+  double *T = M + (NT * tj + ti) * 256 + 64 * ((lane & 15) >> 2) + 16 * (lane & 3) + (lane >> 4);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) T[4 * r] = d[r];
+}
+
+// Element (i, j) of a matrix of tiles.
+template <int NT>
+__device__ __forceinline__ double &element(double *M, int i, int j) {
+  return M[(NT * (i >> 4) + (j >> 4)) * 256 + 64 * ((i & 15) >> 2) + 16 * (i & 3) + (j & 15)];
 }
 
 template <int NT>
@@ -424,51 +521,39 @@ __global__ __launch_bounds__(Small<NT>::threads) void small_kernel(const MuonMat
   const MuonMat a = table[blockIdx.x];
   if ((a.k + 15) / 16 != NT) return;
   extern __shared__ __align__(16) double sq[];
+  __shared__ double diagonal[S::kp];
   double *G = sq, *P = sq + S::size, *Q = sq + 2 * S::size;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   double *area = ws + a.area;
   // (a tall matrix of 33 .. 48 columns has four tiles of partials: columns 4 c + t)
   const Block b = block_of(a.k, 0, a.wide);
-  for (int e = threadIdx.x; e < (NT == 1 ? 256 : kPairDoubles); e += S::threads) {
+  for (int e = threadIdx.x; e < kPairDoubles; e += S::threads) {
     const int ti = e >> 10, tj = (e >> 8) & 3;
     if (tj >= b.tiles || ti > tj) continue;
-    double v = 0.0;
-    if (NT == 1) {                         // one tile: its partials are summed here
-      for (int q = 0; q < a.splits; q += 8) {
-        double w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = q + i < a.splits ? area[int64_t(q + i) * kPairDoubles + e] : 0.0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v += w[i];
-      }
-    } else {
-      v = area[e];
-    }
+    const double v = area[e];
     const int i = column_of(b, a.wide, ti, ((e & 63) >> 4) + 4 * ((e >> 6) & 3));
     const int j = column_of(b, a.wide, tj, e & 15);
     if (i >= S::kp || j >= S::kp) continue;
-    G[i * S::pitch + j] = v;
-    if (ti < tj) G[j * S::pitch + i] = v;
+    element<NT>(G, i, j) = v;
+    if (ti < tj) element<NT>(G, j, i) = v;
+    if (i == j) diagonal[i] = v;
   }
   __syncthreads();
-  double trace = 0.0;
-  for (int i = 0; i < S::kp; ++i) trace += G[i * S::pitch + i];
-  const double inv = inverse_norm(trace, p.eps);
-  __syncthreads();
-  for (int e = threadIdx.x; e < S::kp * S::kp; e += S::threads) {
-    const int i = e / S::kp, j = e % S::kp;
-    G[i * S::pitch + j] *= inv * inv;
-    Q[i * S::pitch + j] = i == j ? inv : 0.0;
+  const double inv = inverse_norm(wave_sum(lane < S::kp ? diagonal[lane] : 0.0), p.eps);
+  for (int e = threadIdx.x; e < S::size; e += S::threads) {
+    G[e] *= inv * inv;
+    const int r = e >> 8;                                // its tile: NT ti + tj
+    const int i = 16 * (r / NT) + ((e & 63) >> 4) + 4 * ((e >> 6) & 3), j = 16 * (r % NT) + (e & 15);
+    Q[e] = i == j ? inv : 0.0;
   }
   __syncthreads();
   constexpr int per = (S::tiles + S::waves - 1) / S::waves;
   constexpr int both = (2 * S::tiles + S::waves - 1) / S::waves;
-  auto put = [&](double *M, int i, int j, double v, bool mirror) {
-    M[i * S::pitch + j] = v;
-    if (mirror) M[j * S::pitch + i] = v;
-  };
+  f64x4_t I;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) I[r] = (lane >> 4) + 4 * r == (lane & 15) ? 1.0 : 0.0;
   for (int it = 0; it < p.steps; ++it) {
-    f64x4_t d[both];
+    f64x4_t d[both], s[per];
     // S = G G
 #pragma unroll
     for (int q = 0; q < per; ++q) {
@@ -476,23 +561,21 @@ __global__ __launch_bounds__(Small<NT>::threads) void small_kernel(const MuonMat
       if (t >= S::tiles) break;
       int ti, tj;
       tile_of_index(t, ti, tj);
-      d[q] = lds_product<NT>(G, G, ti, tj);
-      each(ti, tj, [&](int i, int j, int r) { put(P, i, j, d[q][r], ti < tj); });
+      s[q] = lds_product<NT>(G, G, ti, tj);
+      put_tile<NT>(P, ti, tj, s[q]);
     }
     __syncthreads();
     // H = G P = a G + b S + c G S in G's place, P = a I + b G + c S in S's
-    double g[per][4], s[per][4];
+    f64x4_t g[per];
 #pragma unroll
     for (int q = 0; q < per; ++q) {
       const int t = wave + q * S::waves;
       if (t >= S::tiles) break;
       int ti, tj;
       tile_of_index(t, ti, tj);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) g[q][r] = G[(NT * ti + tj) * 256 + 64 * r + lane];
       d[q] = lds_product<NT>(G, P, ti, tj);
-      each(ti, tj, [&](int i, int j, int r) {
-        g[q][r] = G[i * S::pitch + j];
-        s[q][r] = P[i * S::pitch + j];
-      });
     }
     __syncthreads();
 #pragma unroll
@@ -501,81 +584,59 @@ __global__ __launch_bounds__(Small<NT>::threads) void small_kernel(const MuonMat
       if (t >= S::tiles) break;
       int ti, tj;
       tile_of_index(t, ti, tj);
-      each(ti, tj, [&](int i, int j, int r) {
-        put(G, i, j, p.a * g[q][r] + p.b * s[q][r] + p.c * d[q][r], ti < tj);
-        put(P, i, j, (i == j ? p.a : 0.0) + p.b * g[q][r] + p.c * s[q][r], ti < tj);
-      });
+      put_tile<NT>(G, ti, tj, p.a * g[q] + p.b * s[q] + p.c * d[q]);
+      put_tile<NT>(P, ti, tj, (ti == tj ? p.a : 0.0) * I + p.b * g[q] + p.c * s[q]);
     }
     __syncthreads();
     // G <- H P and Q <- Q P; the last time Q alone
-    const bool last = it + 1 == p.steps;
+    const int units = (it + 1 == p.steps ? 1 : 2) * S::tiles;
 #pragma unroll
     for (int q = 0; q < both; ++q) {
       const int t = wave + q * S::waves;
-      if (t >= (last ? 1 : 2) * S::tiles) break;
+      if (t >= units) break;
       int ti, tj;
-      tile_of_index(t % S::tiles, ti, tj);
+      tile_of_index(t < S::tiles ? t : t - S::tiles, ti, tj);
       d[q] = lds_product<NT>(t < S::tiles ? Q : G, P, ti, tj);
     }
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < both; ++q) {
       const int t = wave + q * S::waves;
-      if (t >= (last ? 1 : 2) * S::tiles) break;
+      if (t >= units) break;
       int ti, tj;
-      tile_of_index(t % S::tiles, ti, tj);
-      each(ti, tj, [&](int i, int j, int r) { put(t < S::tiles ? Q : G, i, j, d[q][r], ti < tj); });
+      tile_of_index(t < S::tiles ? t : t - S::tiles, ti, tj);
+      put_tile<NT>(t < S::tiles ? Q : G, ti, tj, d[q]);
     }
     __syncthreads();
   }
-  for (int e = threadIdx.x; e < S::kp * S::kp; e += S::threads)
-    area[e] = Q[e / S::kp * S::pitch + e % S::kp];
+  for (int e = threadIdx.x; e < S::size; e += S::threads)
+    area[e] = element<NT>(Q, e / S::kp, e % S::kp);
 }
 
 // ------------------------------------------------ k x k iterations, k > 64
 //
-// The matrices (kp x kp, row-major) follow each other in the matrix's area: G,
-// S, H, P, Q, Q'.  A workgroup owns one 16 x 16 tile of the upper triangle of a
+// A workgroup owns one 16 x 16 tile of the upper triangle of a
 // product, its four wavefronts a quarter of the sum each; operands come from
 // L2 (both symmetric, so every fragment is four runs of 128 bytes).
 enum MuonStage { kSquare, kPolynomial, kAdvance };
 
-struct Slots {
-  double *G, *S, *H, *P, *Q0, *Q1;
-  __device__ __forceinline__ Slots(double *area, int kp) {
-    const int64_t n = int64_t(kp) * kp;
-    G = area + int64_t(pairs_of(kp)) * kPairDoubles;   // past the summed partials
-    S = G + n;
-    H = S + n;
-    P = H + n;
-    Q0 = P + n;
-    Q1 = Q0 + n;
+// A quarter of the operands of a tile of columns 16 t ..: kp / 16 steps of four
+// rows, all requested before the first is used (past them the last ones again,
+// which the products leave out).
+struct Quarter {
+  double v[16];
+  __device__ __forceinline__ Quarter(const double *M, int kp, int t, int wave) {
+    const int lane = threadIdx.x & 63, steps = kp / 16;
+    const double *x = M + int64_t(4 * wave * steps + (lane >> 4)) * kp + 16 * t + (lane & 15);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = x[4 * (i < steps ? i : steps - 1) * kp];
   }
-  __device__ __forceinline__ double *Q(int i) const { return i & 1 ? Q1 : Q0; }
 };
 
-// A quarter of the sum of tile (ti, tj) of A B.  All operands are requested
-// before the first product (steps past the quarter's end read its last rows).
-__device__ __forceinline__ f64x4_t part_product(const double *A, const double *B, int kp, int ti,
-                                                int tj, int wave) {
-  const int lane = threadIdx.x & 63;
-  const int steps = kp / 16;               // of four rows, a quarter of kp / 4
-  const int64_t at = int64_t(4 * wave * steps + (lane >> 4)) * kp + (lane & 15);
-  const double *x = A + at + 16 * ti, *y = B + at + 16 * tj;
+__device__ __forceinline__ f64x4_t part_product(const Quarter &a, const Quarter &b, int kp) {
   f64x4_t d = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-  for (int h = 0; h < 16; h += 8) {
-    if (h >= steps) break;
-    double u[8], v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int q = h + i < steps ? h + i : steps - 1;
-      u[i] = x[4 * q * kp];
-      v[i] = y[4 * q * kp];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) d = mfma64(h + i < steps ? u[i] : 0.0, v[i], d);
-  }
+  for (int i = 0; i < 16; ++i) d = mfma64(i < kp / 16 ? a.v[i] : 0.0, b.v[i], d);
   return d;
 }
 
@@ -592,25 +653,6 @@ __device__ __forceinline__ double joined_part(f64x4_t d, int wave, double (*red)
   return s;
 }
 
-// The summed partials of a block pair into G, both ways round.
-__global__ __launch_bounds__(256) void unpack_kernel(const MuonMat *table, double *ws) {
-  const MuonMat a = table[blockIdx.z];
-  if (a.k <= 64 || int(blockIdx.y) >= pairs_of(a.k)) return;
-  const int kp = padded(a.k), ti = int(blockIdx.x) >> 2, tj = int(blockIdx.x) & 3;
-  int bi, bj;
-  pair_of(int(blockIdx.y), bi, bj);
-  const Block b = block_of(a.k, bi, a.wide), c = block_of(a.k, bj, a.wide);
-  if (ti >= b.tiles || tj >= c.tiles || (bi == bj && ti > tj)) return;
-  const int e = threadIdx.x;
-  const int i = column_of(b, a.wide, ti, ((e & 63) >> 4) + 4 * (e >> 6));
-  const int j = column_of(c, a.wide, tj, e & 15);
-  if (i >= kp || j >= kp) return;
-  const double v = ws[a.area + int64_t(blockIdx.y) * kPairDoubles + int(blockIdx.x) * 256 + e];
-  double *G = Slots(ws + a.area, kp).G;
-  G[int64_t(i) * kp + j] = v;
-  G[int64_t(j) * kp + i] = v;
-}
-
 __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonParams p, double *ws,
                                                     int stage, int it) {
   __shared__ double red[2][4][4][64];
@@ -622,7 +664,7 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   int ti, tj;
   tile_of_index(t, ti, tj);
-  const Slots m(ws + a.area, kp);
+  const Slots m(ws + a.area, a.splits, kp);
   const int i = 16 * ti + (lane >> 4) + 4 * wave, j = 16 * tj + (lane & 15);
   const int64_t ij = int64_t(i) * kp + j, ji = int64_t(j) * kp + i;
   auto put = [&](double *M, double v) {
@@ -630,11 +672,12 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
     if (ti < tj) M[ji] = v;
   };
   if (stage == kSquare) {
-    put(m.S, joined_part(part_product(m.G, m.G, kp, ti, tj, wave), wave, red[0]));
+    const Quarter x(m.G, kp, ti, wave), y(m.G, kp, tj, wave);
+    put(m.S, joined_part(part_product(x, y, kp), wave, red[0]));
     return;
   }
-  const double *q = m.Q(it);
   if (stage == kPolynomial) {
+    const Quarter x(m.G, kp, ti, wave), y(m.S, kp, tj, wave);
     // the first G is not yet scaled: its powers take the factor here
     double f = 1.0, inv = 1.0;
     if (it == 0) {
@@ -656,14 +699,15 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
     if (!last)
       put(m.H, p.a * g + p.b * s +
                    p.c * (f * f * f *
-                          joined_part(part_product(m.G, m.S, kp, ti, tj, wave), wave, red[0])));
+                          joined_part(part_product(x, y, kp), wave, red[0])));
     return;
   }
   // kAdvance: G <- H P (but the last time) and, past the first, Q' = Q P
-  if (it + 1 < p.steps)
-    put(m.G, joined_part(part_product(m.H, m.P, kp, ti, tj, wave), wave, red[0]));
-  if (it > 0)
-    put(m.Q(it + 1), joined_part(part_product(q, m.P, kp, ti, tj, wave), wave, red[1]));
+  const Quarter y(m.P, kp, tj, wave);
+  const Quarter h(it + 1 < p.steps ? m.H : m.P, kp, ti, wave);
+  const Quarter x(it > 0 ? m.Q(it) : m.P, kp, ti, wave);
+  if (it + 1 < p.steps) put(m.G, joined_part(part_product(h, y, kp), wave, red[0]));
+  if (it > 0) put(m.Q(it + 1), joined_part(part_product(x, y, kp), wave, red[1]));
 }
 
 // ------------------------------------------------------------ the update
@@ -700,17 +744,56 @@ __device__ __forceinline__ void update_run(const MuonMat &a, const MuonParams &p
   }
 }
 
-// k <= 64: Q in LDS, a wavefront to 16 long rows (tall) or 32 (wide) at a time,
-// no barrier between them.
+// k <= 64: a wavefront to 16 long rows (tall) or 32 (wide) at a time, no barrier
+// between them; Q is in LDS, or of k <= 32 in registers.
 //   tall: lane (g, c) loads columns 16 j + 4 g .. + 3 of row c, the operands of
 //     four products; tile t has columns NT c + t.
 //   wide: lane (g, c) loads long rows 2 c, 2 c + 1 of column 4 s + g, the operands
 //     of two tiles; a result's rows are short.
-constexpr int kApplyRows = 256;              // long rows to a workgroup
+// Long rows to a workgroup: what makes up for reading Q.
+constexpr int apply_rows(int NT) { return NT == 1 ? 128 : 256; }
+
+// A lane's Q: row 16 j + 4 g + e, columns NT c .. (tall), or row 4 s + g, columns
+// c, 16 + c .. (wide), as the products ask for them.
+template <int NT>
+struct Factor {
+  static constexpr bool held = NT <= 2;
+  static constexpr int K = 16 * NT, pitch = K + 2;
+  double v[held ? 4 * NT : 1][held ? NT : 1];
+  const double *lds;
+  template <bool WIDE>
+  __device__ __forceinline__ void init(const double *q, int kp, double *shared) {
+    if constexpr (held) {
+      const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+#pragma unroll
+      for (int s = 0; s < 4 * NT; ++s)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int row = WIDE ? 4 * s + g : 16 * (s / 4) + 4 * g + s % 4;
+          v[s][t] = q[row * kp + (WIDE ? 16 * t + c : NT * c + t)];   // (kp = K here)
+        }
+    } else {
+      for (int e = threadIdx.x; e < K * K; e += 256) {
+        const int i = e / K, j = e % K;
+        shared[i * pitch + j] = i < kp && j < kp ? q[i * kp + j] : 0.0;
+      }
+      lds = shared;
+      __syncthreads();
+    }
+  }
+  // of product s (tall: s = 4 j + e)
+  template <bool WIDE>
+  __device__ __forceinline__ double at(int s, int t) const {
+    if constexpr (held) return v[s][t];
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    return WIDE ? lds[(4 * s + g) * pitch + 16 * t + c]
+                : lds[(16 * (s / 4) + 4 * g + s % 4) * pitch + NT * c + t];
+  }
+};
 
 template <int NT, bool Q>
-__device__ __forceinline__ void apply_tall(const MuonMat &a, const MuonParams &p, const double *Qs,
-                                           int pitch, int64_t r, int64_t end) {
+__device__ __forceinline__ void apply_tall(const MuonMat &a, const MuonParams &p,
+                                           const Factor<NT> &f, int64_t r, int64_t end) {
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const bool has_m = a.m != nullptr, read_g = !has_m || p.nesterov;
   Run<4> gr[NT], m[NT];
@@ -738,9 +821,8 @@ __device__ __forceinline__ void apply_tall(const MuonMat &a, const MuonParams &p
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const double u = double(direction<false>(p, has_m, gr[j].v[e], m[j].v[e]));
-      const double *y = Qs + (16 * j + 4 * g + e) * pitch + NT * c;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) d[t] = mfma64(u, y[t], d[t]);
+      for (int t = 0; t < NT; ++t) d[t] = mfma64(u, f.template at<false>(4 * j + e, t), d[t]);
     }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -752,8 +834,8 @@ __device__ __forceinline__ void apply_tall(const MuonMat &a, const MuonParams &p
 }
 
 template <int NT, bool Q>
-__device__ __forceinline__ void apply_wide(const MuonMat &a, const MuonParams &p, const double *Qs,
-                                           int pitch, int64_t r, int64_t end) {
+__device__ __forceinline__ void apply_wide(const MuonMat &a, const MuonParams &p,
+                                           const Factor<NT> &f, int64_t r, int64_t end) {
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const bool has_m = a.m != nullptr, read_g = !has_m || p.nesterov;
   const int along = clamped(end - r - 2 * c, 2);
@@ -775,13 +857,12 @@ __device__ __forceinline__ void apply_wide(const MuonMat &a, const MuonParams &p
   }
 #pragma unroll
   for (int s = 0; s < 4 * NT; ++s) {
-    const double *y = Qs + (4 * s + g) * pitch + c;
     double u[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) u[e] = double(direction<false>(p, has_m, gr[s].v[e], m[s].v[e]));
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const double w = y[16 * t];
+      const double w = f.template at<true>(s, t);
 #pragma unroll
       for (int e = 0; e < 2; ++e) d[t][e] = mfma64(w, u[e], d[t][e]);
     }
@@ -800,26 +881,21 @@ __device__ __forceinline__ void apply_wide(const MuonMat &a, const MuonParams &p
 template <int NT, bool ALIGNED>
 __global__ __launch_bounds__(256, 2) void apply_kernel(const MuonMat *table, MuonParams p,
                                                     const double *ws) {
-  constexpr int K = 16 * NT, pitch = K + 2;
-  __shared__ __align__(16) double Q[K * pitch];
+  using F = Factor<NT>;
+  __shared__ __align__(16) double shared[F::held ? 1 : F::K * F::pitch];
   const MuonMat a = table[blockIdx.y];
   const int kp = padded(a.k);
-  const int64_t from = int64_t(blockIdx.x) * kApplyRows;
-  if (from >= a.n || kp > K || (NT > 1 && kp <= K / 2) || bool(a.quads) != ALIGNED) return;
-  const int64_t end = from + kApplyRows < a.n ? from + kApplyRows : a.n;
-  const double *q = ws + a.area;
-  for (int e = threadIdx.x; e < K * K; e += 256) {
-    const int i = e / K, j = e % K;
-    Q[i * pitch + j] = i < kp && j < kp ? q[i * kp + j] : 0.0;
-  }
-  __syncthreads();
+  const int64_t from = int64_t(blockIdx.x) * apply_rows(NT);
+  if (from >= a.n || kp > F::K || (NT > 1 && kp <= F::K / 2) || bool(a.quads) != ALIGNED) return;
+  const int64_t end = from + apply_rows(NT) < a.n ? from + apply_rows(NT) : a.n;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  F f;
   if (a.wide) {
-    for (int64_t r = from + 32 * wave; r < end; r += 128)
-      apply_wide<NT, ALIGNED>(a, p, Q, pitch, r, end);
+    f.template init<true>(ws + a.area, kp, shared);
+    for (int64_t r = from + 32 * wave; r < end; r += 128) apply_wide<NT, ALIGNED>(a, p, f, r, end);
   } else {
-    for (int64_t r = from + 16 * wave; r < end; r += 64)
-      apply_tall<NT, ALIGNED>(a, p, Q, pitch, r, end);
+    f.template init<false>(ws + a.area, kp, shared);
+    for (int64_t r = from + 16 * wave; r < end; r += 64) apply_tall<NT, ALIGNED>(a, p, f, r, end);
   }
 }
 
@@ -908,14 +984,13 @@ __device__ __forceinline__ void large_block(const MuonMat &a, const MuonParams &
 
 // u of 64 long rows into LDS, four values of a lane at a time along memory.
 template <bool WIDE, bool Q, int threads>
-__device__ __forceinline__ void stage_rows(const MuonMat &a, const MuonParams &p, int64_t from,
-                                           int kp, int pitch, float *us) {
-  const bool has_m = a.m != nullptr, read_g = !has_m || p.nesterov;
+__device__ __forceinline__ void stage_rows(const MuonMat &a, int64_t from, int kp, int pitch,
+                                           float *us) {
   const int per = WIDE ? kLargeRows / 4 : (a.k + 3) / 4;         // runs of a memory row
   const int items = WIDE ? a.k * per : kLargeRows * per;
   const uint32_t inv = 0xffffffffu / uint32_t(per) + 1u;         // e / per for e < 2^16
   for (int e0 = threadIdx.x; e0 < items; e0 += 4 * threads) {
-    Run<4> gr[4], m[4];
+    Run<4> u[4];
     int slot[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -925,8 +1000,7 @@ __device__ __forceinline__ void stage_rows(const MuonMat &a, const MuonParams &p
       // (255 n + 63 and 64 k fit 32 bits)
       const Place at = WIDE ? Place{from, uint32_t(hi) * uint32_t(a.n) + lo}
                             : Place{from * a.k, uint32_t(hi * a.k + lo)};
-      gr[i] = read_g ? load_run<Q, 4>(a.grad, at, live) : Run<4>{};
-      m[i] = has_m ? load_run<Q, 4>(a.m, at, live) : Run<4>{};
+      u[i] = load_run<Q, 4>(a.u, at, live);
       slot[i] = e >= items ? -1 : WIDE ? lo * pitch + hi : hi * pitch + lo;
     }
 #pragma unroll
@@ -934,7 +1008,7 @@ __device__ __forceinline__ void stage_rows(const MuonMat &a, const MuonParams &p
       if (slot[i] < 0) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        us[slot[i] + e * (WIDE ? pitch : 1)] = direction<false>(p, has_m, gr[i].v[e], m[i].v[e]);
+        us[slot[i] + e * (WIDE ? pitch : 1)] = u[i].v[e];
     }
   }
   // the columns past k (a tall row's last run has filled some)
@@ -944,7 +1018,7 @@ __device__ __forceinline__ void stage_rows(const MuonMat &a, const MuonParams &p
 }
 
 template <int NB>
-__global__ __launch_bounds__(64 * NB) void apply_large_kernel(const MuonMat *table, MuonParams p,
+__global__ __launch_bounds__(64 * NB, 2) void apply_large_kernel(const MuonMat *table, MuonParams p,
                                                               double *ws) {
   extern __shared__ __align__(16) float us[];
   const MuonMat a = table[blockIdx.y];
@@ -952,11 +1026,11 @@ __global__ __launch_bounds__(64 * NB) void apply_large_kernel(const MuonMat *tab
   if (from >= a.n || (a.k + 63) / 64 != NB) return;
   const int kp = padded(a.k), pitch = large_pitch(kp);
   const int first = 64 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const double *q = Slots(ws + a.area, kp).Q(p.steps) + first;
+  const double *q = Slots(ws + a.area, a.splits, kp).Q(p.steps) + first;
   with_bool(a.wide, [&](auto W) {
     constexpr bool wide = decltype(W)::value;
     with_bool(a.quads, [&](auto A) {
-      stage_rows<wide, decltype(A)::value, 64 * NB>(a, p, from, kp, pitch, us);
+      stage_rows<wide, decltype(A)::value, 64 * NB>(a, from, kp, pitch, us);
     });
     __syncthreads();
     with_tiles((kp - first) / 16, [&](auto T) {
@@ -973,7 +1047,7 @@ bool raise_lds(F *f, int bytes) {
 
 // A matrix of a call: span0 as muon_span gives it for the call, o the doubles
 // of the workspace that the matrices before it take.
-MuonMat planned(const qlora_muon_mat &q, int64_t span0, int64_t &o) {
+MuonMat planned(const qlora_muon_mat &q, int64_t span0, bool nesterov, double *ws, int64_t &o) {
   MuonMat a{};
   a.grad = q.grad;
   a.m = q.m;
@@ -994,8 +1068,12 @@ MuonMat planned(const qlora_muon_mat &q, int64_t span0, int64_t &o) {
   a.splits = int32_t((a.n + a.span - 1) / a.span);
   a.area = o;
   const int64_t first = int64_t(pairs_of(a.k)) * kPairDoubles, sq = int64_t(kp) * kp;
-  const int64_t squares = a.k <= 64 ? sq : first + 6 * sq;
-  o += squares > a.splits * first ? squares : a.splits * first;
+  o += a.splits * first;
+  if (a.k > 64) {
+    o += 6 * sq;
+    a.u = !a.m ? a.grad : nesterov ? reinterpret_cast<const float *>(ws + o) : a.m;
+    o += (a.n * a.k + 3) / 4 * 2;
+  }
   return a;
 }
 
@@ -1014,7 +1092,7 @@ size_t table_bytes(int32_t n) { return (size_t(n) * sizeof(MuonMat) + 255) / 256
 size_t muon_workspace_bytes(const qlora_muon_mat *mats, int32_t n) {
   const int64_t span = muon_span(mats, n);
   int64_t o = 0;
-  for (int32_t i = 0; i < n; ++i) (void)planned(mats[i], span, o);
+  for (int32_t i = 0; i < n; ++i) (void)planned(mats[i], span, false, nullptr, o);
   return table_bytes(n) + size_t(o) * sizeof(double);
 }
 
@@ -1034,13 +1112,14 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
     c.count = n - i < kMuonChunk ? n - i : kMuonChunk;
     c.first = i;
     for (int j = 0; j < c.count; ++j) {
-      const MuonMat a = c.mats[j] = planned(mats[i + j], span, o);
+      const MuonMat a = c.mats[j] = planned(mats[i + j], span, p.nesterov, ws, o);
       most_k = a.k > most_k ? a.k : most_k;
       const int kp = padded(a.k);
       if (a.k <= 64) {
         small[kp / 16] = true;
         raise(splits[a.quads], a.splits);
-        raise(blocks[a.quads][kp <= 16 ? 1 : kp <= 32 ? 2 : 4], (a.n + kApplyRows - 1) / kApplyRows);
+        const int NT = kp <= 16 ? 1 : kp <= 32 ? 2 : 4;
+        raise(blocks[a.quads][NT], (a.n + apply_rows(NT) - 1) / apply_rows(NT));
       } else {
         raise(splits_large[a.quads], a.splits);
         raise(blocks_large[(a.k + 63) / 64], (a.n + kLargeRows - 1) / kLargeRows);
@@ -1072,7 +1151,8 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
     hipLaunchKernelGGL((small_kernel<NT>), dim3(unsigned(n)), dim3(Small<NT>::threads), \
                        Small<NT>::bytes, s, table, p, ws);                              \
   }
-  QLORA_SMALL(1)
+  if (small[1])
+    hipLaunchKernelGGL(tiny_kernel, dim3(unsigned(n)), dim3(256), 0, s, table, p, ws);
   QLORA_SMALL(2)
   QLORA_SMALL(3)
   QLORA_SMALL(4)
@@ -1083,7 +1163,6 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
     auto go = [&](int stage, int it) {
       hipLaunchKernelGGL(stage_kernel, tiles, dim3(256), 0, s, table, p, ws, stage, it);
     };
-    hipLaunchKernelGGL(unpack_kernel, pairs, dim3(256), 0, s, table, ws);
     for (int it = 0; it < p.steps; ++it) {
       go(kSquare, it);
       go(kPolynomial, it);
