@@ -481,12 +481,17 @@ template <int NT>
 __device__ __forceinline__ f64x4_t lds_product(const double *A, const double *B, int ti, int tj) {
   const int lane = threadIdx.x & 63;
   const double *x = A + ti * 256 + lane, *y = B + tj * 256 + lane;
+  // all operands requested first: left to itself the compiler waits for each pair
+  double u[4 * NT], v[4 * NT];
+#pragma unroll
+  for (int s = 0; s < 4 * NT; ++s) {
+    u[s] = x[s / 4 * NT * 256 + 64 * (s % 4)];
+    v[s] = y[s / 4 * NT * 256 + 64 * (s % 4)];
+  }
+  __builtin_amdgcn_sched_barrier(0);
   f64x4_t d = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-  for (int k = 0; k < NT; ++k)
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-      d = mfma64(x[k * NT * 256 + 64 * s], y[k * NT * 256 + 64 * s], d);
+  for (int s = 0; s < 4 * NT; ++s) d = mfma64(u[s], v[s], d);
   return d;
 }
 
@@ -653,14 +658,37 @@ __device__ __forceinline__ double joined_part(f64x4_t d, int wave, double (*red)
   return s;
 }
 
+// A matrix's tiles are dealt to as few of the 8 XCDs as fill the chip (workgroups
+// go round them), so that each L2 fetches only its own matrices: matrix m is on
+// XCD m % 8, or on 8 / n neighbouring ones where there are fewer than 8.
+__device__ __forceinline__ void stage_job(int n, int tiles, int &which, int &t) {
+  const int x = int(blockIdx.x) % 8, slot = int(blockIdx.x) / 8;
+  if (n >= 8) {
+    which = x + 8 * (slot / tiles);
+    t = slot % tiles;
+  } else {
+    const int per = 8 / n;
+    which = x / per;
+    t = slot * per + x % per;
+  }
+}
+int64_t stage_grid(int64_t n, int64_t tiles) {
+  return n >= 8 ? 8 * tiles * ((n + 7) / 8) : 8 * ((tiles + 8 / n - 1) / (8 / n));
+}
+
 __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonParams p, double *ws,
-                                                    int stage, int it) {
-  __shared__ double red[2][4][4][64];
+                                                    int stage, int it, int n, int tiles) {
+  __shared__ double red[4][4][64];
   __shared__ double norm;
-  const MuonMat a = table[blockIdx.y];
+  int which, t;
+  stage_job(n, tiles, which, t);
+  if (which >= n || t >= tiles) return;
+  const MuonMat a = table[which];
   if (a.k <= 64) return;
-  const int kp = padded(a.k), NT = kp / 16, t = int(blockIdx.x);
-  if (t >= NT * (NT + 1) / 2) return;
+  const int kp = padded(a.k), NT = kp / 16;
+  const bool second = t >= NT * (NT + 1) / 2;              // (kAdvance: the other product)
+  if (second) t -= NT * (NT + 1) / 2;
+  if (t >= NT * (NT + 1) / 2 || (second && stage != kAdvance)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   int ti, tj;
   tile_of_index(t, ti, tj);
@@ -673,7 +701,7 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
   };
   if (stage == kSquare) {
     const Quarter x(m.G, kp, ti, wave), y(m.G, kp, tj, wave);
-    put(m.S, joined_part(part_product(x, y, kp), wave, red[0]));
+    put(m.S, joined_part(part_product(x, y, kp), wave, red));
     return;
   }
   if (stage == kPolynomial) {
@@ -699,15 +727,13 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
     if (!last)
       put(m.H, p.a * g + p.b * s +
                    p.c * (f * f * f *
-                          joined_part(part_product(x, y, kp), wave, red[0])));
+                          joined_part(part_product(x, y, kp), wave, red)));
     return;
   }
-  // kAdvance: G <- H P (but the last time) and, past the first, Q' = Q P
-  const Quarter y(m.P, kp, tj, wave);
-  const Quarter h(it + 1 < p.steps ? m.H : m.P, kp, ti, wave);
-  const Quarter x(it > 0 ? m.Q(it) : m.P, kp, ti, wave);
-  if (it + 1 < p.steps) put(m.G, joined_part(part_product(h, y, kp), wave, red[0]));
-  if (it > 0) put(m.Q(it + 1), joined_part(part_product(x, y, kp), wave, red[1]));
+  // kAdvance: G <- H P (but the last time) or, past the first, Q' = Q P
+  if (second ? it == 0 : it + 1 == p.steps) return;
+  const Quarter x(second ? m.Q(it) : m.H, kp, ti, wave), y(m.P, kp, tj, wave);
+  put(second ? m.Q(it + 1) : m.G, joined_part(part_product(x, y, kp), wave, red));
 }
 
 // ------------------------------------------------------------ the update
@@ -761,6 +787,11 @@ struct Factor {
   static constexpr int K = 16 * NT, pitch = K + 2;
   double v[held ? 4 * NT : 1][held ? NT : 1];
   const double *lds;
+  // Between two uses: or the compiler keeps what it has read from LDS, twice the
+  // registers of everything else.
+  __device__ __forceinline__ void again() {
+    if constexpr (!held) asm volatile("" : "+v"(lds));
+  }
   template <bool WIDE>
   __device__ __forceinline__ void init(const double *q, int kp, double *shared) {
     if constexpr (held) {
@@ -816,14 +847,19 @@ __device__ __forceinline__ void apply_tall(const MuonMat &a, const MuonParams &p
   f64x4_t d[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) d[t] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+  double y[2][NT];                             // a product's Q, and the next one's
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int t = 0; t < NT; ++t) y[0][t] = f.template at<false>(0, t);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const double u = double(direction<false>(p, has_m, gr[j].v[e], m[j].v[e]));
+  for (int s = 0; s < 4 * NT; ++s) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) d[t] = mfma64(u, f.template at<false>(4 * j + e, t), d[t]);
-    }
+    for (int t = 0; t < NT; ++t)
+      if (s + 1 < 4 * NT) y[(s + 1) & 1][t] = f.template at<false>(s + 1, t);
+    if (!Factor<NT>::held) __builtin_amdgcn_sched_barrier(0);
+    const double u = double(direction<false>(p, has_m, gr[s / 4].v[s % 4], m[s / 4].v[s % 4]));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) d[t] = mfma64(u, y[s & 1][t], d[t]);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     Run<NT> x;
@@ -847,25 +883,37 @@ __device__ __forceinline__ void apply_wide(const MuonMat &a, const MuonParams &p
     return Place{(4 * s < a.k ? 4 * s : 0) * a.n + r, uint32_t(g * a.n) + 2 * c};
   };
   auto live_of = [&](int s) { return 4 * s + g < a.k ? along : 0; };
-  Run<2> gr[4 * NT], m[4 * NT];
+  // four products' operands in hand, four on their way
+  Run<2> gr[2][4], m[2][4];
+  auto request = [&](int at, int s0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Place where = place(s0 + i);
+      const int live = live_of(s0 + i);
+      gr[at][i] = read_g ? load_run<Q, 2>(a.grad, where, live) : Run<2>{};
+      m[at][i] = has_m ? load_run<Q, 2>(a.m, where, live) : Run<2>{};
+    }
+  };
+  request(0, 0);
+  double y[2][NT];                             // a product's Q, and the next one's
+#pragma unroll
+  for (int t = 0; t < NT; ++t) y[0][t] = f.template at<true>(0, t);
 #pragma unroll
   for (int s = 0; s < 4 * NT; ++s) {
-    const Place at = place(s);
-    const int live = live_of(s);
-    gr[s] = read_g ? load_run<Q, 2>(a.grad, at, live) : Run<2>{};
-    m[s] = has_m ? load_run<Q, 2>(a.m, at, live) : Run<2>{};
-  }
+    const int j = s / 4, i = s % 4;
+    if (i == 0 && j + 1 < NT) request((j + 1) & 1, 4 * (j + 1));
 #pragma unroll
-  for (int s = 0; s < 4 * NT; ++s) {
+    for (int t = 0; t < NT; ++t)
+      if (s + 1 < 4 * NT) y[(s + 1) & 1][t] = f.template at<true>(s + 1, t);
+    if (!Factor<NT>::held) __builtin_amdgcn_sched_barrier(0);
     double u[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) u[e] = double(direction<false>(p, has_m, gr[s].v[e], m[s].v[e]));
+    for (int e = 0; e < 2; ++e)
+      u[e] = double(direction<false>(p, has_m, gr[j & 1][i].v[e], m[j & 1][i].v[e]));
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const double w = f.template at<true>(s, t);
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) d[t][e] = mfma64(w, u[e], d[t][e]);
-    }
+      for (int e = 0; e < 2; ++e) d[t][e] = mfma64(y[s & 1][t], u[e], d[t][e]);
   }
   Run<2> th[4 * NT];
 #pragma unroll
@@ -879,7 +927,7 @@ __device__ __forceinline__ void apply_wide(const MuonMat &a, const MuonParams &p
 }
 
 template <int NT, bool ALIGNED>
-__global__ __launch_bounds__(256, 2) void apply_kernel(const MuonMat *table, MuonParams p,
+__global__ __launch_bounds__(256) void apply_kernel(const MuonMat *table, MuonParams p,
                                                     const double *ws) {
   using F = Factor<NT>;
   __shared__ __align__(16) double shared[F::held ? 1 : F::K * F::pitch];
@@ -892,10 +940,12 @@ __global__ __launch_bounds__(256, 2) void apply_kernel(const MuonMat *table, Muo
   F f;
   if (a.wide) {
     f.template init<true>(ws + a.area, kp, shared);
-    for (int64_t r = from + 32 * wave; r < end; r += 128) apply_wide<NT, ALIGNED>(a, p, f, r, end);
+    for (int64_t r = from + 32 * wave; r < end; r += 128, f.again())
+      apply_wide<NT, ALIGNED>(a, p, f, r, end);
   } else {
     f.template init<false>(ws + a.area, kp, shared);
-    for (int64_t r = from + 16 * wave; r < end; r += 64) apply_tall<NT, ALIGNED>(a, p, f, r, end);
+    for (int64_t r = from + 16 * wave; r < end; r += 64, f.again())
+      apply_tall<NT, ALIGNED>(a, p, f, r, end);
   }
 }
 
@@ -950,8 +1000,10 @@ __device__ __forceinline__ void large_block(const MuonMat &a, const MuonParams &
   request(0, 0);
   for (int s = 0; s < kp / 4; s += 4) {
     request(2, s + 2);
+    __builtin_amdgcn_sched_barrier(0);
     multiply(0);
     request(0, s + 4);
+    __builtin_amdgcn_sched_barrier(0);
     multiply(2);
   }
 #pragma unroll
@@ -1062,8 +1114,10 @@ MuonMat planned(const qlora_muon_mat &q, int64_t span0, bool nesterov, double *w
   a.quads = (a.wide ? a.n : int64_t(a.k)) % 4 == 0 && ok(a.grad, 16) && ok(a.m, 16) &&
             ok(a.theta, 16) && ok(a.theta16, 8) && ok(a.update, 16);
   const int kp = padded(a.k);
-  // a slab's k x k partial sums stay a small part of what it reads
-  const int64_t span = span0 < kp / 2 ? kp / 2 : span0;
+  // a slab's k x k partial sums stay a small part of what it reads; of k > 64 a
+  // slab is a workgroup to every pair of blocks
+  const int64_t most = a.k <= 64 ? span0 : span0 * pairs_of(a.k) / 2;
+  const int64_t span = most < kp / 2 ? kp / 2 : most;
   a.span = (span + kGramRows - 1) / kGramRows * kGramRows;
   a.splits = int32_t((a.n + a.span - 1) / a.span);
   a.area = o;
@@ -1159,9 +1213,11 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
 #undef QLORA_SMALL
   if (most_k > 64) {
     const int NT = (most_k + 15) / 16;
-    const dim3 tiles(unsigned(NT * (NT + 1) / 2), unsigned(n));
+    const int tiles = NT * (NT + 1) / 2;
     auto go = [&](int stage, int it) {
-      hipLaunchKernelGGL(stage_kernel, tiles, dim3(256), 0, s, table, p, ws, stage, it);
+      const int jobs = stage == kAdvance ? 2 * tiles : tiles;
+      hipLaunchKernelGGL(stage_kernel, dim3(unsigned(stage_grid(n, jobs))), dim3(256), 0, s, table, p,
+                         ws, stage, it, n, jobs);
     };
     for (int it = 0; it < p.steps; ++it) {
       go(kSquare, it);
