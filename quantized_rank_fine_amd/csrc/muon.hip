@@ -418,6 +418,14 @@ __device__ __forceinline__ f64x4_t tile_product(const f64x4_t &a, const f64x4_t 
   return d;
 }
 
+// x + b y + c z.
+__device__ __forceinline__ f64x4_t combined(f64x4_t x, double b, const f64x4_t &y, double c,
+                                            const f64x4_t &z) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) x[r] = __builtin_fma(c, z[r], __builtin_fma(b, y[r], x[r]));
+  return x;
+}
+
 // 1 / (|u| + eps) from |u|^2; a zero update stays zero.
 __device__ __forceinline__ double inverse_norm(double trace, double eps) {
   const double d = sqrt(trace) + eps;
@@ -454,9 +462,9 @@ __global__ __launch_bounds__(256) void tiny_kernel(const MuonMat *table, MuonPar
   Q = I * inv;
   for (int it = 0; it < p.steps; ++it) {
     const f64x4_t S = tile_product(G, G);
-    const f64x4_t P = p.a * I + p.b * G + p.c * S;
+    const f64x4_t P = combined(p.a * I, p.b, G, p.c, S);
     if (it + 1 < p.steps) {
-      const f64x4_t H = p.a * G + p.b * S + p.c * tile_product(G, S);
+      const f64x4_t H = combined(p.a * G, p.b, S, p.c, tile_product(G, S));
       G = tile_product(H, P);
     }
     Q = tile_product(Q, P);
@@ -466,8 +474,9 @@ __global__ __launch_bounds__(256) void tiny_kernel(const MuonMat *table, MuonPar
 }
 
 // 16 < k <= 64: one workgroup, three matrices in LDS: G, S (then P), Q, as tiles
-// of registers ([tile][register][lane], tile = NT ti + tj), so that every operand
-// is one contiguous read.  A product's tiles of the upper triangle are dealt
+// of registers ([tile][register][lane ^ 4 register], tile = NT ti + tj), so that
+// an operand is one contiguous read and a tile's mirror image goes to all banks
+// (without the exchange it goes to 8 of 32, and storing took half the time).  A product's tiles of the upper triangle are dealt
 // over the wavefronts, kept in registers until every read is done, and stored
 // with their mirror images.
 template <int NT>
@@ -477,21 +486,31 @@ struct Small {
   static constexpr int bytes = 3 * size * 8;
 };
 
+// Register r of a lane in a tile.
+__device__ __forceinline__ int in_tile(int r, int lane) { return 64 * r + (lane ^ (4 * r)); }
+
 template <int NT>
 __device__ __forceinline__ f64x4_t lds_product(const double *A, const double *B, int ti, int tj) {
   const int lane = threadIdx.x & 63;
-  const double *x = A + ti * 256 + lane, *y = B + tj * 256 + lane;
-  // all operands requested first: left to itself the compiler waits for each pair
-  double u[4 * NT], v[4 * NT];
+  const double *x = A + ti * 256, *y = B + tj * 256;
+  // operands four products ahead: left to itself the compiler waits for each
+  // pair, and all of them first would leave the products waiting for LDS
+  constexpr int N = 4 * NT, ahead = 4;
+  double u[N], v[N];
+  auto request = [&](int s) {
+    u[s] = x[s / 4 * NT * 256 + in_tile(s % 4, lane)];
+    v[s] = y[s / 4 * NT * 256 + in_tile(s % 4, lane)];
+  };
 #pragma unroll
-  for (int s = 0; s < 4 * NT; ++s) {
-    u[s] = x[s / 4 * NT * 256 + 64 * (s % 4)];
-    v[s] = y[s / 4 * NT * 256 + 64 * (s % 4)];
-  }
+  for (int s = 0; s < ahead; ++s) request(s);
   __builtin_amdgcn_sched_barrier(0);
   f64x4_t d = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-  for (int s = 0; s < 4 * NT; ++s) d = mfma64(u[s], v[s], d);
+  for (int s = 0; s < N; ++s) {
+    if (s + ahead < N) request(s + ahead);
+    __builtin_amdgcn_sched_barrier(0);
+    d = mfma64(u[s], v[s], d);
+  }
   return d;
 }
 
@@ -505,18 +524,19 @@ template <int NT>
 __device__ __forceinline__ void put_tile(double *M, int ti, int tj, const f64x4_t &d) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) M[(NT * ti + tj) * 256 + 64 * r + lane] = d[r];
+  for (int r = 0; r < 4; ++r) M[(NT * ti + tj) * 256 + in_tile(r, lane)] = d[r];
   if (ti == tj) return;
   // element (lane / 16 + 4 r, lane % 16) is (lane % 16, lane / 16 + 4 r) there
-  double *T = M + (NT * tj + ti) * 256 + 64 * ((lane & 15) >> 2) + 16 * (lane & 3) + (lane >> 4);
+  double *T = M + (NT * tj + ti) * 256;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) T[4 * r] = d[r];
+  for (int r = 0; r < 4; ++r)
+    T[in_tile((lane & 15) >> 2, 16 * (lane & 3) + (lane >> 4) + 4 * r)] = d[r];
 }
 
 // Element (i, j) of a matrix of tiles.
 template <int NT>
 __device__ __forceinline__ double &element(double *M, int i, int j) {
-  return M[(NT * (i >> 4) + (j >> 4)) * 256 + 64 * ((i & 15) >> 2) + 16 * (i & 3) + (j & 15)];
+  return M[(NT * (i >> 4) + (j >> 4)) * 256 + in_tile((i & 15) >> 2, 16 * (i & 3) + (j & 15))];
 }
 
 template <int NT>
@@ -532,33 +552,38 @@ __global__ __launch_bounds__(Small<NT>::threads) void small_kernel(const MuonMat
   double *area = ws + a.area;
   // (a tall matrix of 33 .. 48 columns has four tiles of partials: columns 4 c + t)
   const Block b = block_of(a.k, 0, a.wide);
-  for (int e = threadIdx.x; e < kPairDoubles; e += S::threads) {
-    const int ti = e >> 10, tj = (e >> 8) & 3;
-    if (tj >= b.tiles || ti > tj) continue;
-    const double v = area[e];
+  constexpr int N = kPairDoubles / S::threads;
+  double v[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) v[q] = area[threadIdx.x + q * S::threads];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const int e = threadIdx.x + q * S::threads, ti = e >> 10, tj = (e >> 8) & 3;
+    if (tj >= b.tiles || ti > tj) continue;                // (not written)
     const int i = column_of(b, a.wide, ti, ((e & 63) >> 4) + 4 * ((e >> 6) & 3));
     const int j = column_of(b, a.wide, tj, e & 15);
     if (i >= S::kp || j >= S::kp) continue;
-    element<NT>(G, i, j) = v;
-    if (ti < tj) element<NT>(G, j, i) = v;
-    if (i == j) diagonal[i] = v;
+    element<NT>(G, i, j) = v[q];
+    if (ti < tj) element<NT>(G, j, i) = v[q];
+    if (i == j) diagonal[i] = v[q];
   }
   __syncthreads();
   const double inv = inverse_norm(wave_sum(lane < S::kp ? diagonal[lane] : 0.0), p.eps);
   for (int e = threadIdx.x; e < S::size; e += S::threads) {
     G[e] *= inv * inv;
-    const int r = e >> 8;                                // its tile: NT ti + tj
-    const int i = 16 * (r / NT) + ((e & 63) >> 4) + 4 * ((e >> 6) & 3), j = 16 * (r % NT) + (e & 15);
-    Q[e] = i == j ? inv : 0.0;
+    Q[e] = 0.0;
   }
+  __syncthreads();
+  if (int(threadIdx.x) < S::kp) element<NT>(Q, threadIdx.x, threadIdx.x) = inv;
   __syncthreads();
   constexpr int per = (S::tiles + S::waves - 1) / S::waves;
   constexpr int both = (2 * S::tiles + S::waves - 1) / S::waves;
-  f64x4_t I;
+  f64x4_t aI;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) I[r] = (lane >> 4) + 4 * r == (lane & 15) ? 1.0 : 0.0;
+  for (int r = 0; r < 4; ++r) aI[r] = (lane >> 4) + 4 * r == (lane & 15) ? p.a : 0.0;
   for (int it = 0; it < p.steps; ++it) {
     f64x4_t d[both], s[per];
+    const bool last = it + 1 == p.steps;
     // S = G G
 #pragma unroll
     for (int q = 0; q < per; ++q) {
@@ -579,8 +604,8 @@ __global__ __launch_bounds__(Small<NT>::threads) void small_kernel(const MuonMat
       int ti, tj;
       tile_of_index(t, ti, tj);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) g[q][r] = G[(NT * ti + tj) * 256 + 64 * r + lane];
-      d[q] = lds_product<NT>(G, P, ti, tj);
+      for (int r = 0; r < 4; ++r) g[q][r] = G[(NT * ti + tj) * 256 + in_tile(r, lane)];
+      if (!last) d[q] = lds_product<NT>(G, P, ti, tj);
     }
     __syncthreads();
 #pragma unroll
@@ -589,12 +614,12 @@ __global__ __launch_bounds__(Small<NT>::threads) void small_kernel(const MuonMat
       if (t >= S::tiles) break;
       int ti, tj;
       tile_of_index(t, ti, tj);
-      put_tile<NT>(G, ti, tj, p.a * g[q] + p.b * s[q] + p.c * d[q]);
-      put_tile<NT>(P, ti, tj, (ti == tj ? p.a : 0.0) * I + p.b * g[q] + p.c * s[q]);
+      if (!last) put_tile<NT>(G, ti, tj, combined(p.a * g[q], p.b, s[q], p.c, d[q]));
+      put_tile<NT>(P, ti, tj, combined(ti == tj ? aI : 0.0 * aI, p.b, g[q], p.c, s[q]));
     }
     __syncthreads();
     // G <- H P and Q <- Q P; the last time Q alone
-    const int units = (it + 1 == p.steps ? 1 : 2) * S::tiles;
+    const int units = (last ? 1 : 2) * S::tiles;
 #pragma unroll
     for (int q = 0; q < both; ++q) {
       const int t = wave + q * S::waves;
