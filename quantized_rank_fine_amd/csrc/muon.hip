@@ -28,14 +28,14 @@ namespace qlora {
 namespace {
 
 // A matrix in the kernels: n long, k short; quads: 16-byte accesses.  span: long rows to a Gram workgroup,
-// `splits` of them; area: where its fp64 scratch begins.  u: the direction, of
+// `splits` of them; apply: long rows to an update workgroup (k <= 64); area: where its fp64 scratch begins.  u: the direction, of
 // k > 64 (grad, m or an array of its own).
 struct MuonMat {
   const float *grad, *u;
   float *m, *theta;
   uint16_t *theta16;
   float *update;
-  int64_t n, span, area;
+  int64_t n, span, apply, area;
   int32_t k, wide, quads, splits;
   float scale;
 };
@@ -801,9 +801,6 @@ __device__ __forceinline__ void update_run(const MuonMat &a, const MuonParams &p
 //     four products; tile t has columns NT c + t.
 //   wide: lane (g, c) loads long rows 2 c, 2 c + 1 of column 4 s + g, the operands
 //     of two tiles; a result's rows are short.
-// Long rows to a workgroup: what makes up for reading Q.
-constexpr int apply_rows(int NT) { return NT == 1 ? 128 : 256; }
-
 // A lane's Q: row 16 j + 4 g + e, columns NT c .. (tall), or row 4 s + g, columns
 // c, 16 + c .. (wide), as the products ask for them.
 template <int NT>
@@ -848,27 +845,51 @@ struct Factor {
 };
 
 template <int NT, bool Q>
-__device__ __forceinline__ void apply_tall(const MuonMat &a, const MuonParams &p,
-                                           const Factor<NT> &f, int64_t r, int64_t end) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const bool has_m = a.m != nullptr, read_g = !has_m || p.nesterov;
+struct TallRows {
   Run<4> gr[NT], m[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int live = r + c < end ? clamped(a.k - 16 * j - 4 * g, 4) : 0;
-    const Place at = {r * a.k + (16 * j < a.k ? 16 * j : 0), uint32_t(c * a.k + 4 * g)};
-    gr[j] = read_g ? load_run<Q, 4>(a.grad, at, live) : Run<4>{};
-    m[j] = has_m ? load_run<Q, 4>(a.m, at, live) : Run<4>{};
-  }
   Run<NT> th[4];
-  const int mine = clamped(a.k - NT * c, NT);
-  auto place = [&](int i) {
-    return Place{(r + 4 * i < end ? r + 4 * i : 0) * a.k, uint32_t(g * a.k + NT * c)};
-  };
-  auto live_of = [&](int i) { return r + 4 * i + g < end ? mine : 0; };
+  int mine;
+  __device__ __forceinline__ Place place(const MuonMat &a, int64_t r, int64_t end, int i) const {
+    const int lane = threadIdx.x & 63;
+    return {(r + 4 * i < end ? r + 4 * i : 0) * a.k,
+            uint32_t((lane >> 4) * a.k + NT * (lane & 15))};
+  }
+  __device__ __forceinline__ int live(int64_t r, int64_t end, int i) const {
+    return r + 4 * i + ((threadIdx.x & 63) >> 4) < end ? mine : 0;
+  }
+  __device__ __forceinline__ void request(const MuonMat &a, const MuonParams &p, int64_t r,
+                                          int64_t end) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const bool has_m = a.m != nullptr, read_g = !has_m || p.nesterov;
+    mine = clamped(a.k - NT * c, NT);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    th[i] = a.theta ? load_run<Q, NT>(a.theta, place(i), live_of(i)) : Run<NT>{};
+    for (int j = 0; j < NT; ++j) {
+      const int live = r + c < end ? clamped(a.k - 16 * j - 4 * g, 4) : 0;
+      const Place at = {(r < end ? r : 0) * a.k + (16 * j < a.k ? 16 * j : 0),
+                        uint32_t(c * a.k + 4 * g)};
+      gr[j] = read_g ? load_run<Q, 4>(a.grad, at, live) : Run<4>{};
+      m[j] = has_m ? load_run<Q, 4>(a.m, at, live) : Run<4>{};
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      th[i] = a.theta ? load_run<Q, NT>(a.theta, place(a, r, end, i), live(r, end, i)) : Run<NT>{};
+  }
+};
+
+template <int NT, bool Q>
+__device__ __forceinline__ void apply_tall(const MuonMat &a, const MuonParams &p,
+                                           const Factor<NT> &f, int64_t r, int64_t end,
+                                           TallRows<NT, Q> &x) {
+  const bool has_m = a.m != nullptr;
+  double u[4 * NT];
+#pragma unroll
+  for (int s = 0; s < 4 * NT; ++s)
+    u[s] = double(direction<false>(p, has_m, x.gr[s / 4].v[s % 4], x.m[s / 4].v[s % 4]));
+  Run<NT> th[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) th[i] = x.th[i];
+  // the next rows are on their way meanwhile (past the end: nothing is live)
+  x.request(a, p, r + 64, end);
   f64x4_t d[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) d[t] = f64x4_t{0.0, 0.0, 0.0, 0.0};
@@ -881,52 +902,66 @@ __device__ __forceinline__ void apply_tall(const MuonMat &a, const MuonParams &p
     for (int t = 0; t < NT; ++t)
       if (s + 1 < 4 * NT) y[(s + 1) & 1][t] = f.template at<false>(s + 1, t);
     if (!Factor<NT>::held) __builtin_amdgcn_sched_barrier(0);
-    const double u = double(direction<false>(p, has_m, gr[s / 4].v[s % 4], m[s / 4].v[s % 4]));
 #pragma unroll
-    for (int t = 0; t < NT; ++t) d[t] = mfma64(u, y[s & 1][t], d[t]);
+    for (int t = 0; t < NT; ++t) d[t] = mfma64(u[s], y[s & 1][t], d[t]);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    Run<NT> x;
+    Run<NT> v;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) x.v[t] = float(d[t][i]);
-    update_run<Q, NT>(a, p, place(i), live_of(i), x, th[i]);
+    for (int t = 0; t < NT; ++t) v.v[t] = float(d[t][i]);
+    update_run<Q, NT>(a, p, x.place(a, r, end, i), x.live(r, end, i), v, th[i]);
   }
 }
 
 template <int NT, bool Q>
+struct WideRows {
+  // four products' operands in hand, four on their way
+  Run<2> gr[2][4], m[2][4];
+  // column (row of memory) 4 s + g
+  __device__ __forceinline__ Place place(const MuonMat &a, int64_t r, int64_t end, int s) const {
+    const int lane = threadIdx.x & 63;
+    return {(4 * s < a.k ? 4 * s : 0) * a.n + (r < end ? r : 0),
+            uint32_t((lane >> 4) * a.n) + 2 * (lane & 15)};
+  }
+  __device__ __forceinline__ int live(const MuonMat &a, int64_t r, int64_t end, int s) const {
+    const int lane = threadIdx.x & 63;
+    return 4 * s + (lane >> 4) < a.k ? clamped(end - r - 2 * (lane & 15), 2) : 0;
+  }
+  __device__ __forceinline__ void request(const MuonMat &a, const MuonParams &p, int64_t r,
+                                          int64_t end, int j) {
+    const bool has_m = a.m != nullptr, read_g = !has_m || p.nesterov;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Place at = place(a, r, end, 4 * j + i);
+      const int n = live(a, r, end, 4 * j + i);
+      gr[j & 1][i] = read_g ? load_run<Q, 2>(a.grad, at, n) : Run<2>{};
+      m[j & 1][i] = has_m ? load_run<Q, 2>(a.m, at, n) : Run<2>{};
+    }
+  }
+};
+
+template <int NT, bool Q>
 __device__ __forceinline__ void apply_wide(const MuonMat &a, const MuonParams &p,
-                                           const Factor<NT> &f, int64_t r, int64_t end) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const bool has_m = a.m != nullptr, read_g = !has_m || p.nesterov;
-  const int along = clamped(end - r - 2 * c, 2);
+                                           const Factor<NT> &f, int64_t r, int64_t end,
+                                           WideRows<NT, Q> &x) {
+  const bool has_m = a.m != nullptr;
   f64x4_t d[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t) d[t][0] = d[t][1] = f64x4_t{0.0, 0.0, 0.0, 0.0};
-  // column (row of memory) 4 s + g
-  auto place = [&](int s) {
-    return Place{(4 * s < a.k ? 4 * s : 0) * a.n + r, uint32_t(g * a.n) + 2 * c};
-  };
-  auto live_of = [&](int s) { return 4 * s + g < a.k ? along : 0; };
-  // four products' operands in hand, four on their way
-  Run<2> gr[2][4], m[2][4];
-  auto request = [&](int at, int s0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const Place where = place(s0 + i);
-      const int live = live_of(s0 + i);
-      gr[at][i] = read_g ? load_run<Q, 2>(a.grad, where, live) : Run<2>{};
-      m[at][i] = has_m ? load_run<Q, 2>(a.m, where, live) : Run<2>{};
-    }
-  };
-  request(0, 0);
+  Run<2> th[4 * NT];
   double y[2][NT];                             // a product's Q, and the next one's
 #pragma unroll
   for (int t = 0; t < NT; ++t) y[0][t] = f.template at<true>(0, t);
 #pragma unroll
   for (int s = 0; s < 4 * NT; ++s) {
     const int j = s / 4, i = s % 4;
-    if (i == 0 && j + 1 < NT) request((j + 1) & 1, 4 * (j + 1));
+    if (i == 0 && j + 1 < NT) x.request(a, p, r, end, j + 1);
+    if (s == 4 * NT - 4)                       // theta, behind the last of u
+#pragma unroll
+      for (int q = 0; q < 4 * NT; ++q)
+        th[q] = a.theta ? load_run<Q, 2>(a.theta, x.place(a, r, end, q), x.live(a, r, end, q))
+                        : Run<2>{};
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       if (s + 1 < 4 * NT) y[(s + 1) & 1][t] = f.template at<true>(s + 1, t);
@@ -934,43 +969,44 @@ __device__ __forceinline__ void apply_wide(const MuonMat &a, const MuonParams &p
     double u[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      u[e] = double(direction<false>(p, has_m, gr[j & 1][i].v[e], m[j & 1][i].v[e]));
+      u[e] = double(direction<false>(p, has_m, x.gr[j & 1][i].v[e], x.m[j & 1][i].v[e]));
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) d[t][e] = mfma64(y[s & 1][t], u[e], d[t][e]);
   }
-  Run<2> th[4 * NT];
-#pragma unroll
-  for (int i = 0; i < 4 * NT; ++i)
-    th[i] = a.theta ? load_run<Q, 2>(a.theta, place(i), live_of(i)) : Run<2>{};
+  x.request(a, p, r + 128, end, 0);
 #pragma unroll
   for (int i = 0; i < 4 * NT; ++i) {
-    const Run<2> x = {{float(d[i / 4][0][i % 4]), float(d[i / 4][1][i % 4])}};
-    update_run<Q, 2>(a, p, place(i), live_of(i), x, th[i]);
+    const Run<2> v = {{float(d[i / 4][0][i % 4]), float(d[i / 4][1][i % 4])}};
+    update_run<Q, 2>(a, p, x.place(a, r, end, i), x.live(a, r, end, i), v, th[i]);
   }
 }
 
 template <int NT, bool ALIGNED>
-__global__ __launch_bounds__(256) void apply_kernel(const MuonMat *table, MuonParams p,
+__global__ __launch_bounds__(256, ALIGNED ? 2 : 1) void apply_kernel(const MuonMat *table, MuonParams p,
                                                     const double *ws) {
   using F = Factor<NT>;
   __shared__ __align__(16) double shared[F::held ? 1 : F::K * F::pitch];
   const MuonMat a = table[blockIdx.y];
   const int kp = padded(a.k);
-  const int64_t from = int64_t(blockIdx.x) * apply_rows(NT);
+  const int64_t from = int64_t(blockIdx.x) * a.apply;
   if (from >= a.n || kp > F::K || (NT > 1 && kp <= F::K / 2) || bool(a.quads) != ALIGNED) return;
-  const int64_t end = from + apply_rows(NT) < a.n ? from + apply_rows(NT) : a.n;
+  const int64_t end = from + a.apply < a.n ? from + a.apply : a.n;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   F f;
   if (a.wide) {
+    WideRows<NT, ALIGNED> x;
+    x.request(a, p, from + 32 * wave, end, 0);
     f.template init<true>(ws + a.area, kp, shared);
     for (int64_t r = from + 32 * wave; r < end; r += 128, f.again())
-      apply_wide<NT, ALIGNED>(a, p, f, r, end);
+      apply_wide<NT, ALIGNED>(a, p, f, r, end, x);
   } else {
+    TallRows<NT, ALIGNED> x;
+    x.request(a, p, from + 16 * wave, end);
     f.template init<false>(ws + a.area, kp, shared);
     for (int64_t r = from + 16 * wave; r < end; r += 64, f.again())
-      apply_tall<NT, ALIGNED>(a, p, f, r, end);
+      apply_tall<NT, ALIGNED>(a, p, f, r, end, x);
   }
 }
 
@@ -1145,6 +1181,9 @@ MuonMat planned(const qlora_muon_mat &q, int64_t span0, bool nesterov, double *w
   const int64_t span = most < kp / 2 ? kp / 2 : most;
   a.span = (span + kGramRows - 1) / kGramRows * kGramRows;
   a.splits = int32_t((a.n + a.span - 1) / a.span);
+  // one round of workgroups, each of which reads Q once (256 or 512 rows of 64
+  // adapters of 4096 x 64: 77.4 and 70.5 us)
+  a.apply = span0 < 1024 ? (span0 + 127) / 128 * 128 : 1024;
   a.area = o;
   const int64_t first = int64_t(pairs_of(a.k)) * kPairDoubles, sq = int64_t(kp) * kp;
   o += a.splits * first;
@@ -1198,7 +1237,7 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
         small[kp / 16] = true;
         raise(splits[a.quads], a.splits);
         const int NT = kp <= 16 ? 1 : kp <= 32 ? 2 : 4;
-        raise(blocks[a.quads][NT], (a.n + apply_rows(NT) - 1) / apply_rows(NT));
+        raise(blocks[a.quads][NT], (a.n + a.apply - 1) / a.apply);
       } else {
         raise(splits_large[a.quads], a.splits);
         raise(blocks_large[(a.k + 63) / 64], (a.n + kLargeRows - 1) / kLargeRows);
