@@ -29,14 +29,34 @@ __device__ __forceinline__ float sigmoid(float v) {
 constexpr float kGeluTwo = 1.59576912160573081f;     // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
 
-// act(z).  (1 + tanh v) / 2 = sigmoid(2 v) and Phi(z) = erfc(-z / sqrt 2) / 2
-// keep the digits of the left tails, where 1 + tanh and 1 + erf cancel.
+// Phi(z), within 3e-7, and e = e^(-z^2 / 2): erfc(x) =
+// e^(-x^2) (a1 t + ... + a5 t^5), t = 1 / (1 + 0.3275911 x), of Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26, for x = |z| / sqrt 2.  It
+// shares e with the derivative and takes 15 operations where erfcf takes 60
+// (the forward of 2048 x 4096 x 11008 with it 263 us, so 229).
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+  const float a = fabsf(z);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.231641888f, a, 1.0f));
+  e = __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
+  float s = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+  s = __builtin_fmaf(s, t, 1.421413741f);
+  s = __builtin_fmaf(s, t, -0.284496736f);
+  s = __builtin_fmaf(s, t, 0.254829592f);
+  const float tail = 0.5f * s * t * e;
+  return z < 0.0f ? tail : 1.0f - tail;
+}
+
+// act(z).  (1 + tanh v) / 2 = sigmoid(2 v) keeps the digits of the left tail,
+// where 1 + tanh cancels.
 template <int act>
 __device__ __forceinline__ float activated(float z) {
   if (act == kActRelu) return fmaxf(z, 0.0f);
   if (act == kActSilu) return z * sigmoid(z);
   if (act == kActGeluTanh) return z * sigmoid(kGeluTwo * __builtin_fmaf(kGeluCube * z * z, z, z));
-  if (act == kActGelu) return 0.5f * z * erfcf(-0.70710678118654752f * z);
+  if (act == kActGelu) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
   return z;
 }
 
@@ -62,11 +82,10 @@ __device__ __forceinline__ void activated(float z, float &f, float &df) {
     df = __builtin_fmaf(f * (1.0f - s), kGeluTwo * __builtin_fmaf(3.0f * kGeluCube * c, c, 1.0f), s);
   }
   if (act == kActGelu) {
-    const float cdf = 0.5f * erfcf(-0.70710678118654752f * z);
+    float e;
+    const float cdf = normal_cdf(z, e);
     f = z * cdf;
-    // e^(-z^2 / 2) / sqrt(2 pi)
-    df = __builtin_fmaf(0.39894228040143268f * z,
-                        __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z), cdf);
+    df = __builtin_fmaf(0.39894228040143268f * z, e, cdf);   // z e / sqrt(2 pi)
   }
 }
 

@@ -104,10 +104,11 @@ __global__ __launch_bounds__(kThreads) void bias_sum_kernel(const double *partia
 
 }  // namespace
 
-// 64 rows, or more where there would be more than 256 slabs.
+// 64 rows of up to 128, else 32, or more where there would be more than 256 slabs.
 int64_t ep_bwd_slab(int64_t M) {
-  const int64_t most = ((M + 255) / 256 + 63) / 64 * 64;
-  return most < 64 ? 64 : most;
+  if (M <= 128) return 64;
+  const int64_t most = ((M + 255) / 256 + 31) / 32 * 32;
+  return most < 32 ? 32 : most;
 }
 
 int64_t ep_bwd_slabs(int64_t M) { return (M + ep_bwd_slab(M) - 1) / ep_bwd_slab(M); }

@@ -4,8 +4,8 @@ The end is checked from its own z: Z is the plain forward's result (the same
 accumulators, so the same bits where there is no bias, and in fp32 one rounded
 addition where there is), and y against float64 from z.  Of an fp32 y:
 sigma(v) is within 0.28 * 4 2^-24 (its argument's error) + 3 2^-24 (exp2,
-addition, reciprocal) < 5 2^-24, erfc within 4 steps, then three products and
-sums: 8 2^-24 of |act| and 12 2^-24 of the parts (the derivatives' of
+addition, reciprocal) < 5 2^-24, Phi within half of 1.5e-7 (its formula's) and 3
+2^-24 < 5 2^-24, then three products and sums: 8 2^-24 of |act| and 12 2^-24 of the parts (the derivatives' of
 (1 + |z|)).  A bf16 z is known to half a step, 2^-8 |z| (act' <= 1.13), and a
 bf16 result adds 2^-8 of itself."""
 
