@@ -1010,10 +1010,10 @@ __global__ __launch_bounds__(256, ALIGNED ? 2 : 1) void apply_kernel(const MuonM
   }
 }
 
-// k > 64: 64 long rows of u in LDS (fp32) for a workgroup, each of whose NB
+// k > 64: 32 long rows of u in LDS (fp32) for a workgroup, each of whose NB
 // wavefronts forms a block of 64 columns of O; Q comes from L2, each value once
 // a workgroup, requested a product ahead.
-constexpr int kLargeRows = 64;
+constexpr int kLargeRows = 32, kLargeTiles = kLargeRows / 16;
 
 // LDS row pitch (floats): 17 past a multiple of 64, so that a fragment (16 rows
 // of 4) and a column written by consecutive lanes spread over the banks.
@@ -1025,15 +1025,15 @@ __device__ __forceinline__ void large_block(const MuonMat &a, const MuonParams &
                                             int pitch, const double *q, int kp, int64_t from,
                                             int first) {
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  f64x4_t d[4][T];
+  f64x4_t d[kLargeTiles][T];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kLargeTiles; ++i)
 #pragma unroll
     for (int t = 0; t < T; ++t) d[i][t] = f64x4_t{0.0, 0.0, 0.0, 0.0};
   // two products of operands in hand, two on their way (kp / 4 is a multiple of
   // four; past the end the last ones again)
   double y[4][T];
-  float x[4][4];
+  float x[4][kLargeTiles];
   const float *xs = us + c * pitch + g;
   const double *ys = q + int64_t(g) * kp + c;
   const int last = kp / 4 - 2;
@@ -1044,7 +1044,7 @@ __device__ __forceinline__ void large_block(const MuonMat &a, const MuonParams &
 #pragma unroll
       for (int t = 0; t < T; ++t) y[at + h][t] = ys[int64_t(4 * (e + h)) * kp + 16 * t];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[at + h][i] = xs[16 * i * pitch + 4 * (e + h)];
+      for (int i = 0; i < kLargeTiles; ++i) x[at + h][i] = xs[16 * i * pitch + 4 * (e + h)];
     }
   };
   auto multiply = [&](int at) {
@@ -1053,7 +1053,7 @@ __device__ __forceinline__ void large_block(const MuonMat &a, const MuonParams &
 #pragma unroll
       for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kLargeTiles; ++i) {
           const double u = double(x[at + h][i]);
           d[i][t] = WIDE ? mfma64(y[at + h][t], u, d[i][t]) : mfma64(u, y[at + h][t], d[i][t]);
         }
@@ -1069,7 +1069,7 @@ __device__ __forceinline__ void large_block(const MuonMat &a, const MuonParams &
   }
 #pragma unroll
   for (int t = 0; t < T; ++t) {
-    Run<1> th[4][4];
+    Run<1> th[kLargeTiles][4];
     // long row row0 + (wide: c, tall: g), column col0 + (wide: g, tall: c)
     auto row0 = [&](int i, int r) { return from + 16 * i + (WIDE ? 0 : 4 * r); };
     auto col0 = [&](int r) { return first + 16 * t + (WIDE ? 4 * r : 0); };
@@ -1083,19 +1083,19 @@ __device__ __forceinline__ void large_block(const MuonMat &a, const MuonParams &
                   : Place{row * a.k + col, uint32_t(g * a.k + c)};
     };
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kLargeTiles; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         th[i][r] = a.theta ? load_run<true, 1>(a.theta, place(i, r), live_of(i, r)) : Run<1>{};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kLargeTiles; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         update_run<true, 1>(a, p, place(i, r), live_of(i, r), Run<1>{{float(d[i][t][r])}}, th[i][r]);
   }
 }
 
-// u of 64 long rows into LDS, four values of a lane at a time along memory.
+// u of a workgroup's long rows into LDS, four values of a lane at a time along memory.
 template <bool WIDE, bool Q, int threads>
 __device__ __forceinline__ void stage_rows(const MuonMat &a, int64_t from, int kp, int pitch,
                                            float *us) {
@@ -1131,7 +1131,7 @@ __device__ __forceinline__ void stage_rows(const MuonMat &a, int64_t from, int k
 }
 
 template <int NB>
-__global__ __launch_bounds__(64 * NB, 2) void apply_large_kernel(const MuonMat *table, MuonParams p,
+__global__ __launch_bounds__(64 * NB, 4) void apply_large_kernel(const MuonMat *table, MuonParams p,
                                                               double *ws) {
   extern __shared__ __align__(16) float us[];
   const MuonMat a = table[blockIdx.y];
