@@ -1177,7 +1177,7 @@ MuonMat planned(const qlora_muon_mat &q, int64_t span0, bool nesterov, double *w
   const int kp = padded(a.k);
   // a slab's k x k partial sums stay a small part of what it reads; of k > 64 a
   // slab is a workgroup to every pair of blocks
-  const int64_t most = a.k <= 64 ? span0 : span0 * pairs_of(a.k) / 2;
+  const int64_t most = a.k <= 64 ? span0 : span0 * pairs_of(a.k);
   const int64_t span = most < kp / 2 ? kp / 2 : most;
   a.span = (span + kGramRows - 1) / kGramRows * kGramRows;
   a.splits = int32_t((a.n + a.span - 1) / a.span);
