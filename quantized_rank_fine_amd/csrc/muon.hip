@@ -653,20 +653,22 @@ enum MuonStage { kSquare, kPolynomial, kAdvance };
 // A quarter of the operands of a tile of columns 16 t ..: kp / 16 steps of four
 // rows, all requested before the first is used (past them the last ones again,
 // which the products leave out).
+template <int N>                              // kp <= 16 N
 struct Quarter {
-  double v[16];
+  double v[N];
   __device__ __forceinline__ Quarter(const double *M, int kp, int t, int wave) {
     const int lane = threadIdx.x & 63, steps = kp / 16;
     const double *x = M + int64_t(4 * wave * steps + (lane >> 4)) * kp + 16 * t + (lane & 15);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = x[4 * (i < steps ? i : steps - 1) * kp];
+    for (int i = 0; i < N; ++i) v[i] = x[4 * (i < steps ? i : steps - 1) * kp];
   }
 };
 
-__device__ __forceinline__ f64x4_t part_product(const Quarter &a, const Quarter &b, int kp) {
+template <int N>
+__device__ __forceinline__ f64x4_t part_product(const Quarter<N> &a, const Quarter<N> &b, int kp) {
   f64x4_t d = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) d = mfma64(i < kp / 16 ? a.v[i] : 0.0, b.v[i], d);
+  for (int i = 0; i < N; ++i) d = mfma64(i < kp / 16 ? a.v[i] : 0.0, b.v[i], d);
   return d;
 }
 
@@ -701,19 +703,11 @@ int64_t stage_grid(int64_t n, int64_t tiles) {
   return n >= 8 ? 8 * tiles * ((n + 7) / 8) : 8 * ((tiles + 8 / n - 1) / (8 / n));
 }
 
-__global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonParams p, double *ws,
-                                                    int stage, int it, int n, int tiles) {
-  __shared__ double red[4][4][64];
-  __shared__ double norm;
-  int which, t;
-  stage_job(n, tiles, which, t);
-  if (which >= n || t >= tiles) return;
-  const MuonMat a = table[which];
-  if (a.k <= 64) return;
-  const int kp = padded(a.k), NT = kp / 16;
-  const bool second = t >= NT * (NT + 1) / 2;              // (kAdvance: the other product)
-  if (second) t -= NT * (NT + 1) / 2;
-  if (t >= NT * (NT + 1) / 2 || (second && stage != kAdvance)) return;
+// One workgroup's tile t of a launch's product (second: of kAdvance's other one).
+template <int N>
+__device__ __forceinline__ void stage_tile(const MuonMat &a, const MuonParams &p, double *ws,
+                                           int stage, int it, int kp, int t, bool second,
+                                           double (*red)[4][64], double &norm) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   int ti, tj;
   tile_of_index(t, ti, tj);
@@ -725,12 +719,12 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
     if (ti < tj) M[ji] = v;
   };
   if (stage == kSquare) {
-    const Quarter x(m.G, kp, ti, wave), y(m.G, kp, tj, wave);
+    const Quarter<N> x(m.G, kp, ti, wave), y(m.G, kp, tj, wave);
     put(m.S, joined_part(part_product(x, y, kp), wave, red));
     return;
   }
   if (stage == kPolynomial) {
-    const Quarter x(m.G, kp, ti, wave), y(m.S, kp, tj, wave);
+    const Quarter<N> x(m.G, kp, ti, wave), y(m.S, kp, tj, wave);
     // the first G is not yet scaled: its powers take the factor here
     double f = 1.0, inv = 1.0;
     if (it == 0) {
@@ -757,8 +751,25 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
   }
   // kAdvance: G <- H P (but the last time) or, past the first, Q' = Q P
   if (second ? it == 0 : it + 1 == p.steps) return;
-  const Quarter x(second ? m.Q(it) : m.H, kp, ti, wave), y(m.P, kp, tj, wave);
+  const Quarter<N> x(second ? m.Q(it) : m.H, kp, ti, wave), y(m.P, kp, tj, wave);
   put(second ? m.Q(it + 1) : m.G, joined_part(part_product(x, y, kp), wave, red));
+}
+
+__global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonParams p, double *ws,
+                                                    int stage, int it, int n, int tiles) {
+  __shared__ double red[4][4][64];
+  __shared__ double norm;
+  int which, t;
+  stage_job(n, tiles, which, t);
+  if (which >= n || t >= tiles) return;
+  const MuonMat a = table[which];
+  if (a.k <= 64) return;
+  const int kp = padded(a.k), NT = kp / 16;
+  const bool second = t >= NT * (NT + 1) / 2;              // (kAdvance: the other product)
+  if (second) t -= NT * (NT + 1) / 2;
+  if (t >= NT * (NT + 1) / 2 || (second && stage != kAdvance)) return;
+  if (kp <= 128) stage_tile<8>(a, p, ws, stage, it, kp, t, second, red, norm);
+  else stage_tile<16>(a, p, ws, stage, it, kp, t, second, red, norm);
 }
 
 // ------------------------------------------------------------ the update
@@ -1067,32 +1078,35 @@ __device__ __forceinline__ void large_block(const MuonMat &a, const MuonParams &
     __builtin_amdgcn_sched_barrier(0);
     multiply(2);
   }
+  // long row row0 + (wide: c, tall: g), column col0 + (wide: g, tall: c)
+  auto row0 = [&](int i, int r) { return from + 16 * i + (WIDE ? 0 : 4 * r); };
+  auto col0 = [&](int t, int r) { return first + 16 * t + (WIDE ? 4 * r : 0); };
+  auto live_of = [&](int t, int i, int r) {
+    return row0(i, r) + (WIDE ? c : g) < a.n && col0(t, r) + (WIDE ? g : c) < a.k;
+  };
+  auto place = [&](int t, int i, int r) {
+    const int64_t row = row0(i, r) < a.n ? row0(i, r) : 0;
+    const int col = col0(t, r) < a.k ? col0(t, r) : 0;
+    return WIDE ? Place{col * a.n + row, uint32_t(g * a.n) + c}
+                : Place{row * a.k + col, uint32_t(g * a.k + c)};
+  };
+  // (all of theta before the first store, behind which no load moves)
+  Run<1> th[T][kLargeTiles][4];
 #pragma unroll
-  for (int t = 0; t < T; ++t) {
-    Run<1> th[kLargeTiles][4];
-    // long row row0 + (wide: c, tall: g), column col0 + (wide: g, tall: c)
-    auto row0 = [&](int i, int r) { return from + 16 * i + (WIDE ? 0 : 4 * r); };
-    auto col0 = [&](int r) { return first + 16 * t + (WIDE ? 4 * r : 0); };
-    auto live_of = [&](int i, int r) {
-      return row0(i, r) + (WIDE ? c : g) < a.n && col0(r) + (WIDE ? g : c) < a.k;
-    };
-    auto place = [&](int i, int r) {
-      const int64_t row = row0(i, r) < a.n ? row0(i, r) : 0;
-      const int col = col0(r) < a.k ? col0(r) : 0;
-      return WIDE ? Place{col * a.n + row, uint32_t(g * a.n) + c}
-                  : Place{row * a.k + col, uint32_t(g * a.k + c)};
-    };
-#pragma unroll
-    for (int i = 0; i < kLargeTiles; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        th[i][r] = a.theta ? load_run<true, 1>(a.theta, place(i, r), live_of(i, r)) : Run<1>{};
+  for (int t = 0; t < T; ++t)
 #pragma unroll
     for (int i = 0; i < kLargeTiles; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        update_run<true, 1>(a, p, place(i, r), live_of(i, r), Run<1>{{float(d[i][t][r])}}, th[i][r]);
-  }
+        th[t][i][r] = a.theta ? load_run<true, 1>(a.theta, place(t, i, r), live_of(t, i, r)) : Run<1>{};
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int i = 0; i < kLargeTiles; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        update_run<true, 1>(a, p, place(t, i, r), live_of(t, i, r), Run<1>{{float(d[i][t][r])}},
+                            th[t][i][r]);
 }
 
 // u of a workgroup's long rows into LDS, four values of a lane at a time along memory.
