@@ -50,7 +50,7 @@ __device__ __forceinline__ float normal_cdf(float z, float &e) {
 // where 1 + tanh cancels.
 template <int act>
 __device__ __forceinline__ float activated(float z) {
-  if (act == kActRelu) return fmaxf(z, 0.0f);
+  if (act == kActRelu) return z <= 0.0f ? 0.0f : z;          // (a NaN stays one)
   if (act == kActSilu) return z * sigmoid(z);
   if (act == kActGeluTanh) return z * sigmoid(kGeluTwo * __builtin_fmaf(kGeluCube * z * z, z, z));
   if (act == kActGelu) {
@@ -66,8 +66,8 @@ __device__ __forceinline__ void activated(float z, float &f, float &df) {
   f = z;
   df = 1.0f;
   if (act == kActRelu) {
-    f = fmaxf(z, 0.0f);
-    df = z > 0.0f ? 1.0f : 0.0f;
+    f = z <= 0.0f ? 0.0f : z;
+    df = z <= 0.0f ? 0.0f : 1.0f;
   }
   if (act == kActSilu) {
     const float s = sigmoid(z);

@@ -173,6 +173,26 @@ def test_against_the_oracle_with_adapter_options(M, dt):
     assert torch.equal(c.run("none", False, False, False, lora=(2.0, 0.5, keep))[1], plain)
 
 
+@pytest.mark.parametrize("M", [3, 140])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_nan_stays_one(M, dt):
+    """A NaN before the end, or in one of its operands, is a NaN in Y there and
+    nowhere else, whatever the activation."""
+    torch, _ = torch_dev()
+    c = Case(M, 256, 192, 8, dt)
+    want = torch.zeros(M, 192, dtype=torch.bool)
+    c.bias[5] = c.mul[1, 70] = c.res[M - 1, 191] = float("nan")
+    want[:, 5] = want[1, 70] = want[M - 1, 191] = True
+    for kind in ACTS:
+        Y, Z, _ = c.run(kind, True, True, True)
+        assert torch.equal(Y.isnan().cpu(), want), kind
+        assert Z[:, 5].isnan().all() and Z.isnan().sum() == M
+        # and the gradient's: what the loss has of it must not look sound
+        dZ, dm, db = _bwd(Z, c.mul, c.res, kind, dt)
+        assert dm[:, 5].isnan().all(), kind
+        assert dZ[1, 70].isnan() and dZ[M - 1, 191].isnan() and db[191].isnan()
+
+
 def test_no_tokens():
     c = Case(4, 256, 192, 8)
     L = c.L
