@@ -446,7 +446,8 @@ qlora_status qlora_adam_step(float *theta, const float *grad, float *m, float *v
  *   orthogonalises grad.
  * m, u and theta are fp32 as written (each operation rounded), everything
  * between u and X is fp64, X is rounded to fp32 once.  A call's matrices may
- * differ in shape and must not overlap one another; the shorter side is at
+ * differ in shape; neither they nor a matrix's own arrays may overlap.  A matrix
+ * with a value that is not finite gets NaN throughout.  The shorter side is at
  * most QLORA_MAX_RANK, the longer at most 2^24, and pointers need their
  * element's alignment only (16 bytes, and an inner size that is a multiple of
  * 4, are faster).  A matrix's bits may depend on the other shapes of its call.
@@ -602,8 +603,8 @@ size_t qlora_token_top_workspace_bytes(int64_t T, int64_t V, qlora_dtype dt, int
  *     token is skipped, whatever its other inputs hold; NULL: all 1).
  *   ids [T, k] int32, teacher [T, k] fp32; t_j = -inf is q_j = 0.
  *   kl [T] fp32 (output; 0 for a skipped token); dlogits as in
- *   qlora_token_logp_bwd, also in place; 0 in the rows that are skipped or
- *   have no q_j > 0.
+ *   qlora_token_logp_bwd, also in place (then ldd = ld); 0 in the rows that are
+ *   skipped or have no q_j > 0.
  * A word with q_j > 0 that the row cannot give (-inf) makes its kl infinite;
  * its gradient is that of the formula.
  * 1 <= k <= QLORA_MAX_TOP.  ws: qlora_distill_workspace_bytes(T, V, dt, k) bytes

@@ -909,6 +909,8 @@ qlora_status qlora_distill_logits(const void *logits, int64_t ld, int64_t T, int
   qlora_status st = check_logits(ld, T, V, dt, scale);
   if (st != QLORA_OK) return st;
   if (ldd < V || ldd > kMaxLd || k < 1 || k > kMaxTop) return QLORA_ERR_SHAPE;
+  // in place a row's gradient must not reach the next row's logits
+  if (logits == dlogits && T > 1 && ldd != ld) return QLORA_ERR_SHAPE;
   if (!loss || (T > 0 && (!logits || !ids || !teacher || !kl || !dlogits))) return QLORA_ERR_NULL;
   if (!aligned_el(logits, dt) || !aligned_el(dlogits, dt) || !aligned_to(weight, 4) ||
       !aligned_to(ids, 4) || !aligned_to(teacher, 4) || !aligned_to(loss, 4) ||

@@ -58,6 +58,8 @@ def test_distill_refusals():
     assert f(*_swap(a, dx=P + 2, dt=q.F32)) == 3
     assert f(*_swap(a, ws=None)) == 1 and f(*_swap(a, n=n - 1)) == 5
     assert f(*_swap(a, T=0, loss=None)) == 1
+    # in place, rows of another pitch would overwrite logits that are still to be read
+    assert f(*_swap(a, ldd=V + 8)) == 2 and f(*_swap(a, ld=V + 8)) == 2
 
 
 def test_workspaces():
