@@ -198,6 +198,69 @@ def test_many_matrices_of_all_sizes():
     run(mats)
 
 
+def test_the_most_matrices_of_a_call():
+    """A full table, single values and small matrices."""
+    g = np.random.default_rng(6)
+    mats = [Mat(*map(int, g.integers(1, 20, 2)), seed=i) for i in range(q.MUON_MAX_MATS)]
+    say(f"[muon] {len(mats)} matrices")
+    run(mats, check=False)
+    for m in mats[:40] + mats[2000:2040] + mats[-40:]:
+        m.check(0.02, 0.95, True, 0.01, 1e-7, 5, q.MUON_COEF)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (90, 12), (12, 500), (300, 40), (60, 300), (300, 130)])
+def test_a_value_that_is_not_finite(rows, cols, value):
+    """It has no norm: the whole update is NaN, and no other matrix's."""
+    torch, _ = torch_dev()
+    m, other = Mat(rows, cols), Mat(rows, cols, seed=2)
+    m.tg[rows * cols // 2] = value
+    run([m, other], check=False)
+    n = rows * cols
+    assert m.tu[:n].isnan().all() and m.tt[:n].isnan().all()
+    other.check(0.02, 0.95, True, 0.01, 1e-7, 5, q.MUON_COEF)
+
+
+@pytest.mark.parametrize("rows,cols", [(256, 1 << 24), (1 << 24, 256), (64, (1 << 24) - 1),
+                                       ((1 << 24) - 3, 90)])
+def test_the_longest_matrices(rows, cols):
+    """The longest long sides, past 2^32 values: zero but for 120 long rows (the
+    ends among them), which are a small matrix's, and so is the step of them."""
+    torch, dev = torch_dev()
+    say(f"[muon] {rows}x{cols}")
+    k, n, wide = min(rows, cols), max(rows, cols), rows < cols
+    g = np.random.default_rng(7)
+    at = np.unique(np.concatenate([[0, 1, n - 2, n - 1], g.integers(0, n, 116)]))
+    small = Mat(*((k, len(at)) if wide else (len(at), k)), scale=1.0)
+    at = torch.from_numpy(at).to(dev)
+    t = [torch.zeros(rows, cols, device=dev) for _ in range(3)]
+    part = lambda x: x[:, at] if wide else x[at]  # noqa: E731
+    for x, v in zip(t, (small.g, small.m, small.th)):
+        v = torch.from_numpy(v).to(dev)
+        if wide:
+            x[:, at] = v
+        else:
+            x[at] = v
+    update = torch.full((rows, cols), 7.0, device=dev)
+    arr = q.muon_mats([q.muon_mat(rows, cols, *t, None, update)])
+    need = q.qlora_muon_workspace_bytes(arr)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    q.qlora_muon_step(arr, 0.02, ws, need, weight_decay=0.01)
+    torch.cuda.synchronize()
+    for x, name in zip((t[0], t[1], t[2], update), ("tg", "tm", "tt", "tu")):
+        a = getattr(small, name)
+        a[:small.rows * small.cols] = part(x).reshape(-1)
+        # nothing elsewhere (0 in, 0 out)
+        if wide:
+            x[:, at] = 0
+        else:
+            x[at] = 0
+        for r in range(0, rows, max(1, rows // 16)):
+            assert not x[r:r + max(1, rows // 16)].any(), name
+    small.tc = None
+    small.check(0.02, 0.95, True, 0.01, 1e-7, 5, q.MUON_COEF)
+
+
 def test_steps_follow_each_other():
     """Five steps in place, momentum and theta carried on."""
     mats = [Mat(300, 16), Mat(16, 200), Mat(200, 72)]
