@@ -291,6 +291,26 @@ def test_outputs_left_out(dt):
     assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])
 
 
+@pytest.mark.parametrize("M,n", [(1 << 24, 64), (2500, 1 << 19)])
+def test_gradient_far_into_memory(M, n):
+    """Arrays past 2^32 bytes; the ReLU's gradient has one rounding at most."""
+    torch, dev = torch_dev()
+    say(f"[ep bwd] {M}x{n}")
+    g = torch.Generator(dev)
+    g.manual_seed(1)
+    Z, mul, dY = (torch.randn(M, n, generator=g, device=dev) for _ in range(3))
+    dZ, dm, db = _bwd(Z, mul, dY, "relu", "f32")
+    assert torch.equal(dm, dY * Z.clamp(min=0))
+    dY *= Z > 0
+    dY *= mul                                          # now dZ
+    assert torch.equal(dZ, dY)
+    # fp32 over a lane's rows of a slab (1/8 or more of 65536 or 32), fp64 from there on
+    for c in range(0, n, 1 << 19):
+        want = dZ[:, c:c + (1 << 19)].double()
+        tol = 8192 * U * want.abs().sum(0) + U * want.sum(0).abs()
+        assert ((db[c:c + (1 << 19)].double() - want.sum(0)).abs() <= tol).all()
+
+
 def test_no_tokens_gradient():
     torch, dev = torch_dev()
     db = torch.full((128,), 3.0, device=dev)
