@@ -19,6 +19,7 @@
 // Launches: Gram partials over slabs of the long side (and the momentum); their
 // sum; the k x k iterations, in one workgroup's LDS for k <= 64, else by
 // 16 x 16 tiles, one launch a product; the last product and the update.
+#include <algorithm>
 #include <type_traits>
 
 #include "objective.h"
@@ -167,6 +168,21 @@ struct MuonChunk {
   MuonMat mats[kMuonChunk];
 };
 
+// Where the first launches find the matrices: in the table, or, of a call of a
+// few, in their arguments; the Gram kernels then leave them in the table.
+constexpr int kMuonFew = 16;
+struct MuonFew {
+  MuonMat mats[kMuonFew];
+  MuonMat *table;
+  __device__ __forceinline__ const MuonMat &operator[](unsigned i) const { return mats[i]; }
+  __device__ __forceinline__ void leave(unsigned i) const { table[i] = mats[i]; }
+};
+struct MuonTable {
+  const MuonMat *table;
+  __device__ __forceinline__ const MuonMat &operator[](unsigned i) const { return table[i]; }
+  __device__ __forceinline__ void leave(unsigned) const {}
+};
+
 // A wavefront's 16 long rows of one block of T tiles as the products' operands:
 // x[s][t] is tile t's of product s.
 template <bool WIDE, bool Q, bool kStep, int T>
@@ -270,11 +286,10 @@ __device__ __forceinline__ void gram_rows(const MuonMat &a, const MuonParams &p,
 
 // ONE: k <= 64.  Q: matrices of 16-byte accesses, or the others (whose loads take
 // more registers).
-template <bool ONE, bool Q>
-__global__ __launch_bounds__(kGramThreads, 2) void gram_kernel(const MuonMat *table, MuonParams p,
-                                                            double *ws) {
+template <bool ONE, bool Q, class Mats>
+__global__ __launch_bounds__(kGramThreads, 2) void gram_kernel(Mats mats, MuonParams p, double *ws) {
   __shared__ double sum[kPairDoubles];
-  const MuonMat a = table[blockIdx.z];
+  const MuonMat a = mats[blockIdx.z];
   if ((a.k <= 64) != ONE || bool(a.quads) != Q || int(blockIdx.x) >= a.splits ||
       int(blockIdx.y) >= pairs_of(a.k))
     return;
@@ -322,6 +337,7 @@ __global__ __launch_bounds__(kGramThreads, 2) void gram_kernel(const MuonMat *ta
     const int i = e >> 10, j = (e >> 8) & 3;
     if (i < b.tiles && j < c.tiles && (bi != bj || i <= j)) out[e] = sum[e];
   }
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) mats.leave(blockIdx.z);
 }
 
 // The table of the call's matrices, which the other launches read.
@@ -331,8 +347,9 @@ __global__ __launch_bounds__(64) void table_kernel(MuonChunk c, MuonMat *table) 
 
 // The momentum of matrices of k > 64, whose values several wavefronts read, and
 // (Nesterov) their direction.
-__global__ __launch_bounds__(256) void momentum_kernel(const MuonMat *table, MuonParams p) {
-  const MuonMat a = table[blockIdx.y];
+template <class Mats>
+__global__ __launch_bounds__(256) void momentum_kernel(Mats mats, MuonParams p) {
+  const MuonMat a = mats[blockIdx.y];
   if (a.k <= 64 || !a.m) return;
   const int64_t all = a.n * a.k, step = int64_t(gridDim.x) * 1024;
   for (int64_t first = int64_t(blockIdx.x) * 1024; first < all; first += step) {
@@ -439,13 +456,13 @@ __global__ __launch_bounds__(256) void tiny_kernel(const MuonMat *table, MuonPar
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double *area = ws + a.area;
   double v = 0.0;                                      // register `wave` of this lane
-  for (int q = 0; q < a.splits; q += 16) {
-    double w[16];
+  for (int q = 0; q < a.splits; q += 32) {
+    double w[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 32; ++i)
       w[i] = area[int64_t(q + i < a.splits ? q + i : q) * kPairDoubles + threadIdx.x];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += q + i < a.splits ? w[i] : 0.0;
+    for (int i = 0; i < 32; ++i) v += q + i < a.splits ? w[i] : 0.0;
   }
   part[wave][lane] = v;
   __syncthreads();
@@ -648,7 +665,8 @@ __global__ __launch_bounds__(Small<NT>::threads) void small_kernel(const MuonMat
 // A workgroup owns one 16 x 16 tile of the upper triangle of a
 // product, its four wavefronts a quarter of the sum each; operands come from
 // L2 (both symmetric, so every fragment is four runs of 128 bytes).
-enum MuonStage { kSquare, kPolynomial, kAdvance };
+// kLast is the last iteration's Q P, with P formed where it is read.
+enum MuonStage { kSquare, kPolynomial, kAdvance, kLast };
 
 // A quarter of the operands of a tile of columns 16 t ..: kp / 16 steps of four
 // rows, all requested before the first is used (past them the last ones again,
@@ -738,19 +756,29 @@ __device__ __forceinline__ void stage_tile(const MuonMat &a, const MuonParams &p
       inv = inverse_norm(norm, p.eps);
       f = inv * inv;
     }
-    const bool last = it + 1 == p.steps;
     const double g = f * m.G[ij], s = f * f * m.S[ij];
     const double v = (i == j ? p.a : 0.0) + p.b * g + p.c * s;
     put(m.P, v);
     if (it == 0) put(m.Q1, inv * v);
-    if (!last)
+    if (p.steps > 1)
       put(m.H, p.a * g + p.b * s +
                    p.c * (f * f * f *
                           joined_part(part_product(x, y, kp), wave, red)));
     return;
   }
-  // kAdvance: G <- H P (but the last time) or, past the first, Q' = Q P
-  if (second ? it == 0 : it + 1 == p.steps) return;
+  if (stage == kLast) {
+    const Quarter<N> x(m.Q(it), kp, ti, wave), g(m.G, kp, tj, wave);
+    Quarter<N> y(m.S, kp, tj, wave);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const bool diagonal = 4 * (wave * (kp / 16) + e) + (lane >> 4) == 16 * tj + (lane & 15);
+      y.v[e] = (diagonal ? p.a : 0.0) + p.b * g.v[e] + p.c * y.v[e];
+    }
+    put(m.Q(it + 1), joined_part(part_product(x, y, kp), wave, red));
+    return;
+  }
+  // kAdvance: G <- H P or, past the first, Q' = Q P
+  if (second && it == 0) return;
   const Quarter<N> x(second ? m.Q(it) : m.H, kp, ti, wave), y(m.P, kp, tj, wave);
   put(second ? m.Q(it + 1) : m.G, joined_part(part_product(x, y, kp), wave, red));
 }
@@ -1239,8 +1267,8 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
   int most_k = 0;
   bool small[5] = {};
   auto raise = [](int64_t &to, int64_t v) { to = v > to ? v : to; };
+  MuonChunk c;
   for (int32_t i = 0; i < n; i += kMuonChunk) {
-    MuonChunk c;
     c.count = n - i < kMuonChunk ? n - i : kMuonChunk;
     c.first = i;
     for (int j = 0; j < c.count; ++j) {
@@ -1258,22 +1286,33 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
         if (a.m) raise(values, a.n * a.k);
       }
     }
-    hipLaunchKernelGGL(table_kernel, dim3(1), dim3(64), 0, s, c, table);
+    if (n > kMuonFew) hipLaunchKernelGGL(table_kernel, dim3(1), dim3(64), 0, s, c, table);
   }
-  if (values) {
-    const int64_t b = (values + 1023) / 1024;
-    hipLaunchKernelGGL(momentum_kernel, dim3(unsigned(b < 1024 ? b : 1024), unsigned(n)), dim3(256), 0,
-                       s, table, p);
-  }
-#define QLORA_GRAM(ONE, Q, X, Y)                                                       \
-  if (X)                                                                               \
-    hipLaunchKernelGGL((gram_kernel<ONE, Q>), dim3(unsigned(X), unsigned(Y), unsigned(n)), \
-                       dim3(kGramThreads), 0, s, table, p, ws)
-  QLORA_GRAM(true, true, splits[1], 1);
-  QLORA_GRAM(true, false, splits[0], 1);
-  QLORA_GRAM(false, true, splits_large[1], pairs_of(most_k));
-  QLORA_GRAM(false, false, splits_large[0], pairs_of(most_k));
+  auto first = [&](auto mats) {
+    using Mats = decltype(mats);
+    if (values) {
+      const int64_t b = (values + 1023) / 1024;
+      hipLaunchKernelGGL((momentum_kernel<Mats>), dim3(unsigned(b < 1024 ? b : 1024), unsigned(n)),
+                         dim3(256), 0, s, mats, p);
+    }
+#define QLORA_GRAM(ONE, Q, X, Y)                                                               \
+  if (X)                                                                                       \
+    hipLaunchKernelGGL((gram_kernel<ONE, Q, Mats>), dim3(unsigned(X), unsigned(Y), unsigned(n)), \
+                       dim3(kGramThreads), 0, s, mats, p, ws)
+    QLORA_GRAM(true, true, splits[1], 1);
+    QLORA_GRAM(true, false, splits[0], 1);
+    QLORA_GRAM(false, true, splits_large[1], pairs_of(most_k));
+    QLORA_GRAM(false, false, splits_large[0], pairs_of(most_k));
 #undef QLORA_GRAM
+  };
+  if (n <= kMuonFew) {
+    MuonFew few{};
+    std::copy(c.mats, c.mats + n, few.mats);
+    few.table = table;
+    first(few);
+  } else {
+    first(MuonTable{table});
+  }
   const dim3 pairs(16, unsigned(pairs_of(most_k)), unsigned(n));
   if (most_k > 16) hipLaunchKernelGGL(gram_sum_kernel, pairs, dim3(256), 0, s, table, ws);
 #define QLORA_SMALL(NT)                                                                 \
@@ -1298,9 +1337,10 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
                          ws, stage, it, n, jobs);
     };
     for (int it = 0; it < p.steps; ++it) {
+      const bool last = it > 0 && it + 1 == p.steps;
       go(kSquare, it);
-      go(kPolynomial, it);
-      if (p.steps > 1) go(kAdvance, it);
+      go(last ? kLast : kPolynomial, it);
+      if (p.steps > 1 && !last) go(kAdvance, it);
     }
   }
 #define QLORA_APPLY(NT, Q)                                                                     \
