@@ -79,7 +79,8 @@ __device__ __forceinline__ void activated(float z, float &f, float &df) {
     f = z * s;
     // past 30, s (1 - s) is 0 and z^2 may be infinite
     const float c = fminf(fabsf(z), 30.0f);
-    df = __builtin_fmaf(f * (1.0f - s), kGeluTwo * __builtin_fmaf(3.0f * kGeluCube * c, c, 1.0f), s);
+    df = __builtin_fmaf(f * (1.0f - s),
+                        kGeluTwo * __builtin_fmaf(3.0f * kGeluCube * c, c, 1.0f), s);
   }
   if (act == kActGelu) {
     float e;

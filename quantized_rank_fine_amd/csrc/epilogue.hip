@@ -6,6 +6,9 @@
 // over a lane's rows of the slab, fp64 from there on) leave as partials that a
 // second launch adds in a fixed order, or as dbias where there is one slab.
 // dZ enters the sums before it is rounded.
+// 2048 x 11008 bf16, SiLU with a factor: 36 us, 6.3 TB/s of 226 MB (a copy
+// reaches 5.1), 43 with the launch's own; 509 x 4096 fp32, GELU with a bias: 6.6
+// and 2.4, 25 MB, latency.
 #include "epilogue.h"
 
 namespace qlora {
@@ -104,7 +107,8 @@ __global__ __launch_bounds__(kThreads) void bias_sum_kernel(const double *partia
 
 }  // namespace
 
-// 64 rows of up to 128, else 32, or more where there would be more than 256 slabs.
+// 64 rows of up to 128 (one or two slabs), else 32, or more where there would be
+// more than 256 slabs (509 x 4096 fp32 with 64: 13.0 us, with 32: 9.8).
 int64_t ep_bwd_slab(int64_t M) {
   if (M <= 128) return 64;
   const int64_t most = ((M + 255) / 256 + 31) / 32 * 32;

@@ -17,8 +17,18 @@
 // would leave O two decimals).  O is rounded to fp32 once.
 //
 // Launches: Gram partials over slabs of the long side (and the momentum); their
-// sum; the k x k iterations, in one workgroup's LDS for k <= 64, else by
-// 16 x 16 tiles, one launch a product; the last product and the update.
+// sum; the k x k iterations, in one wavefront for k <= 16, in one workgroup's LDS
+// for k <= 64, else by 16 x 16 tiles, one launch a product; the last product and
+// the update.
+//
+// What bounds them (copy rate 5.1 TB/s, fp64 matrix products 74 TFLOP/s; traced):
+//   64 of 4096 x 64: 173 us, of them Gram 43 (226 MB, 5.2 TB/s), iterations 38
+//     (a chain of 18 products of 64^3 on one CU a matrix, about 23 by the matrix
+//     cores), update 72 (320 MB, 4.4 TB/s).
+//   4 of rank 200 (11008 and 4096): 250 us, of them momentum 15 (6.3 TB/s), Gram
+//     57 (fp64: 19 by the matrix cores), 14 launches of iterations 6.3 each
+//     (latency), update 77 (fp64: 35 by the matrix cores, and Q from L2).
+//   2 of 4096 x 16: 19 us, three launches of 6 to 7 that wait for each other.
 #include <algorithm>
 #include <type_traits>
 
@@ -28,8 +38,9 @@
 namespace qlora {
 namespace {
 
-// A matrix in the kernels: n long, k short; quads: 16-byte accesses.  span: long rows to a Gram workgroup,
-// `splits` of them; apply: long rows to an update workgroup (k <= 64); area: where its fp64 scratch begins.  u: the direction, of
+// A matrix in the kernels: n long, k short; quads: 16-byte accesses.  span: long
+// rows to a Gram workgroup, `splits` of them; apply: long rows to an update
+// workgroup (k <= 64); area: where its fp64 scratch begins.  u: the direction, of
 // k > 64 (grad, m or an array of its own).
 struct MuonMat {
   const float *grad, *u;
@@ -135,9 +146,9 @@ __device__ __forceinline__ void with_tiles(int t, F &&f) {
 //     consecutive long rows 4 g .. of column 16 t + c, one for each of four
 //     products.
 // The momentum is advanced on the way where one wavefront sees every value
-// (k <= 64), else by a pass of its own before, which also leaves u.  The four wavefronts of a
-// workgroup share a slab's rows and leave the sum of theirs, [pair][tile][
-// register][lane] in fp64, tile = 4 ti + tj.
+// (k <= 64), else by a pass of its own before, which also leaves u.  The four
+// wavefronts of a workgroup share a slab's rows and leave the sum of theirs,
+// [pair][tile][register][lane] in fp64, tile = 4 ti + tj.
 struct Block {
   int first, tiles, width;                     // columns first .. first + width - 1
 };
@@ -169,7 +180,8 @@ struct MuonChunk {
 };
 
 // Where the first launches find the matrices: in the table, or, of a call of a
-// few, in their arguments; the Gram kernels then leave them in the table.
+// few, in their arguments; the Gram kernels then leave them in the table, and the
+// launch that fills it is spared (2 of 4096 x 16: 21.8 -> 19.0 us).
 constexpr int kMuonFew = 16;
 struct MuonFew {
   MuonMat mats[kMuonFew];
@@ -212,7 +224,8 @@ struct GramRows<false, Q, kStep, T> {
     for (int s = 0; s < 4; ++s) {
 #pragma unroll
       for (int t = 0; t < T; ++t)
-        x[s][t] = double(kStep ? direction<true>(p, a.m != nullptr, g[s].v[t], m[s].v[t]) : g[s].v[t]);
+        x[s][t] =
+            double(kStep ? direction<true>(p, a.m != nullptr, g[s].v[t], m[s].v[t]) : g[s].v[t]);
       if (kStep && a.m) store_run<Q, T>(a.m, at[s], live[s], m[s]);
     }
   }
@@ -240,7 +253,8 @@ struct GramRows<true, Q, kStep, T> {
     for (int t = 0; t < T; ++t) {
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        x[s][t] = double(kStep ? direction<true>(p, a.m != nullptr, g[t].v[s], m[t].v[s]) : g[t].v[s]);
+        x[s][t] =
+            double(kStep ? direction<true>(p, a.m != nullptr, g[t].v[s], m[t].v[s]) : g[t].v[s]);
       if (kStep && a.m) store_run<Q, 4>(a.m, at[t], live[t], m[t]);
     }
   }
@@ -287,7 +301,8 @@ __device__ __forceinline__ void gram_rows(const MuonMat &a, const MuonParams &p,
 // ONE: k <= 64.  Q: matrices of 16-byte accesses, or the others (whose loads take
 // more registers).
 template <bool ONE, bool Q, class Mats>
-__global__ __launch_bounds__(kGramThreads, 2) void gram_kernel(Mats mats, MuonParams p, double *ws) {
+__global__ __launch_bounds__(kGramThreads, 2) void gram_kernel(Mats mats, MuonParams p,
+                                                               double *ws) {
   __shared__ double sum[kPairDoubles];
   const MuonMat a = mats[blockIdx.z];
   if ((a.k <= 64) != ONE || bool(a.quads) != Q || int(blockIdx.x) >= a.splits ||
@@ -395,7 +410,8 @@ __global__ __launch_bounds__(256) void gram_sum_kernel(const MuonMat *table, dou
   if (i >= block_of(a.k, bi, a.wide).tiles || j >= block_of(a.k, bj, a.wide).tiles ||
       (bi == bj && i > j))
     return;
-  double *x = ws + a.area + int64_t(blockIdx.y) * kPairDoubles + int(blockIdx.x) * 256 + threadIdx.x;
+  double *x =
+      ws + a.area + int64_t(blockIdx.y) * kPairDoubles + int(blockIdx.x) * 256 + threadIdx.x;
   const int64_t n = int64_t(pairs) * kPairDoubles;
   double s = 0.0;
   for (int b = 0; b < a.splits; b += 8) {
@@ -493,9 +509,9 @@ __global__ __launch_bounds__(256) void tiny_kernel(const MuonMat *table, MuonPar
 // 16 < k <= 64: one workgroup, three matrices in LDS: G, S (then P), Q, as tiles
 // of registers ([tile][register][lane ^ 4 register], tile = NT ti + tj), so that
 // an operand is one contiguous read and a tile's mirror image goes to all banks
-// (without the exchange it goes to 8 of 32, and storing took half the time).  A product's tiles of the upper triangle are dealt
-// over the wavefronts, kept in registers until every read is done, and stored
-// with their mirror images.
+// (without the exchange it goes to 8 of 32, and storing took half the time).  A
+// product's tiles of the upper triangle are dealt over the wavefronts, kept in
+// registers until every read is done, and stored with their mirror images.
 template <int NT>
 struct Small {
   static constexpr int kp = 16 * NT, tiles = NT * (NT + 1) / 2, size = kp * kp;
@@ -662,16 +678,18 @@ __global__ __launch_bounds__(Small<NT>::threads) void small_kernel(const MuonMat
 
 // ------------------------------------------------ k x k iterations, k > 64
 //
-// A workgroup owns one 16 x 16 tile of the upper triangle of a
-// product, its four wavefronts a quarter of the sum each; operands come from
-// L2 (both symmetric, so every fragment is four runs of 128 bytes).
+// A workgroup owns one 16 x 16 tile of the upper triangle of a product, its four
+// wavefronts a quarter of the sum each; operands come from L2 (both symmetric, so
+// every fragment is four runs of 128 bytes).  A launch is latency: 4 matrices of
+// rank 200 take 4.5 to 6.3 us, of which 0.3 are products.
 // kLast is the last iteration's Q P, with P formed where it is read.
 enum MuonStage { kSquare, kPolynomial, kAdvance, kLast };
 
 // A quarter of the operands of a tile of columns 16 t ..: kp / 16 steps of four
 // rows, all requested before the first is used (past them the last ones again,
-// which the products leave out).
-template <int N>                              // kp <= 16 N
+// which the products leave out).  kp <= 16 N; N = 8 where it does (30 of rank 128,
+// a launch 9.9 -> 7.4 us).
+template <int N>
 struct Quarter {
   double v[N];
   __device__ __forceinline__ Quarter(const double *M, int kp, int t, int wave) {
@@ -705,7 +723,8 @@ __device__ __forceinline__ double joined_part(f64x4_t d, int wave, double (*red)
 
 // A matrix's tiles are dealt to as few of the 8 XCDs as fill the chip (workgroups
 // go round them), so that each L2 fetches only its own matrices: matrix m is on
-// XCD m % 8, or on 8 / n neighbouring ones where there are fewer than 8.
+// XCD m % 8, or on 8 / n neighbouring ones where there are fewer than 8 (4 of
+// rank 200, a launch: 6.6 -> 6.4 us).
 __device__ __forceinline__ void stage_job(int n, int tiles, int &which, int &t) {
   const int x = int(blockIdx.x) % 8, slot = int(blockIdx.x) / 8;
   if (n >= 8) {
@@ -796,8 +815,10 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
   const bool second = t >= NT * (NT + 1) / 2;              // (kAdvance: the other product)
   if (second) t -= NT * (NT + 1) / 2;
   if (t >= NT * (NT + 1) / 2 || (second && stage != kAdvance)) return;
-  if (kp <= 128) stage_tile<8>(a, p, ws, stage, it, kp, t, second, red, norm);
-  else stage_tile<16>(a, p, ws, stage, it, kp, t, second, red, norm);
+  if (kp <= 128)
+    stage_tile<8>(a, p, ws, stage, it, kp, t, second, red, norm);
+  else
+    stage_tile<16>(a, p, ws, stage, it, kp, t, second, red, norm);
 }
 
 // ------------------------------------------------------------ the update
@@ -805,7 +826,7 @@ __global__ __launch_bounds__(256) void stage_kernel(const MuonMat *table, MuonPa
 // O = u Q and theta's step.  The operands and results of a product are again
 // chosen for the memory: u comes straight into registers, four values of a lane
 // at a time, and a lane's results of all tiles are neighbours.
-//
+
 // A value's step from its X.
 __device__ __forceinline__ float stepped(const MuonParams &p, float scale, float th, float x) {
   return th - p.lr * (scale * x + p.wd * th);
@@ -830,7 +851,8 @@ __device__ __forceinline__ void update_run(const MuonMat &a, const MuonParams &p
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i < live) (a.theta16 + at.base)[at.lane + i] = __builtin_bit_cast(uint16_t, (__bf16)th.v[i]);
+      if (i < live)
+        (a.theta16 + at.base)[at.lane + i] = __builtin_bit_cast(uint16_t, (__bf16)th.v[i]);
   }
 }
 
@@ -1023,8 +1045,9 @@ __device__ __forceinline__ void apply_wide(const MuonMat &a, const MuonParams &p
 }
 
 template <int NT, bool ALIGNED>
-__global__ __launch_bounds__(256, ALIGNED ? 2 : 1) void apply_kernel(const MuonMat *table, MuonParams p,
-                                                    const double *ws) {
+__global__ __launch_bounds__(256, ALIGNED ? 2 : 1) void apply_kernel(const MuonMat *table,
+                                                                     MuonParams p,
+                                                                     const double *ws) {
   using F = Factor<NT>;
   __shared__ __align__(16) double shared[F::held ? 1 : F::K * F::pitch];
   const MuonMat a = table[blockIdx.y];
@@ -1051,7 +1074,8 @@ __global__ __launch_bounds__(256, ALIGNED ? 2 : 1) void apply_kernel(const MuonM
 
 // k > 64: 32 long rows of u in LDS (fp32) for a workgroup, each of whose NB
 // wavefronts forms a block of 64 columns of O; Q comes from L2, each value once
-// a workgroup, requested a product ahead.
+// a workgroup, requested a product ahead.  4 of rank 200: 77 us; with 64 rows,
+// which halve the reads of Q but leave half the workgroups to a CU, 19 more.
 constexpr int kLargeRows = 32, kLargeTiles = kLargeRows / 16;
 
 // LDS row pitch (floats): 17 past a multiple of 64, so that a fragment (16 rows
@@ -1126,7 +1150,8 @@ __device__ __forceinline__ void large_block(const MuonMat &a, const MuonParams &
     for (int i = 0; i < kLargeTiles; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        th[t][i][r] = a.theta ? load_run<true, 1>(a.theta, place(t, i, r), live_of(t, i, r)) : Run<1>{};
+        th[t][i][r] = a.theta ? load_run<true, 1>(a.theta, place(t, i, r), live_of(t, i, r))
+                              : Run<1>{};
 #pragma unroll
   for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -1333,8 +1358,8 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
     const int tiles = NT * (NT + 1) / 2;
     auto go = [&](int stage, int it) {
       const int jobs = stage == kAdvance ? 2 * tiles : tiles;
-      hipLaunchKernelGGL(stage_kernel, dim3(unsigned(stage_grid(n, jobs))), dim3(256), 0, s, table, p,
-                         ws, stage, it, n, jobs);
+      hipLaunchKernelGGL(stage_kernel, dim3(unsigned(stage_grid(n, jobs))), dim3(256), 0, s, table,
+                         p, ws, stage, it, n, jobs);
     };
     for (int it = 0; it < p.steps; ++it) {
       const bool last = it > 0 && it + 1 == p.steps;
