@@ -1244,13 +1244,14 @@ MuonMat planned(const qlora_muon_mat &q, int64_t span0, bool nesterov, double *w
   const int kp = padded(a.k);
   // a slab's k x k partial sums stay a small part of what it reads; of k > 64 a
   // slab is a workgroup to every pair of blocks
-  const int64_t most = a.k <= 64 ? span0 : span0 * pairs_of(a.k);
+  const int64_t most = a.k <= 16 ? span0 * 2 / 3 : a.k <= 64 ? span0 : span0 * pairs_of(a.k);
   const int64_t span = most < kp / 2 ? kp / 2 : most;
   a.span = (span + kGramRows - 1) / kGramRows * kGramRows;
   a.splits = int32_t((a.n + a.span - 1) / a.span);
   // one round of workgroups, each of which reads Q once (256 or 512 rows of 64
   // adapters of 4096 x 64: 77.4 and 70.5 us)
-  a.apply = span0 < 1024 ? (span0 + 127) / 128 * 128 : 1024;
+  const int64_t rows = kp <= 16 ? 128 : 1024;
+  a.apply = span0 < rows ? (span0 + 127) / 128 * 128 : rows;
   a.area = o;
   const int64_t first = int64_t(pairs_of(a.k)) * kPairDoubles, sq = int64_t(kp) * kp;
   o += a.splits * first;
