@@ -1242,14 +1242,19 @@ MuonMat planned(const qlora_muon_mat &q, int64_t span0, bool nesterov, double *w
   a.quads = (a.wide ? a.n : int64_t(a.k)) % 4 == 0 && ok(a.grad, 16) && ok(a.m, 16) &&
             ok(a.theta, 16) && ok(a.theta16, 8) && ok(a.update, 16);
   const int kp = padded(a.k);
-  // a slab's k x k partial sums stay a small part of what it reads; of k > 64 a
-  // slab is a workgroup to every pair of blocks
+  // A slab's k x k partial sums stay a small part of what it reads.  512
+  // workgroups a call; of k <= 16, whose partial sums are smallest, 768, as many as
+  // the chip holds (56 of rank 16, 8888 and 2000 long: 25.3 -> 20.9 us; 64 of 4096 x
+  // 64 so: 43.3 -> 44.4; 1024 for rank 16: 26.9); of k > 64 a slab is a workgroup to
+  // every pair of blocks.
   const int64_t most = a.k <= 16 ? span0 * 2 / 3 : a.k <= 64 ? span0 : span0 * pairs_of(a.k);
   const int64_t span = most < kp / 2 ? kp / 2 : most;
   a.span = (span + kGramRows - 1) / kGramRows * kGramRows;
   a.splits = int32_t((a.n + a.span - 1) / a.span);
-  // one round of workgroups, each of which reads Q once (256 or 512 rows of 64
-  // adapters of 4096 x 64: 77.4 and 70.5 us)
+  // One round of workgroups, each of which reads Q once (256 or 512 rows of 64
+  // adapters of 4096 x 64: 77.4 and 70.5 us).  Q of k <= 16 is 2 KB and five times as
+  // many workgroups fit (1024, 256 and 128 rows of 28 of rank 8, 4096 and 11008
+  // long: 20.3, 14.5 and 11.0 us; of k <= 32, 1024 and 512: 32.7 and 33.1).
   const int64_t rows = kp <= 16 ? 128 : 1024;
   a.apply = span0 < rows ? (span0 + 127) / 128 * 128 : rows;
   a.area = o;
@@ -1263,7 +1268,7 @@ MuonMat planned(const qlora_muon_mat &q, int64_t span0, bool nesterov, double *w
   return a;
 }
 
-// Long rows to a slab, before a matrix's own bounds: 512 workgroups a call.
+// Long rows to a slab of a call with 512, before a matrix's own bounds.
 int64_t muon_span(const qlora_muon_mat *mats, int32_t n) {
   int64_t all = 0;
   for (int32_t i = 0; i < n; ++i)
