@@ -1294,7 +1294,7 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
   const int64_t span = muon_span(mats, n);
   // largest grids, by whether matrices have 16-byte accesses
   int64_t o = 0, blocks[2][5] = {}, blocks_large[5] = {}, splits[2] = {}, splits_large[2] = {};
-  int64_t values = 0;
+  int64_t values = 0, values_small = 0;
   int most_k = 0;
   bool small[5] = {};
   auto raise = [](int64_t &to, int64_t v) { to = v > to ? v : to; };
@@ -1308,6 +1308,7 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
       const int kp = padded(a.k);
       if (a.k <= 64) {
         small[kp / 16] = true;
+        values_small += a.n * a.k;
         raise(splits[a.quads], a.splits);
         const int NT = kp <= 16 ? 1 : kp <= 32 ? 2 : 4;
         raise(blocks[a.quads][NT], (a.n + a.apply - 1) / a.apply);
@@ -1318,6 +1319,30 @@ hipError_t launch_muon(const qlora_muon_mat *mats, int32_t n, const MuonParams &
       }
     }
     if (n > kMuonFew) hipLaunchKernelGGL(table_kernel, dim3(1), dim3(64), 0, s, c, table);
+  }
+  // Matrices of both kinds of access cost a launch more of each kernel: the few of
+  // a short call all go without 16-byte accesses, those of k <= 64 where they are
+  // small (8 and 8 of rank 3, 82 and 1248 long: 27.4 -> 19.1 us; one adapter of 4097
+  // and 11008 x 50, 0.75 M values: 112 -> 97, but of three, 2.3 M: 123 -> 134; 4 and
+  // 4 of rank 150: 226 -> 219).
+  if (n <= kMuonFew) {
+    auto without = [&](bool small_ones) {
+      for (int i = 0; i < n; ++i)
+        if ((c.mats[i].k <= 64) == small_ones) c.mats[i].quads = 0;
+    };
+    auto join = [&](int64_t *x, int64_t *y) {
+      raise(*x, *y);
+      *y = 0;
+    };
+    if (splits[0] && splits[1] && values_small <= 3 << 19) {
+      without(true);
+      join(&splits[0], &splits[1]);
+      for (int t = 0; t < 5; ++t) join(&blocks[0][t], &blocks[1][t]);
+    }
+    if (splits_large[0] && splits_large[1]) {
+      without(false);
+      join(&splits_large[0], &splits_large[1]);
+    }
   }
   auto first = [&](auto mats) {
     using Mats = decltype(mats);

@@ -198,6 +198,17 @@ def test_many_matrices_of_all_sizes():
     run(mats)
 
 
+@pytest.mark.parametrize("sizes", [
+    [(82, 3), (3, 1248), (16, 16)], [(40, 500), (501, 40), (33, 70)], [(200, 90), (90, 201)],
+    [(60, 400), (401, 60), (300, 130), (131, 300), (7, 7)], [(40000, 50), (48, 4000)],
+    [(100, 16)] * 16, [(101, 15), (100, 16)] * 8, [(100, 16), (101, 15), (30, 100)] * 6])
+def test_calls_of_matrices_of_both_kinds_of_access(sizes):
+    """Short calls, whose matrices travel with the launch, and the first longer one;
+    aligned and not; small and large."""
+    say(f"[muon] {sizes[:5]} x {len(sizes)}")
+    run([Mat(r, c, seed=i, off=i % 2) for i, (r, c) in enumerate(sizes)])
+
+
 def test_the_most_matrices_of_a_call():
     """A full table, single values and small matrices."""
     g = np.random.default_rng(6)
