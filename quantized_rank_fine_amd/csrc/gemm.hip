@@ -936,7 +936,7 @@ __device__ __forceinline__ void epilogue_ep(f32x16_t (&acc)[2][8], char *smem, c
       *reinterpret_cast<f32x4_t *>(w) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
       *reinterpret_cast<f32x4_t *>(w + 1024) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
       *reinterpret_cast<f32x4_t *>(w + 2048) = __builtin_shufflevector(v, v, 8, 9, 10, 11);
-      *reinterpret_cast<f32x4_t *>(w + 3072) = __builtin_shufflevector(v, v, 12, 13, 14, 15);
+      *reinterpret_cast<f32x4_t *>(w + 3 * 1024) = __builtin_shufflevector(v, v, 12, 13, 14, 15);
     }
     __syncthreads();
 #pragma unroll
