@@ -161,15 +161,16 @@ def dropout_keep(rows, cols, p, seed, counter, only=None):
 
 def token_top(x, k, scale=1.0):
     """The k largest logits of each row, ties to the lower index: (ids, log p).
-    A NaN is no word."""
+    A NaN is no word: behind all others, with the id -1."""
     x = np.asarray(x, np.float64)
-    order = np.argsort(np.where(np.isnan(x), np.inf, -x), axis=1, kind="stable")[:, :k]
+    order = np.lexsort((-x, np.isnan(x)), axis=1)[:, :k]
     m = x.max(1, keepdims=True)
     m = np.where(np.isfinite(m), m, 0.0)
     with np.errstate(divide="ignore"):
         lp = scale * (x - m) - np.log(np.exp(scale * (x - m)).sum(1, keepdims=True))
     lp = np.where(x == -np.inf, -np.inf, lp)
-    return order, np.take_along_axis(lp, order, 1)
+    some = ~np.isnan(np.take_along_axis(x, order, 1))
+    return np.where(some, order, -1), np.take_along_axis(lp, order, 1)
 
 
 def distill(x, ids, teacher, weight, scale=1.0, normalize=True):

@@ -144,7 +144,7 @@ __device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF
   }
   const float least = value_of(bound);
   // All words reach -inf; of those that are -inf themselves only the first k
-  // can be among the best.
+  // can be among the best (unless some of them are NaN: fill_masked).
   const bool all = bound == kKeyLeast;
   auto offer = [&](float x, int32_t v) {
     if (x >= least && !(all && x == least && v >= k)) {
@@ -198,6 +198,37 @@ __device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF
   return list.n;
 }
 
+// A list of all the row's words but the -inf ones from word k on that is shorter
+// than k (n entries): there is a NaN among the first k words.  The next -inf words
+// go to its end, in order.  For one wavefront, or several that do the same; returns
+// the new length.  Only such rows come here; they cost the walk to as many -inf
+// words (4096 x 32000 bf16 of NaN alone, which walk to the end: 149 us, without 45).
+template <bool BF16>
+__device__ __forceinline__ int fill_masked(TopList &list, const char *row, int32_t V, int n,
+                                           int k) {
+  constexpr int N = 8;
+  const int lane = threadIdx.x % 64;
+  for (int32_t from = k; from < V && n < k; from += 64 * N) {
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int32_t v = from + 64 * i + lane;
+      x[i] = load1<BF16>(row, uint32_t(v < V ? v : V - 1));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int32_t v = from + 64 * i + lane;
+      const bool hit = v < V && x[i] == -INFINITY;
+      const uint64_t hits = __ballot(hit);
+      const int at = n + __popcll(hits & ((uint64_t(1) << lane) - 1));
+      if (hit && at < k) list.e[at] = entry_of(x[i], uint32_t(v));
+      n += __popcll(hits);
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  return n < k ? n : k;
+}
+
 // The best min(n, k) of the list's n entries to its front, in order.
 template <int threads>
 __device__ __forceinline__ void order(TopList &list, int n, int k) {
@@ -235,7 +266,7 @@ __device__ __forceinline__ void write_row(const TopRows &o, int64_t t, const Row
 }
 
 // A row's alternatives from its list's best n, which are in order (fewer than
-// k: a row of NaN).
+// k: NaN has left no more).
 template <int threads>
 __device__ __forceinline__ void write_top(const TopRows &o, int64_t t, const TopList &list, int n,
                                           const RowResult &r, float scale) {
@@ -312,6 +343,7 @@ __global__ __launch_bounds__(threads, ONE && BF16 ? 8 : 1) void top_kernel(Logit
     if (threads > 64)
       s = joined(lane < threads / 64 ? red[lane] : Stat{-INFINITY, 0.0f, 0.0f}, c);
     if (lone) {
+      if (n < o.k) n = fill_masked<BF16>(list, row, V, n, o.k);
       const RowResult r = finished<BF16, 64>(s, row, V, xy, a.scale, nullptr);
       const uint64_t e = lane < n ? list.e[lane] : 0;
       const int j = lane < n ? place_of(list, n, e) : lane;
@@ -322,6 +354,10 @@ __global__ __launch_bounds__(threads, ONE && BF16 ? 8 : 1) void top_kernel(Logit
     order<threads>(list, n, o.k);
     n = n < o.k ? n : o.k;
   } else {
+    if (n < o.k) {
+      n = fill_masked<BF16>(list, row, V, n, o.k);
+      __syncthreads();
+    }
     s = joined_block<threads>(s, c, red);
   }
   const RowResult r = finished<BF16, threads>(s, row, V, xy, a.scale, red);
@@ -388,6 +424,10 @@ __global__ __launch_bounds__(kJoinThreads) void top_join_kernel(LogitRows a, Top
     const int lane = threadIdx.x % 64;
     const uint64_t full = __ballot(lane < o.k && lane < n + take && list.e[lane] != 0);
     n = full == ~uint64_t(0) ? 64 : __ffsll((unsigned long long)~full) - 1;
+    __syncthreads();
+  }
+  if (n < o.k) {
+    n = fill_masked<BF16>(list, row_at<BF16>(a.x, t * a.ld), int32_t(a.V), n, o.k);
     __syncthreads();
   }
   const RowResult r = join_row<BF16>(a, part, segments, t, y);

@@ -84,6 +84,13 @@ def test_oracle_top():
     assert ob.token_top(np.array([[np.nan, 1.0, 2.0]]), 2)[0].tolist() == [[2, 1]]
 
 
+def test_oracle_top_of_nan_beside_a_mask():
+    """A NaN is behind a word at -inf, and no word where too few are left."""
+    n, i = np.nan, np.inf
+    x = np.array([[n, -i, -i, -i], [-i, n, 1.0, n], [n, n, n, n], [-i, n, -i, i]])
+    assert ob.token_top(x, 3)[0].tolist() == [[1, 2, 3], [2, 0, -1], [-1, -1, -1], [3, 0, 2]]
+
+
 @pytest.mark.parametrize("s", [1.0, 0.7])
 def test_oracle_distill(s):
     """Against itself the loss is 0 and so is the gradient; one alternative is

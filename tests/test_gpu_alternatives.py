@@ -163,6 +163,43 @@ def test_top_of_rows_with_nan(V):
     assert np.isnan(top).all() and np.isnan(h.cpu().numpy()).all()
 
 
+@pytest.mark.parametrize("V", [64, 300, 2049, 8191, 16000, 32003, 40007, 131077])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_top_of_nan_beside_a_mask(V, dt):
+    """NaN among the first words of rows that -inf leaves few others: as many
+    words at -inf as are asked for, the lowest, wherever they lie."""
+    torch, dev = torch_dev()
+    at = np.arange(V)
+    for k in (2, 20, 64):
+        g = np.random.default_rng(V + k)
+        masked = lambda: np.full(V, -np.inf)  # noqa: E731
+        rows = {n: masked() for n in ("first", "all of the first", "every other", "few live",
+                                      "long run", "few left", "last alone", "none", "an infinity")}
+        rows["first"][0] = np.nan
+        rows["all of the first"][:k] = np.nan
+        rows["every other"][::2] = np.nan
+        rows["few live"][g.permutation(V)[:k // 2]] = g.standard_normal(k // 2)
+        rows["few live"][:k // 2] = np.nan
+        rows["long run"][:V - 70] = np.nan
+        rows["few left"][:] = np.nan
+        rows["few left"][g.permutation(V)[:k // 2]] = -np.inf
+        rows["few left"][V // 3] = 0.5
+        rows["last alone"][:V - 1] = np.nan
+        rows["an infinity"][at % 7 == 0] = np.nan
+        rows["an infinity"][V - 2] = np.inf
+        say(f"[top nan] V={V} {dt} k={k}")
+        v = torch.from_numpy(np.stack(list(rows.values())).astype(np.float32)).to(dev)
+        x = v.to(torch.bfloat16 if dt == "bf16" else torch.float32)
+        want, _ = ob.token_top(out_to_f64(x, dt).reshape(len(rows), V), k)
+        for many in (1, 9):                        # and too many rows to be cut
+            ids, top, _, h = _top(x.repeat(many, 1), V, dt, None, 1.0, k)
+            for i, name in enumerate(list(rows) * many):
+                assert np.array_equal(ids[i], want[i % len(rows)]), (name, k, ids[i])
+            sound = np.array([n == "none" for n in rows] * many)
+            assert np.isnan(top[~sound]).all() and np.isnan(h.cpu().numpy()[~sound]).all()
+            assert np.all(top[sound] == -np.inf)
+
+
 def test_top_many_rows():
     """More rows than a grid's dimension holds, tiny vocabularies."""
     x, xv = _rows(40000, 9, 9, "bf16", 1, 1)
