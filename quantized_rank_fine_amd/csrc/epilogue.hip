@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kThreads) void ep_bwd_kernel(EpBwdArgs a) {
 #pragma unroll
         for (int e = 0; e < W; ++e) {
           float f = 0.0f, df = 1.0f;
-          if (a.Z) activated<act>(x[e], f, df);
+          if (a.Z) activated<act, BF16>(x[e], f, df);
           h[e] = d[e] * f;
           d[e] = d[e] * df;
           if (a.mul) d[e] *= g[e];

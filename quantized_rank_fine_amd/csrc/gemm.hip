@@ -973,7 +973,7 @@ __device__ __forceinline__ void epilogue_ep(f32x16_t (&acc)[2][8], char *smem, c
             __builtin_nontemporal_store(narrow<kOutBf16>(z), reinterpret_cast<u32x4_t *>(
                                                                  static_cast<char *>(ep.z) + at));
 #pragma unroll
-          for (int e = 0; e < W; ++e) y[e] = activated<act>(z[e]);
+          for (int e = 0; e < W; ++e) y[e] = activated<act, kOutBf16>(z[e]);
           if (ep.mul) {
             widen<kOutBf16>(mu[i], g);
 #pragma unroll

@@ -511,7 +511,7 @@ __device__ __forceinline__ void fwd_small_reduce_block(const SmallReduceArgs &ra
   if constexpr (kEp) {
     const float z = y + bias;
     if (ep.z) store(ep.z, z);
-    with_act(ep.act, [&](auto A) { y = activated<decltype(A)::value>(z); });
+    with_act(ep.act, [&](auto A) { y = activated<decltype(A)::value, kY16>(z); });
     if (ep.mul) y *= mu;
     if (ep.res) y += re;
   }

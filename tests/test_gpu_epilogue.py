@@ -311,6 +311,57 @@ def test_gradient_far_into_memory(M, n):
         assert ((db[c:c + (1 << 19)].double() - want.sum(0)).abs() <= tol).all()
 
 
+def _tail_bounds(z, kind, half):
+    """Bounds of act(z) and act'(z) relative to the size of their terms, U = 2^-24.
+
+    GELU: e^(-z^2/2) or erfc take an argument of up to 1.3 U (constant, product), which
+    moves them by (1 + z^2) 1.3 U, or twice that where z^2 has two roundings; exp2
+    or erfcf, a reciprocal, a polynomial and three products give 16 U at most.  SiLU:
+    1.3 U of v = z moves e^-v by 1.3 |v| U; exp2, addition, reciprocal, product 8 U.
+    GELU_TANH: v = 2 sqrt(2 / pi) (z + 0.044715 z^3) is within 5 U, its product with
+    log2 e 1.3 U more.  The derivatives have two products and a sum more each.  A
+    result's rounding is `half` of it."""
+    if kind == "gelu":
+        rel, phi = (2.6 * z * z + 18) * U, np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        terms = special.ndtr(z) + np.abs(z) * phi
+    else:
+        v = z if kind == "silu" else math.sqrt(8 / math.pi) * (z + 0.044715 * z ** 3)
+        rel = (1.5 * np.abs(v) + 12) * U if kind == "silu" else (6.5 * np.abs(v) + 16) * U
+        slope = 1.0 if kind == "silu" else math.sqrt(8 / math.pi) * (1 + 0.134145 * z * z)
+        terms = special.expit(v) * (1 + np.abs(z) * slope * special.expit(-v))
+    f, df = act(z, kind)
+    return (rel + half) * np.abs(f), rel * terms + half * np.abs(df)
+
+
+@pytest.mark.parametrize("kind,low", [("gelu", -12.5), ("gelu_tanh", -9.5), ("silu", -80.0)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_digits_of_the_tails(kind, low, dt):
+    """act and act' keep the digits of their type where they are small: of the forward
+    z = bias (no input, no adapter), of the gradient dY = mul = 1."""
+    torch, dev = torch_dev()
+    n, half = 1024, 2.0 ** -8 if dt == "bf16" else U
+    t = torch.bfloat16 if dt == "bf16" else torch.float32
+    z = torch.linspace(low, 12.0, n, device=dev).to(t)
+    z[:8] = torch.tensor([-3.0, -4.0, -5.0, -6.2, -8.0, -0.75, 1e-3, -1e-3], device=dev)
+    zv = out_to_f64(z, dt)
+    tol, dtol = _tail_bounds(zv, kind, half)
+    f, df = act(zv, kind)
+    one = torch.ones(1, n, dtype=t, device=dev)
+    dZ, dm, _ = _bwd(z[None], one, one, kind, dt)
+    for name, got, want, bound in (("act", dm, f, tol), ("act'", dZ, df, dtol)):
+        err = np.abs(out_to_f64(got, dt).reshape(-1) - want)
+        bad = np.nonzero(err > bound)[0]
+        assert bad.size == 0, (name, bad.size, zv[bad[:5]], (err / np.abs(want))[bad[:5]])
+    for M in (3, 140):
+        say(f"[ep tails] {kind} {dt} M={M}")
+        c = Case(M, 256, n, 0, dt)
+        c.L.tX.zero_()
+        c.bias = z
+        Y, Z, _ = c.run(kind, True, False, False)
+        assert torch.equal(Z, z.expand(M, n))
+        assert (np.abs(out_to_f64(Y, dt).reshape(M, n) - f) <= tol).all(), (kind, M)
+
+
 def test_no_tokens_gradient():
     torch, dev = torch_dev()
     db = torch.full((128,), 3.0, device=dev)
