@@ -3,7 +3,7 @@
 // (the residual's gradient is dY itself).  One pass, HBM-bound: Z, dY and mul
 // read once, dZ and dmul written once.  A workgroup takes a slab of rows of one
 // run of columns, 16 bytes a lane, four rows in flight; its column sums (fp32
-// over a lane's rows of the slab, fp64 from there on) leave as partials that a
+// over 16 rows of a lane, fp64 from there on) leave as partials that a
 // second launch adds in a fixed order, or as dbias where there is one slab.
 // dZ enters the sums before it is rounded.
 // 2048 x 11008 bf16, SiLU with a factor: 36 us, 6.3 TB/s of 226 MB (a copy
@@ -16,19 +16,28 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRowsAhead = 4;
+constexpr int kTurns = 4;            // of them, summed in fp32
 
 template <bool BF16, int kCols>     // kCols: lanes along a row
 __global__ __launch_bounds__(kThreads) void ep_bwd_kernel(EpBwdArgs a) {
   constexpr int W = kWide<BF16>, kRows = kThreads / kCols;
-  __shared__ float red[kRows][kCols * W + 1];
+  __shared__ double red[kRows][kCols * W + 1];
   const int cl = threadIdx.x % kCols, rl = threadIdx.x / kCols;
   const int64_t col = (int64_t(blockIdx.x) * kCols + cl) * W;
   const int64_t from = int64_t(blockIdx.y) * a.slab;
   const int64_t end = from + a.slab < a.M ? from + a.slab : a.M;
   const bool in = col < a.out;
   float sum[W];
+  double total[W];
 #pragma unroll
-  for (int i = 0; i < W; ++i) sum[i] = 0.0f;
+  for (int i = 0; i < W; ++i) total[i] = sum[i] = 0.0f;
+  auto collect = [&] {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      total[i] += double(sum[i]);
+      sum[i] = 0.0f;
+    }
+  };
   constexpr int es = BF16 ? 2 : 4;
   auto at = [&](const void *p, int64_t r) {
     return reinterpret_cast<const u32x4_t *>(static_cast<const char *>(p) + (r * a.out + col) * es);
@@ -38,6 +47,7 @@ __global__ __launch_bounds__(kThreads) void ep_bwd_kernel(EpBwdArgs a) {
   };
   with_act(a.act, [&](auto A) {
     constexpr int act = decltype(A)::value;
+    int turn = 0;
     for (int64_t r0 = from + rl; r0 < end && in; r0 += kRows * kRowsAhead) {
       u32x4_t z[kRowsAhead], dy[kRowsAhead], mu[kRowsAhead];
 #pragma unroll
@@ -68,17 +78,19 @@ __global__ __launch_bounds__(kThreads) void ep_bwd_kernel(EpBwdArgs a) {
         if (a.dZ) *to(a.dZ, r) = narrow<BF16>(d);
         if (a.dmul) *to(a.dmul, r) = narrow<BF16>(h);
       }
+      if (++turn % kTurns == 0) collect();
     }
   });
   if (!a.dbias) return;
+  collect();
 #pragma unroll
-  for (int e = 0; e < W; ++e) red[rl][cl * W + e] = sum[e];
+  for (int e = 0; e < W; ++e) red[rl][cl * W + e] = total[e];
   __syncthreads();
   for (int c = threadIdx.x; c < kCols * W; c += kThreads) {
     const int64_t n = int64_t(blockIdx.x) * kCols * W + c;
     if (n >= a.out) break;
     double s = 0.0;
-    for (int r = 0; r < kRows; ++r) s += double(red[r][c]);
+    for (int r = 0; r < kRows; ++r) s += red[r][c];
     if (a.partial)
       a.partial[int64_t(blockIdx.y) * a.out + n] = s;
     else

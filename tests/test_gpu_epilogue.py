@@ -362,6 +362,23 @@ def test_digits_of_the_tails(kind, low, dt):
         assert (np.abs(out_to_f64(Y, dt).reshape(M, n) - f) <= tol).all(), (kind, M)
 
 
+@pytest.mark.parametrize("M,n", [(1 << 20, 64), (300001, 64), (100003, 320), (1 << 19, 256)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_bias_gradient_of_many_rows(M, n, dt):
+    """The sums of equal values (a mean's gradient), whose roundings all go one way.
+    A lane adds at most 16 rows in fp32: (1 + ... + 16) / 16 half units < 9 2^-24 of the
+    sum, fp64 from there, one rounding."""
+    torch, dev = torch_dev()
+    t = torch.bfloat16 if dt == "bf16" else torch.float32
+    row = (torch.arange(1, n + 1, device=dev) / (3.0 * M)).to(t)
+    scale = torch.full((n,), 1 / 7, device=dev).to(t)
+    dY, mul = row.expand(M, n).contiguous(), scale.expand(M, n).contiguous()
+    _, _, db = _bwd(None, mul, dY, "none", dt, want_dmul=False)
+    want = M * (row * scale if dt == "f32" else row.float() * scale.float()).double()
+    err = ((db.double() - want).abs() / want).max()
+    assert float(err) <= 10 * U, float(err) / U
+
+
 def test_no_tokens_gradient():
     torch, dev = torch_dev()
     db = torch.full((128,), 3.0, device=dev)
