@@ -23,8 +23,8 @@
 //
 // What bounds them (copy rate 5.1 TB/s, fp64 matrix products 74 TFLOP/s; traced):
 //   64 of 4096 x 64: 173 us, of them Gram 43 (226 MB, 5.2 TB/s), iterations 38
-//     (a chain of 18 products of 64^3 on one CU a matrix, about 23 by the matrix
-//     cores), update 72 (320 MB, 4.4 TB/s).
+//     (18 products of 64^3, 14 of them one after the other, on one CU a matrix:
+//     about 23 by the matrix cores), update 72 (320 MB, 4.4 TB/s).
 //   4 of rank 200 (11008 and 4096): 250 us, of them momentum 15 (6.3 TB/s), Gram
 //     57 (fp64: 19 by the matrix cores), 14 launches of iterations 6.3 each
 //     (latency), update 77 (fp64: 35 by the matrix cores, and Q from L2).
@@ -442,8 +442,9 @@ __global__ __launch_bounds__(256) void gram_sum_kernel(const MuonMat *table, dou
 // an A operand whose matrix is symmetric, as all are here.  So a tile of a
 // result feeds the next products as it is.
 //
-// k <= 16: one tile, one wavefront, no LDS after the partials are summed: 17
-// products of four steps, each waiting for the last.
+// k <= 16: one tile, one wavefront, no LDS after the partials are summed: 18
+// products of four steps for the usual five iterations, 14 of them one after the
+// other (H P and Q P need not wait for each other).
 __device__ __forceinline__ f64x4_t tile_product(const f64x4_t &a, const f64x4_t &b) {
   f64x4_t d = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll

@@ -173,6 +173,31 @@ def test_options(rows, cols, kw):
     run([Mat(rows, cols)], **kw)
 
 
+def _slope(steps):
+    """The peak of s |q'(s^2)|, as scanned above, for more steps."""
+    lam = np.logspace(-14, 0, 200001)
+    p, dp, x, dx = np.ones_like(lam), np.zeros_like(lam), lam.copy(), np.ones_like(lam)
+    a, b, c = q.MUON_COEF
+    for _ in range(steps):
+        s, ds = a + b * x + c * x * x, (b + 2 * c * x) * dx
+        p, dp = p * s, dp * s + p * ds
+        x, dx = x * s * s, dx * s * s + 2 * x * s * ds
+    return (np.sqrt(lam) * np.abs(dp)).max()
+
+
+@pytest.mark.parametrize("steps", [6, 7, 8])
+@pytest.mark.parametrize("rows,cols", [(300, 16), (64, 500), (400, 200), (700, 256)])
+def test_more_steps_of_the_usual_polynomial(rows, cols, steps):
+    """Up to the most that is allowed; the slope is 0.15 a^(2 steps), as the header
+    says, and 10% more than its scan is left for what lies between its points."""
+    slope = _slope(steps)
+    assert 0.14 < slope / q.MUON_COEF[0] ** (2 * steps) < 0.16
+    for kind in ("plain", "strong"):
+        say(f"[muon] {rows}x{cols} {kind} {steps} steps")
+        run([Mat(rows, cols, kind=kind)], steps=steps,
+            tol=1.1 * slope * 4 * min(rows, cols) * 2.0 ** -53)
+
+
 def test_parts_left_out():
     """No momentum, no theta, no copy, no update: each alone."""
     mats = [Mat(90, 12, m=False), Mat(12, 90, theta=False), Mat(90, 100, copy=False),
