@@ -288,7 +288,7 @@ qlora_status qlora_linear_bwd_lora(const qlora_nf4 *wq, const void *X, const voi
  * projection's output it is the gated product of a feed-forward block; with a
  * residual alone, the projection back into the residual stream.  Computed in
  * fp32 from the accumulators on; Y and Z are rounded once each.  Y may be mul
- * or residual itself.
+ * or residual itself (which then are not X).
  *   NONE z, RELU max(z, 0), SILU z sigma(z), GELU z Phi(z),
  *   GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
  * act keeps its digits in the left tail: it is within (3 z^2 + 18) 2^-24 of itself
@@ -452,7 +452,8 @@ qlora_status qlora_adam_step(float *theta, const float *grad, float *m, float *v
  * with a value that is not finite gets NaN throughout.  The shorter side is at
  * most QLORA_MAX_RANK, the longer at most 2^24, and pointers need their
  * element's alignment only (16 bytes, and an inner size that is a multiple of
- * 4, are faster).  A matrix's bits may depend on the other shapes of its call.
+ * 4, are faster; so are calls of their own for matrices of shorter sides above
+ * 64).  A matrix's bits may depend on the other shapes of its call.
  * 0 <= n <= QLORA_MUON_MAX_MATS; mats is a host array, read before the call
  * returns.  momentum >= 0, eps >= 0 and weight_decay >= 0, all values finite,
  * 1 <= steps <= 16 and a^(2 steps) <= 1e9 (QLORA_ERR_VALUE; a = 3.4445 allows

@@ -49,8 +49,9 @@ __device__ __forceinline__ float polynomial(const float (&c)[N], float t) {
 //     itself down to z = -2, 8.2e-7 to -4 (emulated; erfc without any error of its
 //     own, of the rounded argument: 4.6e-8, 3.2e-7, 1.1e-6).
 // They share e with the derivative and take 18 and 27 operations where erfcf takes 60:
-// 2048 x 4096 x 11008 with GELU, fp32: 277 us, with erfcf 289 (bf16: 242); the
-// gradient of 2048 x 11008 fp32: 47.9, with erfcf 54.0.
+// 2048 x 4096 x 11008 with GELU and z saved, fp32: 277 us, with erfcf 289 (with the
+// tanh form 250; bf16 235 and 224); the gradient of 2048 x 11008 fp32: 47.9, with
+// erfcf 54.0.
 template <bool BF16>
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
   const float w = z * z, x = fabsf(z);

@@ -875,8 +875,9 @@ __device__ __forceinline__ void epilogue(f32x16_t (&acc)[2][8], char *smem, cons
 // the segments of mul and res requested before the exchange (one wavefront to
 // a SIMD has the registers, and nothing else hides their latency).
 // 2048 x 4096 x 11008, r = 16, SiLU with a factor, z saved, bf16: the whole call
-// 222-227 us (832 TFLOP/s), the plain forward there 241-243; the elementwise
-// pass that it spares would move 180 MB.
+// 224 us (827 TFLOP/s), the plain forward in turn with it 209 (in fp32 255 and
+// 226); the elementwise pass that it spares would move 180 MB.  Either is up to a
+// quarter slower for the first 50 calls or so of a program.
 template <bool kOutBf16>
 __device__ __forceinline__ void epilogue_ep(f32x16_t (&acc)[2][8], char *smem, const RankOps &ro,
                                             const uint16_t *__restrict__ P16, int ldp,
