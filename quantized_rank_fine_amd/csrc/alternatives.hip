@@ -96,7 +96,9 @@ __device__ __forceinline__ int counted(F &&f, int *sum) {
   return n;
 }
 
-// The largest word of each held group, and of the lane.
+// The largest word of each held group, and of the lane.  A signalling NaN takes the
+// words before it along (a maximum makes it a quiet one, which the next drops): what
+// comes out is a word of the lane or -inf, but perhaps not the largest.
 template <bool BF16, int threads, int NG>
 __device__ __forceinline__ float group_maxima(const Held<BF16, threads, NG> &h,
                                               float (&gm)[8 * NG / kGroup<BF16>]) {
@@ -116,13 +118,15 @@ __device__ __forceinline__ float group_maxima(const Held<BF16, threads, NG> &h,
 
 // Adds a held chunk's best k words (words [from, end) of the groups, and the
 // ones with the first) to the list behind its first `have` entries; end - from
-// is at most the words that are held, gm and top are theirs (group_maxima).
-// Returns the new length (every lane).
+// is at most the words that are held, gm and top are theirs (group_maxima), nan
+// says that there may be a NaN among the lane's: it then looks into every group (a
+// smaller top only lowers the bound).  Returns the new length (every lane).
 template <bool BF16, int threads, int NG>
 __device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF16> &cut,
                                         int32_t from, int32_t end,
-                                        const float (&gm)[8 * NG / kGroup<BF16>], float top, int k,
-                                        int have, TopList &list, uint32_t *keys, int *sum) {
+                                        const float (&gm)[8 * NG / kGroup<BF16>], float top,
+                                        bool nan, int k, int have, TopList &list, uint32_t *keys,
+                                        int *sum) {
   constexpr int W = kGroup<BF16>, G = 8 * NG / W;
   constexpr int share = threads > 128 ? threads / 128 : 1;   // lanes to a key
   const int32_t one = from == 0 ? cut.one(int32_t(threadIdx.x)) : cut.V;
@@ -144,7 +148,7 @@ __device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF
     const uint32_t run = uint32_t(list.e[k - 1] >> 32);      // what is below cannot enter
     bound = run > bound ? run : bound;
   }
-  const float least = value_of(bound);
+  const float least = value_of(bound), skip = nan ? -INFINITY : least;
   // All words reach -inf; of those that are -inf themselves only the first k
   // can be among the best (unless some of them are NaN: fill_masked).
   const bool all = bound == kKeyLeast;
@@ -164,7 +168,7 @@ __device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF
     if (has_one) f(h.one, one);
 #pragma unroll
     for (int g = 0; g < G; ++g, at += threads * W) {
-      if (at >= end || !(gm[g] >= least)) continue;
+      if (at >= end || gm[g] < skip) continue;
       float e[W];
       unpack<BF16>(h.q[g], e);
 #pragma unroll
@@ -204,7 +208,7 @@ __device__ __forceinline__ int add_best(Held<BF16, threads, NG> &h, const Cut<BF
 // than k (n entries): there is a NaN among the first k words.  The next -inf words
 // go to its end, in order.  For one wavefront, or several that do the same; returns
 // the new length.  Only such rows come here; they cost the walk to as many -inf
-// words (4096 x 32000 bf16 of NaN alone, which walk to the end: 149 us, without 45).
+// words (4096 x 32000 bf16 of NaN alone, which walk to the end: 158 us, without 45).
 template <bool BF16>
 __device__ __forceinline__ int fill_masked(TopList &list, const char *row, int32_t V, int n,
                                            int k) {
@@ -323,12 +327,13 @@ __global__ __launch_bounds__(threads, ONE && BF16 ? 8 : 1) void top_kernel(Logit
     float gm[8 * NG / kGroup<BF16>];
     const float top = group_maxima(h, gm);
     add_sums<ENT>(s, h, c, fmaxf(s.m, top));
+    asm volatile("" : "+v"(s.t), "+v"(s.w));   // (w now, not later with all its terms)
     if (ONE) {
       // (the barriers of add_best come before the sums are read)
       s = joined(s, c);
       if (threads > 64 && threadIdx.x % 64 == 0) red[threadIdx.x / 64] = s;
     }
-    n = add_best(h, k, from, end, gm, top, o.k, n, list, keys, sum);
+    n = add_best(h, k, from, end, gm, top, s.t != s.t, o.k, n, list, keys, sum);
     if (ONE) break;
     order<threads>(list, n, o.k);
     n = n < o.k ? n : o.k;
@@ -391,7 +396,8 @@ __global__ __launch_bounds__(kPartThreads) void top_part_kernel(LogitRows a, int
     float gm[8 * kPartNG / kGroup<BF16>];
     const float top = group_maxima(h, gm);
     add_sums<ENT>(s, h, c, top);
-    n = add_best(h, cut, from, end, gm, top, k, 0, list, keys, sum);
+    asm volatile("" : "+v"(s.t), "+v"(s.w));   // (w now, not later with all its terms)
+    n = add_best(h, cut, from, end, gm, top, s.t != s.t, k, 0, list, keys, sum);
     order<kPartThreads>(list, n, k);
   }
   const int64_t at = t * gridDim.x + blockIdx.x;

@@ -200,6 +200,33 @@ def test_top_of_nan_beside_a_mask(V, dt):
             assert np.all(top[sound] == -np.inf)
 
 
+@pytest.mark.parametrize("V", [64, 300, 2049, 8191, 32003, 40007, 131077])
+@pytest.mark.parametrize("dt,bits", [("bf16", 0x7f81), ("bf16", 0xff81), ("bf16", 0xffc0),
+                                     ("f32", 0x7f800001), ("f32", 0xff800001), ("f32", 0xffc00000)])
+def test_top_of_every_kind_of_nan(V, dt, bits):
+    """Signalling and quiet NaN of both signs, few and many of them, beside ordinary
+    words and words at -inf: the other words of their groups are found."""
+    torch, dev = torch_dev()
+    g = np.random.default_rng(V)
+    x = (g.standard_normal((4, V)) * 2).astype(np.float32)
+    x[g.random(x.shape) < 0.3] = -np.inf
+    nan = g.random(x.shape) < np.array([0.0, 0.01, 0.5, 0.98])[:, None]
+    nan[:, g.integers(0, V)] = True
+    u = np.uint16 if dt == "bf16" else np.uint32
+    t = torch.from_numpy(x).to(torch.bfloat16 if dt == "bf16" else torch.float32)
+    xv = np.where(nan, np.nan, t.double().numpy())
+    raw = t.view(torch.int16 if dt == "bf16" else torch.int32).numpy().view(u).copy()
+    raw[nan] = bits
+    xd = torch.from_numpy(raw.view(np.int16 if dt == "bf16" else np.int32)).to(dev).view(t.dtype)
+    for k in (1, 20, 64):
+        say(f"[top nan] V={V} {dt} {bits:#x} k={k}")
+        want, _ = ob.token_top(xv, k)
+        for many in (1, 17):                       # and too many rows to be cut
+            ids, top, _, h = _top(xd.repeat(many, 1), V, dt, None, 1.0, k)
+            assert np.array_equal(ids, np.tile(want, (many, 1)))
+            assert np.isnan(top).all() and np.isnan(h.cpu().numpy()).all()
+
+
 def test_top_many_rows():
     """More rows than a grid's dimension holds, tiny vocabularies."""
     x, xv = _rows(40000, 9, 9, "bf16", 1, 1)
